@@ -277,6 +277,121 @@ typedef struct {
 MUON_API muon_status_t muon_qk_clip(const muon_qk_slice_t* slices, int n, const float* s_max_dev,
                                     int n_heads, float tau, void* stream);
 
+/* ---- the step's inputs: 8-bit activation checkpoints, weight gradients, attention ----
+ * muon_plan_step reads one gradient per matrix and muon_qk_clip the largest attention
+ * logit of every head. The calls below produce both from a training step's own tensors.
+ * They are asynchronous on `stream`, allocate nothing and can be captured into a graph.
+ * Calls that write the same buffers, or share a workspace, must be ordered by the caller.
+ *
+ * status_dev (where present): optional uint32 in device memory that receives
+ * MUON_ERR_TIMEOUT if a bounded wait inside a kernel gives up (the outputs may then hold
+ * garbage). The calls never clear it: zero it before its first use. */
+
+/* One activation X (rows x cols, row-major, F32 or BF16) and its 8-bit checkpoint: int8
+ * values q (rows x cols, ld_q) and one power-of-two scale per row and group of 32
+ * columns, held as a biased exponent byte (rows x ceil(cols/32), ld_e):
+ *   amax = max |x| over the group, E = max(floor(log2 amax) - 6, -126), byte = E + 127
+ *   q = clamp(round_half_even(x 2^-E), -127, 127),      restored value = q 2^E
+ * |x - q 2^E| <= 2^E / 2 (2^E where |x| rounds past 127), 2^E <= amax / 64. A restored
+ * value has 7 significant bits, so BF16 and F32 hold it exactly. A group with a NaN or an
+ * infinity gets byte 255 and restores as NaN throughout. Byte 0 stands for 2^-127; store
+ * never writes it.
+ * q is 16-byte aligned with ld_q a multiple of 16; exps is 4-byte aligned with ld_e a
+ * multiple of 4. rows may be 0. Bytes of q and exps beyond cols are not written. */
+typedef struct {
+  void* X;             /* read by muon_act8_store, written by muon_act8_restore */
+  int8_t* q;
+  uint8_t* exps;
+  int64_t rows, cols, ld_x, ld_q, ld_e;
+  int32_t dtype;       /* muon_dtype_t of X */
+  int32_t reserved;
+} muon_act8_t;
+
+/* Stores / restores n activations, up to 128 per launch. Nothing written may overlap
+ * anything else of the call (MUON_ERR_ALIAS). */
+MUON_API muon_status_t muon_act8_store(const muon_act8_t* items, int n, void* stream);
+MUON_API muon_status_t muon_act8_restore(const muon_act8_t* items, int n, void* stream);
+
+/* Weight gradients from a checkpoint. For each group g of consecutive tokens:
+ *   dW_g[o, i] (+)= sum over t in [offsets[g], offsets[g+1]) of dY[t, o] q[t, i] 2^E[t, i/32]
+ * One group is a dense matrix, several are the experts of a layer, with their tokens
+ * sorted by expert; a group may be empty (dW_g = 0, or left alone with accumulate).
+ * dY (tokens x out) is BF16, 16-byte aligned, ld_dy a multiple of 8. dW is F32 or BF16,
+ * aligned to its element: group g starts stride_w elements after group g - 1, rows are
+ * ld_w apart. Products are exact, sums are FP32, and a BF16 dW (with accumulate: its sum
+ * with the old value) is rounded once. offsets: groups + 1 int32 in device memory (NULL:
+ * one group of all tokens); each is read as clamped to [0, tokens], and a group whose end
+ * lies before its start is empty. Tokens outside every group are not read.
+ * The workspace (256-byte aligned) may be NULL when muon_weight_grad_workspace_size is 0. */
+typedef struct {
+  const void* dY;
+  const int8_t* q;
+  const uint8_t* exps;
+  void* dW;
+  const int32_t* offsets;
+  uint32_t* status_dev;
+  int64_t tokens, out, in;
+  int64_t ld_dy, ld_q, ld_e, ld_w, stride_w;
+  int32_t groups;
+  int32_t w_dtype;     /* muon_dtype_t of dW */
+  int32_t accumulate;  /* 0: dW = sum, 1: dW += sum */
+  int32_t reserved;
+} muon_weight_grad_t;
+
+MUON_API size_t muon_weight_grad_workspace_size(const muon_weight_grad_t* a);
+MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
+/* Softmax attention over packed sequences, with what its backward pass and QK-Clip need.
+ * Sequence s has the query rows [q_offsets[s], q_offsets[s+1]) and the keys
+ * [k_offsets[s], k_offsets[s+1]); query head h reads key head h / (heads / kv_heads).
+ *   S_ij = scale q_i . k_j for the visible keys: all of the sequence, or with causal, of m
+ *          queries and n keys, j <= i + n - m (rows aligned at the end of the keys)
+ *   lse_i = log sum_j exp(S_ij),  o_i = sum_j exp(S_ij - lse_i) v_j
+ *   s_max[h] = max(s_max[h], largest S_ij of head h over all sequences)
+ * A row that sees no key has o = 0 and lse = -inf. s_max is raised, never lowered, so it
+ * collects the maximum over micro-batches: set it to -inf before the first (NaN logits do
+ * not raise it). Rows outside every sequence are neither read nor written.
+ * The backward pass recomputes P = exp(S - lse) and needs the forward pass's o and lse:
+ *   delta_i = o_i . dout_i,  dV = P^T dout,  dS = P (dout V^T - delta)
+ *   dQ = scale dS K,  dK = scale dS^T Q   (dK and dV summed over the heads of a key head)
+ * Keys that no row sees get zero gradients. Sums are taken in a fixed order: the results
+ * of equal calls are equal bit for bit.
+ * Tensors q, o, dout, dq (q_tokens x heads x head_dim) and k, v, dk, dv (k_tokens x
+ * kv_heads x head_dim) are BF16 with unit stride along head_dim, 16-byte aligned, their
+ * token and head strides (in elements) multiples of 8. Views of one buffer (packed q, k,
+ * v) may interleave. lse is heads x q_tokens F32, contiguous. head_dim is a multiple of 8
+ * up to 128; P and dS are rounded to BF16 for the products, all sums are FP32.
+ * Offsets are n_seq + 1 int32 in device memory (NULL: one sequence of all tokens); each is
+ * read as clamped to [0, tokens], and a sequence whose end lies before its start is empty.
+ * Offsets must not decrease. A NaN or infinity of a sequence stays within it. */
+typedef struct {
+  void* ptr;
+  int64_t ld;          /* stride between tokens */
+  int64_t head;        /* stride between heads */
+} muon_heads_t;
+
+typedef struct {
+  muon_heads_t q, k, v, o;
+  muon_heads_t dout, dq, dk, dv;   /* backward only */
+  float* lse;
+  float* s_max;                    /* heads floats or NULL; forward only */
+  const int32_t* q_offsets;
+  const int32_t* k_offsets;
+  uint32_t* status_dev;
+  int64_t q_tokens, k_tokens;
+  int32_t n_seq;
+  int32_t heads, kv_heads, head_dim;
+  int32_t causal;
+  float scale;
+} muon_attention_t;
+
+MUON_API muon_status_t muon_attention_forward(const muon_attention_t* a, void* stream);
+/* The backward pass's scratch: 4 bytes per head and query row, rounded up. */
+MUON_API size_t muon_attention_workspace_size(const muon_attention_t* a);
+MUON_API muon_status_t muon_attention_backward(const muon_attention_t* a, void* workspace,
+                                               size_t ws_bytes, void* stream);
+
 /* Self-test of the device-side timeout path: launches one thread that waits, with
  * the same bounded wait the pipelined kernels use, on an mbarrier nothing arrives
  * at, for limit_cycles SM clock cycles (1 .. 2e9), then records MUON_ERR_TIMEOUT

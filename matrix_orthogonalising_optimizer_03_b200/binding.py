@@ -66,6 +66,33 @@ class MuonNSMatrix(ctypes.Structure):
                 ("ld_x", c_int64), ("ld_o", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
 
 
+class MuonAct8(ctypes.Structure):
+    _fields_ = [("X", c_void_p), ("q", c_void_p), ("exps", c_void_p), ("rows", c_int64),
+                ("cols", c_int64), ("ld_x", c_int64), ("ld_q", c_int64), ("ld_e", c_int64),
+                ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class MuonWeightGrad(ctypes.Structure):
+    _fields_ = [("dY", c_void_p), ("q", c_void_p), ("exps", c_void_p), ("dW", c_void_p),
+                ("offsets", c_void_p), ("status_dev", c_void_p), ("tokens", c_int64),
+                ("out", c_int64), ("in_", c_int64), ("ld_dy", c_int64), ("ld_q", c_int64),
+                ("ld_e", c_int64), ("ld_w", c_int64), ("stride_w", c_int64), ("groups", c_int32),
+                ("w_dtype", c_int32), ("accumulate", c_int32), ("reserved", c_int32)]
+
+
+class MuonHeads(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("ld", c_int64), ("head", c_int64)]
+
+
+class MuonAttention(ctypes.Structure):
+    _fields_ = ([(n, MuonHeads) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")] +
+                [("lse", c_void_p), ("s_max", c_void_p), ("q_offsets", c_void_p),
+                 ("k_offsets", c_void_p), ("status_dev", c_void_p), ("q_tokens", c_int64),
+                 ("k_tokens", c_int64), ("n_seq", c_int32), ("heads", c_int32),
+                 ("kv_heads", c_int32), ("head_dim", c_int32), ("causal", c_int32),
+                 ("scale", c_float)])
+
+
 _lib = None
 
 
@@ -100,6 +127,13 @@ def load(path: str = LIB_PATH):
         "muon_plan_profile_enable": (c_int, [c_void_p, c_int]),
         "muon_wait_probe": (c_int, [c_void_p, c_int64, c_void_p]),
         "muon_qk_clip": (c_int, [P(MuonQkSlice), c_int, c_void_p, c_int, c_float, c_void_p]),
+        "muon_act8_store": (c_int, [P(MuonAct8), c_int, c_void_p]),
+        "muon_act8_restore": (c_int, [P(MuonAct8), c_int, c_void_p]),
+        "muon_weight_grad_workspace_size": (c_size_t, [P(MuonWeightGrad)]),
+        "muon_weight_grad": (c_int, [P(MuonWeightGrad), c_void_p, c_size_t, c_void_p]),
+        "muon_attention_forward": (c_int, [P(MuonAttention), c_void_p]),
+        "muon_attention_workspace_size": (c_size_t, [P(MuonAttention)]),
+        "muon_attention_backward": (c_int, [P(MuonAttention), c_void_p, c_size_t, c_void_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -188,6 +222,12 @@ def _stream_ptr(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+def _on_stream(stream):
+    """Context that makes `stream` current, so that what a call allocates belongs to it."""
+    import contextlib
+    return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _stats_ptr(stats) -> Optional[int]:
@@ -380,6 +420,270 @@ def qk_clip(slices, s_max, tau: float = 100.0, stream=None):
     """QK-Clip, one call. slices: list of (W tensor fp32 2-D CUDA, row0, rows, head, power);
     s_max: CUDA float32 tensor with one entry per head."""
     QkClipPlan(slices, s_max, tau).apply(stream)
+
+
+class Act8:
+    """An 8-bit checkpoint of an activation of `rows` x `cols`: int8 values `q` and one
+    exponent byte per row and group of 32 columns, `exps` (both with padded rows)."""
+
+    def __init__(self, q, exps, cols: int):
+        torch = _torch()
+        if q.dtype != torch.int8 or exps.dtype != torch.uint8:
+            raise MuonError(3, "a checkpoint holds int8 values and uint8 exponents")
+        for t, nm in ((q, "q"), (exps, "exps")):
+            _check_2d(t, nm)
+        if q.device != exps.device:
+            raise MuonError(1, "q and exps must be on the same device")
+        if q.size(0) != exps.size(0) or q.size(1) < cols or exps.size(1) < (cols + 31) // 32:
+            raise MuonError(2, "q and exps are too small for the checkpoint")
+        self.q, self.exps, self.cols = q, exps, int(cols)
+        self.rows, self.device = q.size(0), q.device
+
+    def rows_of(self, lo: int, hi: int) -> "Act8":
+        """The checkpoint of rows [lo, hi) (a view)."""
+        return Act8(self.q[lo:hi], self.exps[lo:hi], self.cols)
+
+    @property
+    def ld(self):
+        """Leading dimensions of q and exps (a single row may carry any stride)."""
+        if self.rows <= 1:
+            return (self.cols + 15) // 16 * 16, ((self.cols + 31) // 32 + 3) // 4 * 4
+        return self.q.stride(0), self.exps.stride(0)
+
+
+def new_act8(rows: int, cols: int, device="cuda") -> Act8:
+    """Buffers for an 8-bit checkpoint of a rows x cols activation (see `act8_store`)."""
+    torch = _torch()
+    return Act8(torch.zeros((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device),
+                torch.ones((rows, ((cols + 31) // 32 + 3) // 4 * 4), dtype=torch.uint8, device=device),
+                cols)
+
+
+def _act8_array(xs, cks):
+    if len(xs) != len(cks):
+        raise MuonError(1, "activations and checkpoints must have the same length")
+    arr = (MuonAct8 * len(xs))()
+    for i, (x, c) in enumerate(zip(xs, cks)):
+        _check_2d(x, "X")
+        if x.device != cks[0].device or c.device != cks[0].device:
+            raise MuonError(1, "activations and checkpoints must be on the same device")
+        if x.size(0) != c.rows or x.size(1) != c.cols:
+            raise MuonError(2, "activation and checkpoint shapes differ")
+        ld_q, ld_e = c.ld
+        arr[i] = MuonAct8(x.data_ptr(), c.q.data_ptr(), c.exps.data_ptr(), c.rows, c.cols,
+                          max(x.stride(0), x.size(1)), ld_q, ld_e, _dtype_code(x), 0)
+    return arr
+
+
+def act8_store(xs, cks, stream=None):
+    """Stores lists of 2-D CUDA activations (fp32 or bf16) in their 8-bit checkpoints."""
+    arr = _act8_array(xs, cks)
+    with _on(_device_of(cks)):
+        _check(load().muon_act8_store(arr, len(arr), _stream_ptr(stream)), "muon_act8_store")
+
+
+def act8_restore(cks, outs, stream=None):
+    """Restores 8-bit checkpoints into 2-D CUDA tensors (fp32 or bf16; both hold them exactly)."""
+    arr = _act8_array(outs, cks)
+    with _on(_device_of(cks)):
+        _check(load().muon_act8_restore(arr, len(arr), _stream_ptr(stream)), "muon_act8_restore")
+
+
+def _offsets_ptr(offsets, device, name: str):
+    if offsets is None:
+        return None
+    if offsets.dtype != _torch().int32 or offsets.dim() != 1 or offsets.numel() < 2 or \
+            not offsets.is_contiguous():
+        raise MuonError(1, f"{name} must be a contiguous 1-D int32 tensor of at least 2 elements")
+    if offsets.device != device:
+        raise MuonError(1, f"{name} must be on the device of the tensors")
+    return offsets.data_ptr()
+
+
+def _status_on(status, device):
+    p = _status_ptr(status)
+    if status is not None and status.device != device:
+        raise MuonError(1, "status must be on the device of the tensors")
+    return p
+
+
+class WeightGradPlan:
+    """dW = dY^T X with X read from its 8-bit checkpoint, over fixed buffers: the arguments
+    are checked and marshalled once, every `apply()` enqueues one gradient.
+
+    dy: tokens x out bf16; ck: checkpoint of the tokens x in activation; dw: out x in, or
+    groups x out x in with `offsets` (int32 CUDA tensor of groups + 1 token offsets, read on
+    the device by every call), fp32 or bf16. accumulate: dW += instead of dW =.
+    The tensors must stay alive while the plan is used; `workspace` (allocated when not
+    given) belongs to this plan alone while calls are in flight."""
+
+    def __init__(self, dy, ck: Act8, dw, offsets=None, accumulate: bool = False, workspace=None,
+                 status=None):
+        torch = _torch()
+        self._lib = load()
+        _check_2d(dy, "dY")
+        if dy.dtype != torch.bfloat16:
+            raise MuonError(3, "dY must be bfloat16")
+        if dw.dim() == 2:
+            dw3 = dw.unsqueeze(0)
+        elif dw.dim() == 3 and offsets is not None:
+            dw3 = dw
+        else:
+            raise MuonError(2, "dW must be out x in, or groups x out x in with offsets")
+        if not dw.is_cuda or dy.device != dw.device or ck.device != dw.device:
+            raise MuonError(1, "dY, the checkpoint and dW must be CUDA tensors on the same device")
+        groups, out, inn = dw3.shape
+        if groups < 1 or (offsets is not None and offsets.numel() != groups + 1):
+            raise MuonError(2, "offsets must have groups + 1 elements")
+        if dy.size(0) != ck.rows or dy.size(1) != out or ck.cols != inn:
+            raise MuonError(2, "dY, checkpoint and dW shapes do not match")
+        if inn > 1 and dw3.stride(2) != 1:
+            raise MuonError(2, "dW must have unit column stride")
+        ld_q, ld_e = ck.ld
+        ld_w = dw3.stride(1) if out > 1 else inn
+        self._a = MuonWeightGrad(
+            dy.data_ptr(), ck.q.data_ptr(), ck.exps.data_ptr(), dw.data_ptr(),
+            _offsets_ptr(offsets, dw.device, "offsets"), _status_on(status, dw.device), ck.rows,
+            out, inn, dy.stride(0) if dy.size(0) > 1 else (out + 7) // 8 * 8, ld_q, ld_e, ld_w,
+            dw3.stride(0) if groups > 1 else 0, groups, _dtype_code(dw), int(bool(accumulate)), 0)
+        self._keep = (dy, ck, dw, offsets, status)
+        self.device = dw.device
+        with _on(self.device):
+            size = int(self._lib.muon_weight_grad_workspace_size(ctypes.byref(self._a)))
+        self.workspace = workspace
+        if workspace is None and size:
+            self.workspace = new_workspace(size, self.device)
+
+    def apply(self, stream=None):
+        ws = self.workspace
+        with _on(self.device):
+            _check(self._lib.muon_weight_grad(ctypes.byref(self._a), ws.data_ptr() if ws is not None else None,
+                                              ws.numel() if ws is not None else 0, _stream_ptr(stream)),
+                   "muon_weight_grad")
+
+
+def weight_grad(dy, ck: Act8, dw, offsets=None, accumulate: bool = False, workspace=None,
+                status=None, stream=None):
+    """One weight gradient (see `WeightGradPlan`). Returns the workspace used (or None)."""
+    with _on_stream(stream):
+        plan = WeightGradPlan(dy, ck, dw, offsets, accumulate, workspace, status)
+        plan.apply()
+    return plan.workspace
+
+
+def _heads(t, name: str, tokens: int, heads: int, dim: int, device) -> MuonHeads:
+    if t.dtype != _torch().bfloat16:
+        raise MuonError(3, f"{name} must be bfloat16")
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise MuonError(2, f"{name} must be {tokens} x {heads} x {dim} (got {tuple(t.shape)})")
+    if not t.is_cuda or t.device != device:
+        raise MuonError(1, f"{name} must be a CUDA tensor on the device of q")
+    if dim > 1 and t.stride(2) != 1:
+        raise MuonError(2, f"{name} must have unit stride along head_dim")
+    return MuonHeads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+class AttentionPlan:
+    """Softmax attention of packed sequences over fixed buffers (muon_attention_*): the
+    arguments are checked and marshalled once; `forward()` writes o and lse and raises s_max,
+    `backward()` writes the gradients.
+
+    q, o: q_tokens x heads x head_dim; k, v: k_tokens x kv_heads x head_dim (bf16); lse:
+    heads x q_tokens fp32. q_offsets / k_offsets: int32 CUDA tensors of n_seq + 1 token
+    offsets, read on the device by every call (None: one sequence; for self-attention pass
+    the same tensor twice). s_max: fp32 tensor of `heads` entries, the S_max of QK-Clip, to be
+    filled with -inf before the first micro-batch. scale: 1 / sqrt(head_dim) by default.
+    grads: (dout, dq, dk, dv), needed by backward(). The tensors must stay alive while the
+    plan is used."""
+
+    def __init__(self, q, k, v, o, lse, q_offsets=None, k_offsets=None, causal: bool = True,
+                 scale: Optional[float] = None, s_max=None, grads=None, workspace=None, status=None):
+        torch = _torch()
+        self._lib = load()
+        if q.dim() != 3 or k.dim() != 3:
+            raise MuonError(2, "q and k must be tokens x heads x head_dim")
+        dev, (qt, h, d), (kt, g, _) = q.device, q.shape, k.shape
+        a = MuonAttention()
+        for n, t in (("q", q), ("o", o)):
+            setattr(a, n, _heads(t, n, qt, h, d, dev))
+        for n, t in (("k", k), ("v", v)):
+            setattr(a, n, _heads(t, n, kt, g, d, dev))
+        if grads is not None:
+            dout, dq, dk, dv = grads
+            for n, t in (("dout", dout), ("dq", dq)):
+                setattr(a, n, _heads(t, n, qt, h, d, dev))
+            for n, t in (("dk", dk), ("dv", dv)):
+                setattr(a, n, _heads(t, n, kt, g, d, dev))
+        if lse.dtype != torch.float32 or tuple(lse.shape) != (h, qt) or not lse.is_contiguous() or \
+                lse.device != dev:
+            raise MuonError(2, f"lse must be a contiguous fp32 tensor of {h} x {qt} on the device of q")
+        if s_max is not None and (s_max.dtype != torch.float32 or tuple(s_max.shape) != (h,) or
+                                  not s_max.is_contiguous() or s_max.device != dev):
+            raise MuonError(2, f"s_max must be a contiguous fp32 tensor of {h} on the device of q")
+        if (q_offsets is None) != (k_offsets is None):
+            raise MuonError(1, "q_offsets and k_offsets are given together")
+        if q_offsets is not None and q_offsets.numel() != k_offsets.numel():
+            raise MuonError(2, "q_offsets and k_offsets must have the same length")
+        a.lse, a.s_max = lse.data_ptr(), s_max.data_ptr() if s_max is not None else None
+        a.q_offsets = _offsets_ptr(q_offsets, dev, "q_offsets")
+        a.k_offsets = _offsets_ptr(k_offsets, dev, "k_offsets")
+        a.status_dev = _status_on(status, dev)
+        a.q_tokens, a.k_tokens = qt, kt
+        a.n_seq = 1 if q_offsets is None else q_offsets.numel() - 1
+        a.heads, a.kv_heads, a.head_dim, a.causal = h, g, d, int(bool(causal))
+        a.scale = d ** -0.5 if scale is None else scale
+        self._a, self.device, self._has_grads = a, dev, grads is not None
+        self._keep = (q, k, v, o, lse, q_offsets, k_offsets, s_max, grads, status)
+        self.workspace = workspace
+        if grads is not None and workspace is None:
+            with _on(dev):
+                size = int(self._lib.muon_attention_workspace_size(ctypes.byref(a)))
+            if size:
+                self.workspace = new_workspace(size, dev)
+
+    def forward(self, stream=None):
+        with _on(self.device):
+            _check(self._lib.muon_attention_forward(ctypes.byref(self._a), _stream_ptr(stream)),
+                   "muon_attention_forward")
+
+    def backward(self, stream=None):
+        if not self._has_grads:
+            raise MuonError(1, "backward needs grads=(dout, dq, dk, dv)")
+        ws = self.workspace
+        with _on(self.device):
+            _check(self._lib.muon_attention_backward(ctypes.byref(self._a),
+                                                     ws.data_ptr() if ws is not None else None,
+                                                     ws.numel() if ws is not None else 0,
+                                                     _stream_ptr(stream)), "muon_attention_backward")
+
+
+def attention_forward(q, k, v, o=None, lse=None, q_offsets=None, k_offsets=None, causal: bool = True,
+                      scale: Optional[float] = None, s_max=None, status=None, stream=None):
+    """One forward pass (see `AttentionPlan`). Returns (o, lse); tensors that are not given
+    are allocated, with rows outside every sequence zero and -inf."""
+    torch = _torch()
+    with _on(q.device if q.is_cuda else None), _on_stream(stream):
+        if o is None:
+            o = torch.zeros_like(q, memory_format=torch.contiguous_format)
+        if lse is None:
+            lse = torch.full((q.size(1), q.size(0)), float("-inf"), dtype=torch.float32, device=q.device)
+        AttentionPlan(q, k, v, o, lse, q_offsets, k_offsets, causal, scale, s_max,
+                      status=status).forward()
+    return o, lse
+
+
+def attention_backward(dout, q, k, v, o, lse, dq=None, dk=None, dv=None, q_offsets=None,
+                       k_offsets=None, causal: bool = True, scale: Optional[float] = None,
+                       workspace=None, status=None, stream=None):
+    """One backward pass (see `AttentionPlan`). Returns (dq, dk, dv); tensors that are not
+    given are allocated, with rows outside every sequence zero."""
+    torch = _torch()
+    with _on(q.device if q.is_cuda else None), _on_stream(stream):
+        dq, dk, dv = (torch.zeros_like(t, memory_format=torch.contiguous_format) if g is None else g
+                      for g, t in ((dq, q), (dk, k), (dv, v)))
+        AttentionPlan(q, k, v, o, lse, q_offsets, k_offsets, causal, scale, grads=(dout, dq, dk, dv),
+                      workspace=workspace, status=status).backward()
+    return dq, dk, dv
 
 
 class StreamedSteps:

@@ -1,0 +1,265 @@
+// Softmax attention of packed sequences and its backward pass (muon_attention_t): host
+// checks and, for now, simple kernels: one warp per query row and head (o, lse, dQ) or per
+// key and key head (dK, dV), in fp32 on the CUDA cores.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attention.h"
+#include "muon.h"
+#include "ptx.cuh"
+#include "validate.h"
+
+namespace muon {
+namespace {
+
+__device__ __forceinline__ float warp_max(float v) {
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+// Raises *p to v; the bit patterns of positive floats order as integers, of negative ones
+// in reverse as unsigned integers. The maximum does not depend on the order of the calls.
+__device__ __forceinline__ void atomic_max_float(float* p, float v) {
+  if (v >= 0.f) atomicMax(reinterpret_cast<int*>(p), __float_as_int(v));
+  else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
+}
+
+// The sequence of a row, or -1.
+__device__ int row_seq(const int32_t* off, int n_seq, int32_t tokens, int row) {
+  if (off == nullptr) return 0;
+  for (int s = 0; s < n_seq; ++s)
+    if (row >= clamp_offset(off, s, tokens) && row < clamp_offset(off, s + 1, tokens)) return s;
+  return -1;
+}
+
+__device__ __forceinline__ const uint16_t* at(const muon_heads_t& h, int64_t t, int head) {
+  return static_cast<const uint16_t*>(h.ptr) + t * h.ld + head * h.head;
+}
+__device__ __forceinline__ uint16_t* at_w(const muon_heads_t& h, int64_t t, int head) {
+  return static_cast<uint16_t*>(h.ptr) + t * h.ld + head * h.head;
+}
+
+__device__ __forceinline__ void load_row(const uint16_t* p, int d, int lane, float (&x)[4]) {
+  for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < d ? bf16_to_f32(p[lane + 32 * i]) : 0.f;
+}
+__device__ __forceinline__ float dot(const float (&x)[4], const float (&y)[4]) {
+  return warp_sum(x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3]);
+}
+
+__global__ void attention_simple_kernel(const __grid_constant__ muon_attention_t a) {
+  const int lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
+  if (i >= a.q_tokens) return;
+  const int s = row_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), i);
+  if (s < 0) return;
+  const SeqRange r = seq_range(a, s);
+  const int kh = h / (a.heads / a.kv_heads);
+  const int vis = a.causal ? min(r.n, i - r.q0 + r.n - r.m + 1) : r.n;
+  float q[4], acc[4] = {}, m = -INFINITY, l = 0.f;
+  load_row(at(a.q, i, h), a.head_dim, lane, q);
+  for (int j = 0; j < vis; ++j) {
+    float k[4], v[4];
+    load_row(at(a.k, r.k0 + j, kh), a.head_dim, lane, k);
+    load_row(at(a.v, r.k0 + j, kh), a.head_dim, lane, v);
+    const float x = dot(q, k) * a.scale, mn = fmaxf(m, x);
+    const float c = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
+    l = l * c + p;
+    for (int e = 0; e < 4; ++e) acc[e] = acc[e] * c + p * v[e];
+    m = mn;
+  }
+  for (int e = 0; e < 4; ++e)
+    if (lane + 32 * e < a.head_dim) at_w(a.o, i, h)[lane + 32 * e] = f32_to_bf16(vis > 0 ? acc[e] / l : 0.f);
+  if (lane == 0) {
+    a.lse[h * a.q_tokens + i] = vis > 0 ? m + logf(l) : -INFINITY;
+    if (a.s_max != nullptr && vis > 0) atomic_max_float(a.s_max + h, m);
+  }
+}
+
+__global__ void attention_dq_simple_kernel(const __grid_constant__ muon_attention_t a, float* delta) {
+  const int lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
+  if (i >= a.q_tokens) return;
+  const int s = row_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), i);
+  if (s < 0) return;
+  const SeqRange r = seq_range(a, s);
+  const int kh = h / (a.heads / a.kv_heads);
+  const int vis = a.causal ? min(r.n, i - r.q0 + r.n - r.m + 1) : r.n;
+  float q[4], o[4], d[4], acc[4] = {};
+  load_row(at(a.q, i, h), a.head_dim, lane, q);
+  load_row(at(a.o, i, h), a.head_dim, lane, o);
+  load_row(at(a.dout, i, h), a.head_dim, lane, d);
+  const float dl = dot(o, d), lse = a.lse[h * a.q_tokens + i];
+  if (lane == 0) delta[h * a.q_tokens + i] = dl;
+  for (int j = 0; j < vis; ++j) {
+    float k[4], v[4];
+    load_row(at(a.k, r.k0 + j, kh), a.head_dim, lane, k);
+    load_row(at(a.v, r.k0 + j, kh), a.head_dim, lane, v);
+    const float p = expf(dot(q, k) * a.scale - lse), ds = p * (dot(d, v) - dl) * a.scale;
+    for (int e = 0; e < 4; ++e) acc[e] += ds * k[e];
+  }
+  for (int e = 0; e < 4; ++e)
+    if (lane + 32 * e < a.head_dim) at_w(a.dq, i, h)[lane + 32 * e] = f32_to_bf16(acc[e]);
+}
+
+__global__ void attention_dkv_simple_kernel(const __grid_constant__ muon_attention_t a, const float* delta) {
+  const int lane = threadIdx.x & 31, kt = blockIdx.x * 4 + (threadIdx.x >> 5), kh = blockIdx.y;
+  if (kt >= a.k_tokens) return;
+  const int s = row_seq(a.k_offsets, a.n_seq, static_cast<int>(a.k_tokens), kt);
+  if (s < 0) return;
+  const SeqRange r = seq_range(a, s);
+  const int j = kt - r.k0, per = a.heads / a.kv_heads;
+  const int first = a.causal ? max(0, j - (r.n - r.m)) : 0;  // the first row that sees key j
+  float k[4], v[4], ak[4] = {}, av[4] = {};
+  load_row(at(a.k, kt, kh), a.head_dim, lane, k);
+  load_row(at(a.v, kt, kh), a.head_dim, lane, v);
+  for (int h = kh * per; h < (kh + 1) * per; ++h)
+    for (int i = r.q0 + first; i < r.q0 + r.m; ++i) {
+      float q[4], d[4];
+      load_row(at(a.q, i, h), a.head_dim, lane, q);
+      load_row(at(a.dout, i, h), a.head_dim, lane, d);
+      const float p = expf(dot(q, k) * a.scale - a.lse[h * a.q_tokens + i]);
+      const float ds = p * (dot(d, v) - delta[h * a.q_tokens + i]) * a.scale;
+      for (int e = 0; e < 4; ++e) {
+        av[e] += p * d[e];
+        ak[e] += ds * q[e];
+      }
+    }
+  for (int e = 0; e < 4; ++e)
+    if (lane + 32 * e < a.head_dim) {
+      at_w(a.dk, kt, kh)[lane + 32 * e] = f32_to_bf16(ak[e]);
+      at_w(a.dv, kt, kh)[lane + 32 * e] = f32_to_bf16(av[e]);
+    }
+}
+
+// ------------------------------------------------------------------ host checks
+// A BF16 tensor tokens x heads x head_dim as the checks see it (strides of axes of one
+// element do not matter and are set to the smallest legal ones).
+struct Span {
+  const void* ptr;
+  int64_t tokens, heads, dim, ld, head;
+};
+
+Span span_of(const muon_heads_t& t, int64_t tokens, int64_t heads, int64_t dim) {
+  Span s{t.ptr, tokens, heads, dim, t.ld, t.head};
+  if (heads == 1) s.head = dim;
+  if (tokens <= 1) s.ld = heads * (s.head > dim ? s.head : dim);
+  return s;
+}
+
+// Rows of one token side by side inside the token stride, or the tokens of one head side by
+// side inside the head stride: no element has two addresses.
+bool nested(const Span& s) {
+  return (s.head >= s.dim && s.ld >= (s.heads - 1) * s.head + s.dim) ||
+         (s.ld >= s.dim && s.head >= (s.tokens - 1) * s.ld + s.dim);
+}
+
+size_t extent(const Span& s) {
+  return s.tokens < 1 ? 0 : static_cast<size_t>((s.tokens - 1) * s.ld + (s.heads - 1) * s.head + s.dim) * 2;
+}
+
+// Whether two tensors may share an address. Interleaved views of one buffer do not: with
+// the same outer stride, the spans of one outer index lie side by side inside it.
+bool may_overlap(const Span& x, const Span& y) {
+  if (!ranges_overlap(x.ptr, extent(x), y.ptr, extent(y))) return false;
+  const int64_t d0 = (reinterpret_cast<intptr_t>(y.ptr) - reinterpret_cast<intptr_t>(x.ptr)) / 2;
+  auto beside = [&](int64_t outer_x, int64_t outer_y, int64_t inner_x, int64_t inner_y) {
+    if (outer_x != outer_y) return false;
+    const int64_t d = ((d0 % outer_x) + outer_x) % outer_x;
+    return d >= inner_x && d + inner_y <= outer_x;
+  };
+  if (beside(x.ld, y.ld, (x.heads - 1) * x.head + x.dim, (y.heads - 1) * y.head + y.dim)) return false;
+  if (beside(x.head, y.head, (x.tokens - 1) * x.ld + x.dim, (y.tokens - 1) * y.ld + y.dim)) return false;
+  return true;
+}
+
+}  // namespace
+
+muon_status_t validate_attention(const muon_attention_t* p, bool backward) {
+  if (p == nullptr) return MUON_ERR_INVALID_ARG;
+  const muon_attention_t& a = *p;
+  const int64_t lim = int64_t(1) << 31;
+  if (a.q_tokens < 0 || a.k_tokens < 0 || a.q_tokens > lim - 65536 || a.k_tokens > lim - 65536 ||
+      a.n_seq < 1 || a.n_seq > (1 << 20) || a.heads < 1 || a.kv_heads < 1 || a.heads > 65535 ||
+      a.heads % a.kv_heads != 0 || a.head_dim < 8 || a.head_dim > 128 || a.head_dim % 8 != 0)
+    return MUON_ERR_SHAPE;
+  if ((a.causal != 0 && a.causal != 1) || !std::isfinite(a.scale) || !(a.scale > 0.f))
+    return MUON_ERR_INVALID_ARG;
+  if (a.n_seq > 1 && (a.q_offsets == nullptr || a.k_offsets == nullptr)) return MUON_ERR_INVALID_ARG;
+  // tensors: the first n_ptr are used; which of them are written
+  const muon_heads_t* t[8] = {&a.q, &a.k, &a.v, &a.o, &a.dout, &a.dq, &a.dk, &a.dv};
+  const bool on_keys[8] = {false, true, true, false, false, false, true, true};
+  const bool written[8] = {false, false, false, !backward, false, true, true, true};
+  const int nt = backward ? 8 : 4;
+  Span s[8];
+  for (int i = 0; i < nt; ++i) {
+    const int64_t tokens = on_keys[i] ? a.k_tokens : a.q_tokens;
+    s[i] = span_of(*t[i], tokens, on_keys[i] ? a.kv_heads : a.heads, a.head_dim);
+    if (tokens == 0) continue;
+    if (t[i]->ptr == nullptr || reinterpret_cast<uintptr_t>(t[i]->ptr) % 16) return MUON_ERR_INVALID_ARG;
+    if (s[i].ld < 1 || s[i].head < 1 || s[i].ld >= (int64_t(1) << 38) || s[i].head >= (int64_t(1) << 38) ||
+        s[i].ld % 8 || s[i].head % 8 || s[i].ld > (int64_t(1) << 44) / tokens || !nested(s[i]))
+      return MUON_ERR_SHAPE;
+  }
+  struct Flat {
+    const void* p;
+    size_t n;
+    bool w;
+  };
+  const size_t off_bytes = (static_cast<size_t>(a.n_seq) + 1) * 4;
+  const Flat f[5] = {
+      {a.lse, a.q_tokens > 0 ? static_cast<size_t>(a.heads) * a.q_tokens * 4 : 0, !backward},
+      {a.s_max, a.s_max != nullptr && !backward ? static_cast<size_t>(a.heads) * 4 : 0, true},
+      {a.q_offsets, a.q_offsets != nullptr ? off_bytes : 0, false},
+      {a.k_offsets, a.k_offsets != nullptr ? off_bytes : 0, false},
+      {a.status_dev, a.status_dev != nullptr ? size_t(4) : 0, true}};
+  if (a.q_tokens > 0 && a.lse == nullptr) return MUON_ERR_INVALID_ARG;
+  for (int i = 0; i < 5; ++i)
+    if (reinterpret_cast<uintptr_t>(f[i].p) % 4) return MUON_ERR_INVALID_ARG;
+  for (int i = 0; i < nt; ++i) {
+    for (int j = 0; j < nt; ++j)
+      if (i != j && written[i] && may_overlap(s[i], s[j])) return MUON_ERR_ALIAS;
+    for (int j = 0; j < 5; ++j)
+      if ((written[i] || f[j].w) && ranges_overlap(s[i].ptr, extent(s[i]), f[j].p, f[j].n)) return MUON_ERR_ALIAS;
+  }
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if ((f[i].w || f[j].w) && ranges_overlap(f[i].p, f[i].n, f[j].p, f[j].n)) return MUON_ERR_ALIAS;
+  return MUON_OK;
+}
+
+}  // namespace muon
+
+extern "C" MUON_API muon_status_t muon_attention_forward(const muon_attention_t* a, void* stream) {
+  using namespace muon;
+  const muon_status_t v = validate_attention(a, false);
+  if (v != MUON_OK || a->q_tokens == 0) return v;
+  int dev = 0, sms = 0;
+  const muon_status_t d = current_device(&dev, &sms);
+  if (d != MUON_OK) return d;
+  attention_simple_kernel<<<dim3((a->q_tokens + 3) / 4, a->heads), 128, 0, static_cast<cudaStream_t>(stream)>>>(*a);
+  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+extern "C" MUON_API size_t muon_attention_workspace_size(const muon_attention_t* a) {
+  if (muon::validate_attention(a, true) != MUON_OK) return 0;
+  return (static_cast<size_t>(a->heads) * a->q_tokens * 4 + 255) / 256 * 256;
+}
+
+extern "C" MUON_API muon_status_t muon_attention_backward(const muon_attention_t* a, void* workspace,
+                                                          size_t ws_bytes, void* stream) {
+  using namespace muon;
+  const muon_status_t v = validate_attention(a, true);
+  if (v != MUON_OK) return v;
+  const size_t need = muon_attention_workspace_size(a);
+  if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need))
+    return MUON_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  const muon_status_t d = current_device(&dev, &sms);
+  if (d != MUON_OK) return d;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* delta = static_cast<float*>(workspace);
+  if (a->q_tokens > 0)
+    attention_dq_simple_kernel<<<dim3((a->q_tokens + 3) / 4, a->heads), 128, 0, st>>>(*a, delta);
+  if (a->k_tokens > 0)
+    attention_dkv_simple_kernel<<<dim3((a->k_tokens + 3) / 4, a->kv_heads), 128, 0, st>>>(*a, delta);
+  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}

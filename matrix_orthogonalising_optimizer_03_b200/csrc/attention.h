@@ -1,0 +1,64 @@
+// Host validation and device helpers shared by the forward and the backward pass.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "muon.h"
+
+namespace muon {
+
+// Host checks of an attention call (no CUDA call); backward: the gradients' tensors too.
+muon_status_t validate_attention(const muon_attention_t* a, bool backward);
+
+// One sequence's rows and keys, clamped to the tensors.
+struct SeqRange {
+  int32_t q0, m;  // first query row, queries
+  int32_t k0, n;  // first key, keys
+};
+
+__device__ __forceinline__ int32_t clamp_offset(const int32_t* off, int i, int32_t tokens) {
+  const int32_t v = __ldg(off + i);
+  return v < 0 ? 0 : v > tokens ? tokens : v;
+}
+
+__device__ __forceinline__ SeqRange seq_range(const muon_attention_t& a, int s) {
+  const int32_t qt = static_cast<int32_t>(a.q_tokens), kt = static_cast<int32_t>(a.k_tokens);
+  SeqRange r{0, qt, 0, kt};
+  if (a.q_offsets != nullptr) {
+    r.q0 = clamp_offset(a.q_offsets, s, qt);
+    r.m = clamp_offset(a.q_offsets, s + 1, qt) - r.q0;
+  }
+  if (a.k_offsets != nullptr) {
+    r.k0 = clamp_offset(a.k_offsets, s, kt);
+    r.n = clamp_offset(a.k_offsets, s + 1, kt) - r.k0;
+  }
+  if (r.m < 0) r.m = 0;
+  if (r.n < 0) r.n = 0;
+  return r;
+}
+
+// Tiles of `rows` rows over packed sequences: sequence s owns the tile slots from
+// off[s] / rows + s on, which is enough for its ceil(len / rows) tiles
+// (floor(e / rows) - floor(b / rows) + 1 >= ceil((e - b) / rows)), so a block finds its
+// sequence by bisection over the offsets, without a prefix sum or a table.
+// Returns the sequence of slot t and the first row of the tile within it.
+__device__ __forceinline__ int tile_seq(const int32_t* off, int n_seq, int32_t tokens, int rows,
+                                        int t, int* row) {
+  if (off == nullptr) {
+    *row = t * rows;
+    return 0;
+  }
+  int lo = 0, hi = n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (clamp_offset(off, mid, tokens) / rows + mid <= t) lo = mid; else hi = mid - 1;
+  }
+  *row = (t - (clamp_offset(off, lo, tokens) / rows + lo)) * rows;
+  return lo;
+}
+
+inline int64_t tile_slots(const int32_t* off, int n_seq, int64_t tokens, int rows) {
+  return off == nullptr ? (tokens + rows - 1) / rows : tokens / rows + n_seq;
+}
+
+}  // namespace muon

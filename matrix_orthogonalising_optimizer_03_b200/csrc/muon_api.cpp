@@ -405,6 +405,10 @@ muon_plan_s* make_ns_plan(const muon_ns_matrix_t* mats, int n, const muon_hparam
 // low bits: SM count) so that a thread reads either nothing or the whole record.
 std::atomic<uint32_t> g_dev_info[kMaxDevices];
 
+}  // namespace
+
+namespace muon {
+
 muon_status_t current_device(int* dev, int* num_sms) {
   if (cudaGetDevice(dev) != cudaSuccess) return MUON_ERR_CUDA;
   if (*dev < 0 || *dev >= kMaxDevices) return MUON_ERR_UNSUPPORTED;
@@ -423,6 +427,10 @@ muon_status_t current_device(int* dev, int* num_sms) {
   *num_sms = static_cast<int>(info & 0xFFFFu);
   return MUON_OK;
 }
+
+}  // namespace muon
+
+namespace {
 
 // Binds the plan to a workspace: absolute slab pointers, tensor maps, and the
 // device copy of the descriptor tables.

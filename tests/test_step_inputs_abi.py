@@ -1,0 +1,172 @@
+"""Host checks of the calls that make a step's inputs: bad arguments are refused before any
+CUDA call, and good ones pass every check up to the device query."""
+import ctypes
+
+import pytest
+
+from matrix_orthogonalising_optimizer_03_b200 import binding as B
+from matrix_orthogonalising_optimizer_03_b200 import build as build_mod
+
+FAKE = 1 << 40
+GB = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return B.load()
+
+
+def act8(**kw):
+    a = dict(X=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, rows=100, cols=70, ld_x=70, ld_q=80, ld_e=4, dtype=1,
+             reserved=0)
+    a.update(kw)
+    return B.MuonAct8(**a)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), 3), (dict(rows=-1), 2), (dict(cols=0), 2), (dict(cols=(1 << 26) + 1, ld_x=1 << 27, ld_q=1 << 27), 2),
+    (dict(ld_x=69), 2), (dict(ld_q=64), 2), (dict(ld_q=72), 2), (dict(ld_e=3), 2), (dict(ld_e=6), 2),
+    (dict(X=None), 1), (dict(q=None), 1), (dict(exps=None), 1), (dict(X=FAKE + 1), 1), (dict(q=FAKE + GB + 8), 1),
+    (dict(exps=FAKE + 2 * GB + 1), 1), (dict(dtype=0, X=FAKE + 2), 1), (dict(q=FAKE + 64), 4),
+    (dict(exps=FAKE + 64), 4), (dict(rows=1 << 41), 2), (dict(rows=1 << 39, ld_x=1 << 30), 2)])
+def test_act8_refusals(lib, kw, status):
+    for f in (lib.muon_act8_store, lib.muon_act8_restore):
+        arr = (B.MuonAct8 * 2)(act8(X=FAKE + 8 * GB, q=FAKE + 9 * GB, exps=FAKE + 10 * GB), act8(**kw))
+        assert f(arr, 2, None) == status
+    assert lib.muon_act8_store(None, 1, None) == 1 and lib.muon_act8_store(None, -1, None) == 1
+    assert lib.muon_act8_store(None, 0, None) == 0 and lib.muon_act8_restore(None, 0, None) == 0
+
+
+def test_act8_aliases_between_items(lib):
+    two = (B.MuonAct8 * 2)(act8(), act8(X=FAKE + 8 * GB, exps=FAKE + 10 * GB))       # one q for both
+    assert lib.muon_act8_store(two, 2, None) == 4
+    shared = (B.MuonAct8 * 2)(act8(), act8(q=FAKE + 9 * GB, exps=FAKE + 10 * GB))    # one X for both
+    assert lib.muon_act8_restore(shared, 2, None) == 4
+
+
+def wgrad(**kw):
+    a = dict(dY=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, dW=FAKE + 3 * GB, offsets=FAKE + 4 * GB, status_dev=None,
+             tokens=100, out=50, in_=70, ld_dy=56, ld_q=80, ld_e=4, ld_w=70, stride_w=3500, groups=3, w_dtype=1,
+             accumulate=0, reserved=0)
+    a.update(kw)
+    return B.MuonWeightGrad(**a)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(w_dtype=4), 3), (dict(tokens=-1), 2), (dict(out=0), 2), (dict(in_=0), 2), (dict(groups=0), 2),
+    (dict(ld_dy=50), 2), (dict(ld_dy=48), 2), (dict(ld_q=64), 2), (dict(ld_q=72), 2), (dict(ld_e=2), 2),
+    (dict(ld_w=69), 2), (dict(stride_w=3499), 2), (dict(accumulate=2), 1), (dict(dW=None), 1), (dict(offsets=None), 1),
+    (dict(dY=None), 1), (dict(q=None), 1), (dict(exps=None), 1), (dict(dY=FAKE + 8), 1), (dict(q=FAKE + GB + 4), 1),
+    (dict(exps=FAKE + 2 * GB + 2), 1), (dict(dW=FAKE + 3 * GB + 1), 1), (dict(offsets=FAKE + 4 * GB + 2), 1),
+    (dict(status_dev=FAKE + 2), 1), (dict(dW=FAKE + 64), 4), (dict(dW=FAKE + GB + 64), 4),
+    (dict(dW=FAKE + 2 * GB + 64), 4), (dict(dW=FAKE + 4 * GB), 4), (dict(status_dev=FAKE + 3 * GB + 400), 4),
+    (dict(tokens=1 << 31), 2), (dict(out=1 << 20, in_=1 << 20, ld_w=1 << 20, ld_dy=1 << 20, ld_q=1 << 20,
+                                     ld_e=1 << 20, groups=1), 2)])
+def test_weight_grad_refusals(lib, kw, status):
+    assert lib.muon_weight_grad(ctypes.byref(wgrad(**kw)), None, 0, None) == status
+    assert lib.muon_weight_grad_workspace_size(ctypes.byref(wgrad(**kw))) == 0
+    assert lib.muon_weight_grad(None, None, 0, None) == 1
+
+
+def attention(**kw):
+    a = B.MuonAttention()
+    tok = dict(q=(0, 4), k=(1, 2), v=(2, 2), o=(3, 4), dout=(4, 4), dq=(5, 4), dk=(6, 2), dv=(7, 2))
+    for n, (i, h) in tok.items():
+        setattr(a, n, B.MuonHeads(FAKE + i * GB, h * 64, 64))
+    a.lse, a.s_max, a.q_offsets, a.k_offsets = FAKE + 8 * GB, FAKE + 9 * GB, FAKE + 10 * GB, FAKE + 11 * GB
+    a.q_tokens, a.k_tokens, a.n_seq, a.heads, a.kv_heads, a.head_dim = 100, 90, 3, 4, 2, 64
+    a.causal, a.scale = 1, 0.125
+    for n, v in kw.items():
+        setattr(a, n, v)
+    return a
+
+
+FORWARD = [
+    (dict(q_tokens=-1), 2), (dict(k_tokens=-1), 2), (dict(n_seq=0), 2), (dict(heads=0), 2), (dict(kv_heads=0), 2),
+    (dict(heads=5), 2), (dict(head_dim=0), 2), (dict(head_dim=68), 2), (dict(head_dim=136), 2), (dict(causal=2), 1),
+    (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=-1.0), 1),
+    (dict(q_offsets=None), 1), (dict(k_offsets=None), 1), (dict(q_offsets=FAKE + 10 * GB + 2), 1),
+    (dict(lse=None), 1), (dict(lse=FAKE + 8 * GB + 2), 1), (dict(s_max=FAKE + 9 * GB + 1), 1),
+    (dict(q=B.MuonHeads(None, 256, 64)), 1), (dict(v=B.MuonHeads(FAKE + 2 * GB + 8, 128, 64)), 1),
+    (dict(q=B.MuonHeads(FAKE, 252, 64)), 2), (dict(q=B.MuonHeads(FAKE, 256, 60)), 2),
+    (dict(q=B.MuonHeads(FAKE, 128, 64)), 2), (dict(k=B.MuonHeads(FAKE + GB, 128, 0)), 2),
+    (dict(k=B.MuonHeads(FAKE + GB, 0, 64)), 2), (dict(o=B.MuonHeads(FAKE + 64, 256, 64)), 4),
+    (dict(o=B.MuonHeads(FAKE, 256, 64)), 4), (dict(o=B.MuonHeads(FAKE + GB + 512, 256, 64)), 4),
+    (dict(lse=FAKE), 4), (dict(lse=FAKE + 3 * GB), 4), (dict(s_max=FAKE + 8 * GB + 40), 4),
+    (dict(s_max=FAKE + 2 * GB), 4), (dict(status_dev=FAKE + 10 * GB), 4), (dict(q_offsets=FAKE + 8 * GB), 4)]
+
+
+@pytest.mark.parametrize("kw,status", FORWARD)
+def test_attention_refusals(lib, kw, status):
+    assert lib.muon_attention_forward(ctypes.byref(attention(**kw)), None) == status
+    assert lib.muon_attention_forward(None, None) == 1
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dout=B.MuonHeads(None, 256, 64)), 1), (dict(dq=B.MuonHeads(FAKE + 5 * GB, 264, 62)), 2),
+    (dict(dq=B.MuonHeads(FAKE, 256, 64)), 4), (dict(dk=B.MuonHeads(FAKE + 7 * GB + 128, 128, 64)), 4),
+    (dict(dv=B.MuonHeads(FAKE + 2 * GB, 128, 64)), 4), (dict(lse=FAKE + 5 * GB), 4), (dict(head_dim=4), 2),
+    (dict(q_offsets=FAKE + 6 * GB), 4)])
+def test_attention_backward_refusals(lib, kw, status):
+    a = attention(**kw)
+    assert lib.muon_attention_workspace_size(ctypes.byref(a)) == 0
+    assert lib.muon_attention_backward(ctypes.byref(a), FAKE + 12 * GB, GB, None) == status
+    assert lib.muon_attention_backward(None, None, 0, None) == 1
+
+
+def test_attention_workspace(lib):
+    a = attention()
+    size = lib.muon_attention_workspace_size(ctypes.byref(a))
+    assert size >= 4 * 4 * 100
+    for ws, n in ((None, size), (FAKE + 12 * GB + 16, size), (FAKE + 12 * GB, size - 1)):
+        assert lib.muon_attention_backward(ctypes.byref(a), ws, n, None) == 5
+
+
+def test_interleaved_views_are_not_aliases(lib):
+    """dq, dk and dv as views of one buffer, token-major and head-major. The workspace size is
+    0 for a refused call and launches nothing."""
+    def size(a):
+        return lib.muon_attention_workspace_size(ctypes.byref(a))
+
+    row, base = 8 * 64, FAKE + 5 * GB
+    a = attention(dq=B.MuonHeads(base, row, 64), dk=B.MuonHeads(base + 512, row, 64),
+                  dv=B.MuonHeads(base + 768, row, 64))
+    assert size(a) > 0
+    a.dv = B.MuonHeads(base + 768 - 16, row, 64)       # reaches into dk
+    assert size(a) == 0
+    a.dv = B.MuonHeads(base + 768, row + 8, 64)        # another token stride: may collide
+    assert size(a) == 0
+    # heads outermost: planes of 100 tokens
+    a = attention(dq=B.MuonHeads(base, 64, 6400), dk=B.MuonHeads(base + 4 * 12800, 64, 6400),
+                  dv=B.MuonHeads(base + 6 * 12800, 64, 6400), k_tokens=100)
+    assert size(a) > 0
+    a.dv = B.MuonHeads(base + 6 * 12800 - 16, 64, 6400)
+    assert size(a) == 0
+
+
+def test_sizes_match_c_compiler(tmp_path):
+    import os
+    import subprocess
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "muon.h"\nint main(void){printf("%zu %zu %zu %zu %zu\\n",'
+                   'sizeof(muon_act8_t),sizeof(muon_weight_grad_t),sizeof(muon_attention_t),'
+                   'offsetof(muon_attention_t, scale),offsetof(muon_weight_grad_t, accumulate));return 0;}\n')
+    subprocess.run(["gcc", "-I", inc, str(src), "-o", str(tmp_path / "s")], check=True)
+    got = list(map(int, subprocess.run([str(tmp_path / "s")], capture_output=True, text=True).stdout.split()))
+    assert got == [ctypes.sizeof(B.MuonAct8), ctypes.sizeof(B.MuonWeightGrad), ctypes.sizeof(B.MuonAttention),
+                   B.MuonAttention.scale.offset, B.MuonWeightGrad.accumulate.offset]
+
+
+def test_binding_refuses_before_any_launch(lib):
+    import torch
+    t = torch.zeros(4, 4)
+    for f in (lambda: B.new_act8(4, 4, device="cpu"), lambda: B.act8_store([t], []),
+              lambda: B.weight_grad(t, None, t), lambda: B.weight_grad(t.to(torch.bfloat16), None, t),
+              lambda: B.attention_forward(t, t, t),
+              lambda: B.attention_forward(*(torch.zeros(4, 2, 8, dtype=torch.bfloat16),) * 3),
+              lambda: B.attention_forward(*(torch.zeros(4, 2, 8),) * 3),
+              lambda: B.Act8(t, t, 4)):
+        with pytest.raises(B.MuonError):
+            f()
