@@ -1,78 +1,489 @@
 // Weight gradients from 8-bit activation checkpoints (muon_weight_grad_t):
 //   dW_g[o, i] (+)= sum over the tokens t of group g of dY[t, o] q[t, i] 2^E[t, i/32]
 //
-// Simple form: a block computes a 64 x 64 tile of one group's gradient from tiles of 16
-// tokens in shared memory, 4 x 4 outputs a thread, in fp32 on the CUDA cores.
+// A GEMM whose reduction axis is the outer axis of both operands: A = dY^T and B = X^T are
+// both MN-major tiles (64 columns x 64 tokens a chunk, 128B swizzle), which tcgen05.mma takes
+// without a transpose. X is restored on the way: q 2^E has 7 significant bits, so it is exact
+// in bf16, and every product dY q 2^E is exact in the fp32 accumulator.
+//
+// Tile 256 (out) x 256 (in) per CTA pair (cta_group::2): each CTA loads its 128 columns of
+// dY and restores its 128 columns of X, so a restored element serves 256 output rows and the
+// restoring work per MMA is half that of single CTAs. Persistent, one CTA per SM, warps:
+//   0      TMA producer: per 64-token k-block 16 KB of dY and 8 KB of q into a ring of 5
+//          stages, on the CTA's own barrier
+//   1      TMEM allocator and (first CTA) MMA issuer, fp32 accumulators double-buffered
+//   2-9    restore: int8 to bf16 by byte permutes (below), into the stage's B operand; the
+//          last k-block of a group also clears the rows past its end in both operands, so
+//          that a neighbouring group's NaN cannot reach this one's sums
+//   10-13  epilogue: TMEM to registers, transposed through shared memory so that any
+//          alignment of dW is written in whole rows
+// Split of the work: tiles are dealt to the 74 CTA pairs in whole rounds; the tiles left over
+// for the last round are split along the tokens into as many parts as keep all pairs busy,
+// whose fp32 partial sums a second kernel adds in order (no atomics).
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
+#include <cstring>
 
 #include "muon.h"
+#include "ns_tc.h"
 #include "ptx.cuh"
 #include "validate.h"
 
 namespace muon {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 namespace {
 
-constexpr int kTile = 64, kTok = 16;
+constexpr int kTile = 256;                    // tile rows (out) and columns (in) of a CTA pair
+constexpr int kTok = 64;                      // tokens per k-block
+constexpr int kABytes = 128 * kTok * 2;       // a CTA's dY columns of one k-block
+constexpr int kQBytes = 128 * kTok;           // its stored X columns
+constexpr int kBBytes = 128 * kTok * 2;       // and the restored ones
+constexpr int kStageBytes = kABytes + kQBytes + kBBytes;
+constexpr int kStages = 5;
+constexpr int kRestoreWarps = 8, kEpiWarps = 4;
+constexpr int kFirstEpi = 2 + kRestoreWarps;
+constexpr int kThreads = 32 * (2 + kRestoreWarps + kEpiWarps);
+constexpr int kStgRow = 33;                   // padded row of the epilogue's transpose box
+constexpr int kStgBytes = kEpiWarps * 32 * kStgRow * 4;
+constexpr int kOffStg = kStages * kStageBytes;
+constexpr int kOffBar = kOffStg + kStgBytes;
+constexpr int kSmemBytes = kOffBar + 256 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kPairs = 74;                    // CTA pairs of a B200 (148 SMs)
+constexpr size_t kPartBytes = size_t(kTile) * kTile * 4;
 
-__device__ __forceinline__ float wg_scale(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7FC00000u)
-                      : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+// How the tiles are dealt: `whole` tiles by one unit each, the `left` ones by `splits` units.
+struct WgradSplit {
+  int32_t tiles_o, tiles_i;
+  int64_t tiles, whole, left;
+  int32_t splits;
+  int64_t units;
+};
+
+// A k-block takes about 0.3 us of a pair; partial sums and the second launch cost about 4 us,
+// so the last round is split where that saves at least 16 k-blocks, into parts of 4 or more.
+WgradSplit split_of(const muon_weight_grad_t& a) {
+  WgradSplit s;
+  s.tiles_o = static_cast<int32_t>((a.out + kTile - 1) / kTile);
+  s.tiles_i = static_cast<int32_t>((a.in + kTile - 1) / kTile);
+  s.tiles = static_cast<int64_t>(s.tiles_o) * s.tiles_i * a.groups;
+  s.whole = s.tiles / kPairs * kPairs;
+  s.left = s.tiles - s.whole;
+  s.splits = 1;
+  if (s.left > 0) {
+    const int64_t kb = (a.tokens / a.groups + kTok - 1) / kTok;  // of a mean group
+    int64_t n = kPairs / s.left;
+    if (n > kb / 4) n = kb / 4;
+    if (n > 1 && kb - kb / n >= 16) s.splits = static_cast<int32_t>(n);
+  }
+  if (s.splits == 1) {
+    s.whole = s.tiles;
+    s.left = 0;
+  }
+  s.units = s.whole + s.left * s.splits;
+  return s;
 }
+
+struct WgradParams {
+  CUtensorMap ty, tq;
+  muon_weight_grad_t a;
+  WgradSplit s;
+  float* parts;
+};
 
 // Token range of group g, clamped to the tensor.
-__device__ __forceinline__ void group_range(const muon_weight_grad_t& a, int g, int64_t* lo, int64_t* hi) {
+__device__ __forceinline__ void group_range(const muon_weight_grad_t& a, int g, int* lo, int* hi) {
+  const int tokens = static_cast<int>(a.tokens);
   if (a.offsets == nullptr) {
     *lo = 0;
-    *hi = a.tokens;
+    *hi = tokens;
     return;
   }
-  const int64_t b = a.offsets[g], e = a.offsets[g + 1];
-  *lo = b < 0 ? 0 : b > a.tokens ? a.tokens : b;
-  *hi = e < 0 ? 0 : e > a.tokens ? a.tokens : e;
-  if (*hi < *lo) *hi = *lo;
+  const int b = __ldg(a.offsets + g), e = __ldg(a.offsets + g + 1);
+  *lo = min(max(b, 0), tokens);
+  *hi = max(min(max(e, 0), tokens), *lo);
 }
 
-__global__ void __launch_bounds__(256) wgrad_simple_kernel(const __grid_constant__ muon_weight_grad_t a) {
-  __shared__ float sy[kTok][kTile + 1], sx[kTok][kTile + 1];
-  const int g = blockIdx.z;
-  const int64_t o0 = static_cast<int64_t>(blockIdx.y) * kTile, i0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  int64_t lo, hi;
-  group_range(a, g, &lo, &hi);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  const uint16_t* dY = static_cast<const uint16_t*>(a.dY);
-  for (int64_t t0 = lo; t0 < hi; t0 += kTok) {
-    for (int j = threadIdx.x; j < kTok * kTile; j += 256) {
-      const int r = j / kTile, c = j % kTile;
-      const int64_t t = t0 + r;
-      sy[r][c] = t < hi && o0 + c < a.out ? bf16_to_f32(dY[t * a.ld_dy + o0 + c]) : 0.f;
-      sx[r][c] = t < hi && i0 + c < a.in
-                     ? a.q[t * a.ld_q + i0 + c] * wg_scale(a.exps[t * a.ld_e + (i0 + c) / 32]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kTok; ++r)
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) acc[y][x] = fmaf(sy[r][ty + 16 * y], sx[r][tx + 16 * x], acc[y][x]);
-    __syncthreads();
+// One unit of work: a tile, its tokens [t0, t1) and, for a split tile, where its sum goes.
+struct Job {
+  int g, o0, i0;    // group, first row and column of the tile
+  int t0, t1, nkb;  // tokens and k-blocks
+  int part;         // partial sum, or -1: dW
+};
+
+__device__ __forceinline__ Job job_of(const WgradParams& P, int64_t u) {
+  Job j;
+  int64_t t = u;
+  int split = 0;
+  j.part = -1;
+  if (u >= P.s.whole) {
+    const int64_t r = (u - P.s.whole) / P.s.splits;
+    split = static_cast<int>(u - P.s.whole - r * P.s.splits);
+    t = P.s.whole + r;
+    j.part = static_cast<int>(u - P.s.whole);
   }
-  for (int y = 0; y < 4; ++y)
-    for (int x = 0; x < 4; ++x) {
-      const int64_t o = o0 + ty + 16 * y, i = i0 + tx + 16 * x;
-      if (o >= a.out || i >= a.in) continue;
-      const int64_t at = g * a.stride_w + o * a.ld_w + i;
-      if (a.w_dtype == MUON_F32) {
-        float* p = static_cast<float*>(a.dW) + at;
-        *p = a.accumulate ? *p + acc[y][x] : acc[y][x];
-      } else {
-        uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
-        *p = f32_to_bf16(a.accumulate ? bf16_to_f32(*p) + acc[y][x] : acc[y][x]);
+  const int per = P.s.tiles_o * P.s.tiles_i;
+  j.g = static_cast<int>(t / per);
+  const int rem = static_cast<int>(t - static_cast<int64_t>(j.g) * per);
+  j.o0 = rem / P.s.tiles_i * kTile;
+  j.i0 = rem % P.s.tiles_i * kTile;
+  int lo, hi;
+  group_range(P.a, j.g, &lo, &hi);
+  if (j.part >= 0) {
+    const int64_t kb = (hi - lo + kTok - 1) / kTok;
+    const int64_t b0 = kb * split / P.s.splits, b1 = kb * (split + 1) / P.s.splits;
+    if (b1 * kTok < hi - lo) hi = lo + static_cast<int>(b1) * kTok;
+    lo += static_cast<int>(b0) * kTok;
+  }
+  j.t0 = lo;
+  j.t1 = hi;
+  j.nkb = (hi - lo + kTok - 1) / kTok;
+  return j;
+}
+
+// 2^(byte - 127) in bf16, twice: byte 0 is a subnormal, byte 255 is NaN.
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
+  const uint32_t s = byte == 255u ? 0x7FC0u : byte == 0u ? 0x0040u : byte << 7;
+  return s | (s << 16);
+}
+
+// Four int8 to bf16 times a power of two. Low 7 bits under the exponent of 128 give
+// 128 + low7, the sign bit there gives 128 or 256; their difference is the value, exactly.
+__device__ __forceinline__ void restore4(uint32_t w, uint32_t s2, uint32_t* lo, uint32_t* hi) {
+  const uint32_t v = w & 0x7F7F7F7Fu, g = w & 0x80808080u, m = 0x43434343u;
+  const uint32_t a0 = __byte_perm(v, m, 0x4140), a1 = __byte_perm(v, m, 0x4342);
+  const uint32_t c0 = __byte_perm(g, m, 0x4140), c1 = __byte_perm(g, m, 0x4342);
+  auto bf2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+  const __nv_bfloat162 r0 = __hmul2(__hsub2(bf2(a0), bf2(c0)), bf2(s2));
+  const __nv_bfloat162 r1 = __hmul2(__hsub2(bf2(a1), bf2(c1)), bf2(s2));
+  *lo = *reinterpret_cast<const uint32_t*>(&r0);
+  *hi = *reinterpret_cast<const uint32_t*>(&r1);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constant__ WgradParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* stg = reinterpret_cast<float*>(smem + kOffStg);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // this CTA's dY and q have landed
+  uint64_t* ready = full + kStages;   // first CTA's: both CTAs' operands are in place
+  uint64_t* empty = ready + kStages;  // the MMAs have read the stage
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const muon_weight_grad_t& a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_cta_rank());
+  const int64_t unit0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&ready[s], 2 * kRestoreWarps);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t par = 0;
+      int64_t loads = 0;
+      bool ok = true;
+      for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+        const Job j = job_of(P, u);
+        for (int kb = 0; kb < j.nkb; ++kb) {
+          if (!mbar_wait(&empty[s], par ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * kStageBytes;
+          const int t = j.t0 + kb * kTok, o = j.o0 + rank * 128;
+          mbar_expect_tx(&full[s], kABytes + kQBytes);
+          tma_load_3d(st, &P.ty, &full[s], o, t, 0);
+          tma_load_3d(st + kABytes / 2, &P.ty, &full[s], o + 64, t, 0);
+          tma_load_3d(st + kABytes, &P.tq, &full[s], j.i0 + rank * 128, t, 0);
+          ++loads;
+          if (++s == kStages) s = 0, par ^= 1u;
+        }
+      }
+      if (!ok) {
+        set_error(a.status_dev, MUON_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // never leave with bulk copies still landing in shared memory
+      for (int64_t r = loads > kStages ? loads - kStages : 0; r < loads; ++r)
+        mbar_wait(&full[r % kStages], static_cast<uint32_t>((r / kStages) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(256, 256, true) | (1u << 15);  // A and B MN-major
+      const uint64_t mn = smem_desc_sw128(0, 64 * kTok * 2, 1024);
+      int s = 0, it = 0;
+      uint32_t par = 0;
+      bool ok = true;
+      for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+        const Job j = job_of(P, u);
+        if (j.nkb == 0) continue;
+        const int ab = it & 1;
+        const uint32_t apar = static_cast<uint32_t>((it >> 1) & 1);
+        ++it;
+        if (!mbar_wait(&tempty[ab], apar ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(ab * 256);
+        for (int kb = 0; kb < j.nkb; ++kb) {
+          if (!mbar_wait(&ready[s], par, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kABytes + kQBytes;
+          const uint64_t ad = mn | static_cast<uint64_t>((sa >> 4) & 0x3FFFu);
+          const uint64_t bd = mn | static_cast<uint64_t>((sb >> 4) & 0x3FFFu);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens are 2 KB of a chunk
+            umma_f16_pair(d, ad + 128u * kk, bd + 128u * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
+          umma_commit_pair(smem_u32(&empty[s]));
+          umma_commit_pair(peer_addr(&empty[s], 1));
+          if (++s == kStages) s = 0, par ^= 1u;
+        }
+        if (!ok) break;
+        umma_commit_pair(smem_u32(&tfull[ab]));
+        umma_commit_pair(peer_addr(&tfull[ab], 1));
+      }
+      if (!ok) {
+        set_error(a.status_dev, MUON_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      umma_commit_pair(smem_u32(done));
+      mbar_wait(done, 0, nullptr);
+    }
+  } else if (warp < kFirstEpi) {
+    // ------------------------------------------------------------ restore
+    // Warp w owns tokens 8w .. 8w+7 of a k-block. A quarter warp reads 64 bytes of token p
+    // and of token p ^ 5: with both layouts swizzled by the token's low 3 bits, its 16-byte
+    // reads of q and its 16-byte writes of bf16 then touch all 32 banks.
+    const int w = warp - 2;
+    const int p = lane >> 3, tok = 8 * w + ((lane & 4) ? p ^ 5 : p), pc = lane & 3;
+    int s = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+      const Job j = job_of(P, u);
+      if (j.nkb == 0) continue;
+      const int col = j.i0 + rank * 128;
+      // exponent bytes of this thread's two 16-column pieces (columns 16 pc + 64 h), one
+      // k-block ahead of their use
+      const int g0 = (col >> 5) + (pc >> 1), ng = static_cast<int>((a.in + 31) >> 5);
+      uint32_t next[2];
+      auto fetch = [&](int kb) {
+        const int t = j.t0 + kb * kTok + tok;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          next[h] = t < j.t1 && g0 + 2 * h < ng
+                        ? __ldg(a.exps + static_cast<int64_t>(t) * a.ld_e + g0 + 2 * h) : 1u;
+      };
+      fetch(0);
+      for (int kb = 0; kb < j.nkb; ++kb) {
+        uint32_t sc[2] = {scale_bf16x2(next[0]), scale_bf16x2(next[1])};
+        if (kb + 1 < j.nkb) fetch(kb + 1);
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], par, abort_flag))) {
+          ok = false;
+          if (lane == 0) {
+            set_error(a.status_dev, MUON_ERR_TIMEOUT);
+            *abort_flag = 1;
+          }
+          break;
+        }
+        uint8_t* st = smem + s * kStageBytes;
+        const bool live = j.t0 + kb * kTok + tok < j.t1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = *reinterpret_cast<const uint4*>(st + kABytes + tok * 128 + (((4 * h + pc) ^ (tok & 7)) << 4));
+          uint4 x0, x1;
+          restore4(q.x, sc[h], &x0.x, &x0.y);
+          restore4(q.y, sc[h], &x0.z, &x0.w);
+          restore4(q.z, sc[h], &x1.x, &x1.y);
+          restore4(q.w, sc[h], &x1.z, &x1.w);
+          if (!live) x0 = x1 = make_uint4(0, 0, 0, 0);
+          uint8_t* row = st + kABytes + kQBytes + h * (64 * kTok * 2) + tok * 128;
+          *reinterpret_cast<uint4*>(row + (((2 * pc) ^ (tok & 7)) << 4)) = x0;
+          *reinterpret_cast<uint4*>(row + (((2 * pc + 1) ^ (tok & 7)) << 4)) = x1;
+          if (!live) {  // the dY of tokens past the group: zeros too
+            uint8_t* y = st + h * (64 * kTok * 2) + tok * 128 + 32 * pc;
+            *reinterpret_cast<uint4*>(y) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(y + 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(&ready[s]);
+          else mbar_arrive_cluster(peer_addr(&ready[s], 0));
+        }
+        if (++s == kStages) s = 0, par ^= 1u;
       }
     }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;  // the TMEM lane quarter this warp may access
+    float* box = stg + (warp - kFirstEpi) * 32 * kStgRow;
+    int it = 0;
+    bool ok = true;
+    for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+      const Job j = job_of(P, u);
+      if (j.nkb == 0 && (j.part >= 0 || a.accumulate)) continue;
+      const int ab = it & 1;
+      if (j.nkb > 0) {
+        const uint32_t apar = static_cast<uint32_t>((it >> 1) & 1);
+        ++it;
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[ab], apar, abort_flag))) {
+          ok = false;
+          if (lane == 0) {
+            set_error(a.status_dev, MUON_ERR_TIMEOUT);
+            *abort_flag = 1;
+          }
+          break;
+        }
+        tc_fence_after();
+      }
+      const int r0 = rank * 128 + quad * 32;                    // first tile row of this warp
+      const int nrow = min(32, static_cast<int>(a.out) - j.o0 - r0);
+#pragma unroll 1
+      for (int c = 0; c < kTile / 32; ++c) {
+        uint32_t v[32];
+        if (j.nkb > 0) {
+          tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(ab * 256 + c * 32), v);
+          tmem_wait_ld();
+          if (c == kTile / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive(&tempty[ab]);
+              else mbar_arrive_cluster(peer_addr(&tempty[ab], 0));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) box[lane * kStgRow + i] = __uint_as_float(v[i]);
+        __syncwarp();
+        const int col = j.i0 + c * 32 + lane;
+        if (col < a.in) {
+          if (j.part >= 0) {
+            float* p = P.parts + static_cast<int64_t>(j.part) * (kTile * kTile) + r0 * kTile + c * 32 + lane;
+            for (int r = 0; r < nrow; ++r) p[r * kTile] = box[r * kStgRow + lane];
+          } else {
+            const int64_t at = j.g * a.stride_w + (j.o0 + r0) * a.ld_w + col;
+            if (a.w_dtype == MUON_F32) {
+              float* p = static_cast<float*>(a.dW) + at;
+              if (a.accumulate)
+                for (int r = 0; r < nrow; ++r) p[r * a.ld_w] += box[r * kStgRow + lane];
+              else
+                for (int r = 0; r < nrow; ++r) p[r * a.ld_w] = box[r * kStgRow + lane];
+            } else {
+              uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
+              if (a.accumulate)
+                for (int r = 0; r < nrow; ++r)
+                  p[r * a.ld_w] = f32_to_bf16(bf16_to_f32(p[r * a.ld_w]) + box[r * kStgRow + lane]);
+              else
+                for (int r = 0; r < nrow; ++r) p[r * a.ld_w] = f32_to_bf16(box[r * kStgRow + lane]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  __syncthreads();
+  cluster_sync_all();  // no cross-CTA signal or TMEM access outstanding
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Adds the partial sums of the split tiles in order: a block per 8 rows of a tile, a thread
+// per column.
+__global__ void __launch_bounds__(kTile) wgrad_join_kernel(const __grid_constant__ WgradParams P) {
+  const muon_weight_grad_t& a = P.a;
+  const int64_t r = blockIdx.x / (kTile / 8);
+  const int row0 = blockIdx.x % (kTile / 8) * 8;
+  const Job j = job_of(P, P.s.whole + r * P.s.splits);
+  int lo, hi;
+  group_range(a, j.g, &lo, &hi);
+  const int64_t kb = (hi - lo + kTok - 1) / kTok;
+  const int col = j.i0 + threadIdx.x;
+  if (col >= a.in) return;
+  float sum[8] = {};
+  for (int s = 0; s < P.s.splits; ++s) {
+    if (kb * s / P.s.splits == kb * (s + 1) / P.s.splits) continue;  // a part without tokens
+    const float* p = P.parts + (r * P.s.splits + s) * (kTile * kTile) + row0 * kTile + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j.o0 + row0 + i < a.out) sum[i] += __ldcs(p + i * kTile);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t o = j.o0 + row0 + i;
+    if (o >= a.out) return;
+    const int64_t at = j.g * a.stride_w + o * a.ld_w + col;
+    if (a.w_dtype == MUON_F32) {
+      float* p = static_cast<float*>(a.dW) + at;
+      *p = a.accumulate ? *p + sum[i] : sum[i];
+    } else {
+      uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
+      *p = f32_to_bf16(a.accumulate ? bf16_to_f32(*p) + sum[i] : sum[i]);
+    }
+  }
+}
+
+// Tensor map of one operand: tokens x cols, boxes of 128 bytes x 64 tokens (the third axis has
+// one entry, its stride is never used).
+bool encode_tokens_map(CUtensorMap* out, CUtensorMapDataType type, int elem, const void* base,
+                       int64_t cols, int64_t tokens, int64_t ld) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens), 1};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * elem), static_cast<cuuint64_t>(ld * elem)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), kTok, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(out, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 muon_status_t validate_weight_grad(const muon_weight_grad_t* p) {
@@ -116,22 +527,57 @@ muon_status_t validate_weight_grad(const muon_weight_grad_t* p) {
 }  // namespace muon
 
 extern "C" MUON_API size_t muon_weight_grad_workspace_size(const muon_weight_grad_t* a) {
-  (void)a;
-  return 0;
+  using namespace muon;
+  if (validate_weight_grad(a) != MUON_OK) return 0;
+  const WgradSplit s = split_of(*a);
+  return static_cast<size_t>(s.left * s.splits) * kPartBytes;
 }
 
 extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, void* workspace,
                                                    size_t ws_bytes, void* stream) {
   using namespace muon;
-  (void)workspace;
-  (void)ws_bytes;
   const muon_status_t v = validate_weight_grad(a);
   if (v != MUON_OK) return v;
+  WgradParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.a = *a;
+  P.s = split_of(*a);
+  const size_t need = static_cast<size_t>(P.s.left * P.s.splits) * kPartBytes;
+  if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need))
+    return MUON_ERR_WORKSPACE;
+  P.parts = static_cast<float*>(workspace);
   int dev = 0, sms = 0;
   const muon_status_t d = current_device(&dev, &sms);
   if (d != MUON_OK) return d;
-  const int64_t ti = (a->out + kTile - 1) / kTile, tj = (a->in + kTile - 1) / kTile;
-  if (ti > 65535) return MUON_ERR_SHAPE;
-  wgrad_simple_kernel<<<dim3(tj, ti, a->groups), 256, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  if (a->tokens > 0 &&
+      !(encode_tokens_map(&P.ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a->dY, a->out, a->tokens, a->ld_dy) &&
+        encode_tokens_map(&P.tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->q, a->in, a->tokens, a->ld_q)))
+    return MUON_ERR_CUDA;
+  // the shared-memory opt-in is a per-device attribute: set it once on each device
+  static std::atomic<uint64_t> attr_devices{0};
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
+    if (cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+      return MUON_ERR_CUDA;
+    attr_devices.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t pairs = P.s.units < sms / 2 ? P.s.units : sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, wgrad_kernel, P) != cudaSuccess) return MUON_ERR_CUDA;
+  if (P.s.left > 0) {
+    wgrad_join_kernel<<<static_cast<unsigned>(P.s.left * (kTile / 8)), kTile, 0, cfg.stream>>>(P);
+    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  }
+  return MUON_OK;
 }
