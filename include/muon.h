@@ -296,8 +296,8 @@ MUON_API muon_status_t muon_qk_clip(const muon_qk_slice_t* slices, int n, const 
  * value has 7 significant bits, so BF16 and F32 hold it exactly. A group with a NaN or an
  * infinity gets byte 255 and restores as NaN throughout. Byte 0 stands for 2^-127; store
  * never writes it.
- * q is 16-byte aligned with ld_q a multiple of 16; exps is 4-byte aligned with ld_e a
- * multiple of 4. rows may be 0. Bytes of q and exps beyond cols are not written. */
+ * q and exps are 16-byte aligned, ld_q and ld_e multiples of 16. rows may be 0. Bytes of q
+ * and exps beyond cols are neither read nor written. */
 typedef struct {
   void* X;             /* read by muon_act8_store, written by muon_act8_restore */
   int8_t* q;

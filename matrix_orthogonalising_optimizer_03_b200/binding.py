@@ -447,7 +447,7 @@ class Act8:
     def ld(self):
         """Leading dimensions of q and exps (a single row may carry any stride)."""
         if self.rows <= 1:
-            return (self.cols + 15) // 16 * 16, ((self.cols + 31) // 32 + 3) // 4 * 4
+            return (self.cols + 15) // 16 * 16, (self.cols + 511) // 512 * 16
         return self.q.stride(0), self.exps.stride(0)
 
 
@@ -455,7 +455,7 @@ def new_act8(rows: int, cols: int, device="cuda") -> Act8:
     """Buffers for an 8-bit checkpoint of a rows x cols activation (see `act8_store`)."""
     torch = _torch()
     return Act8(torch.zeros((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device),
-                torch.ones((rows, ((cols + 31) // 32 + 3) // 4 * 4), dtype=torch.uint8, device=device),
+                torch.ones((rows, (cols + 511) // 512 * 16), dtype=torch.uint8, device=device),
                 cols)
 
 

@@ -233,7 +233,7 @@ muon_status_t validate_act8(const muon_act8_t* items, int n, bool store) {
     if (a.dtype != MUON_F32 && a.dtype != MUON_BF16) return MUON_ERR_DTYPE;
     const int64_t groups = (a.cols + 31) / 32;
     if (a.rows < 0 || a.cols < 1 || a.cols > kMaxCols || a.ld_x < a.cols || a.ld_q < a.cols ||
-        a.ld_e < groups || a.ld_q % 16 || a.ld_e % 4)
+        a.ld_e < groups || a.ld_q % 16 || a.ld_e % 16)
       return MUON_ERR_SHAPE;
     // every byte offset stays far inside 63 bits
     const int64_t lim = int64_t(1) << 40;
@@ -243,7 +243,7 @@ muon_status_t validate_act8(const muon_act8_t* items, int n, bool store) {
     if (a.rows == 0) continue;
     if (a.X == nullptr || a.q == nullptr || a.exps == nullptr) return MUON_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(a.X) % (a.dtype == MUON_BF16 ? 2 : 4) ||
-        reinterpret_cast<uintptr_t>(a.q) % 16 || reinterpret_cast<uintptr_t>(a.exps) % 4)
+        reinterpret_cast<uintptr_t>(a.q) % 16 || reinterpret_cast<uintptr_t>(a.exps) % 16)
       return MUON_ERR_INVALID_ARG;
   }
   for (int i = 0; i < n; ++i) {

@@ -9,8 +9,8 @@
 // Tile 256 (out) x 256 (in) per CTA pair (cta_group::2): each CTA loads its 128 columns of
 // dY and restores its 128 columns of X, so a restored element serves 256 output rows and the
 // restoring work per MMA is half that of single CTAs. Persistent, one CTA per SM, warps:
-//   0      TMA producer: per 64-token k-block 16 KB of dY and 8 KB of q into a ring of 5
-//          stages, on the CTA's own barrier
+//   0      TMA producer: per 64-token k-block 16 KB of dY, 8 KB of q and 1 KB of exponents into
+//          a ring of 5 stages, on the CTA's own barrier
 //   1      TMEM allocator and (first CTA) MMA issuer, fp32 accumulators double-buffered
 //   2-9    restore: int8 to bf16 by byte permutes (below), into the stage's B operand; the
 //          last k-block of a group also clears the rows past its end in both operands, so
@@ -44,9 +44,13 @@ constexpr int kTok = 64;                      // tokens per k-block
 constexpr int kABytes = 128 * kTok * 2;       // a CTA's dY columns of one k-block
 constexpr int kQBytes = 128 * kTok;           // its stored X columns
 constexpr int kBBytes = 128 * kTok * 2;       // and the restored ones
-constexpr int kStageBytes = kABytes + kQBytes + kBBytes;
+constexpr int kEBytesRow = 16;                // exponents of 512 columns, the smallest TMA row
+constexpr int kEBytes = kEBytesRow * kTok;
+constexpr int kOffE = kABytes + kQBytes + kBBytes;
+constexpr int kStageBytes = kOffE + kEBytes;
 constexpr int kStages = 5;
-constexpr int kRestoreWarps = 8, kEpiWarps = 4;
+constexpr int kTeams = 2, kTeamWarps = 4;  // restore teams take k-blocks in turn
+constexpr int kRestoreWarps = kTeams * kTeamWarps, kEpiWarps = 4;
 constexpr int kFirstEpi = 2 + kRestoreWarps;
 constexpr int kThreads = 32 * (2 + kRestoreWarps + kEpiWarps);
 constexpr int kStgRow = 33;                   // padded row of the epilogue's transpose box
@@ -91,7 +95,7 @@ WgradSplit split_of(const muon_weight_grad_t& a) {
 }
 
 struct WgradParams {
-  CUtensorMap ty, tq;
+  CUtensorMap ty, tq, te;
   muon_weight_grad_t a;
   WgradSplit s;
   float* parts;
@@ -108,6 +112,14 @@ __device__ __forceinline__ void group_range(const muon_weight_grad_t& a, int g, 
   const int b = __ldg(a.offsets + g), e = __ldg(a.offsets + g + 1);
   *lo = min(max(b, 0), tokens);
   *hi = max(min(max(e, 0), tokens), *lo);
+}
+
+// Arrives on the first CTA's mbarrier. What it signals is read by the tensor core from this
+// CTA's own shared memory, behind the writer's proxy fence; no generic access of the other CTA
+// depends on it, so the default (CTA) scope is enough. A cluster-scope release here flushed
+// this CTA's traffic on every k-block: 1300 cycles against 260.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // One unit of work: a tile, its tokens [t0, t1) and, for a split tile, where its sum goes.
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&ready[s], 2 * kRestoreWarps);
+      mbar_init(&ready[s], 2 * kTeamWarps);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -225,10 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           }
           uint8_t* st = smem + s * kStageBytes;
           const int t = j.t0 + kb * kTok, o = j.o0 + rank * 128;
-          mbar_expect_tx(&full[s], kABytes + kQBytes);
+          mbar_expect_tx(&full[s], kABytes + kQBytes + kEBytes);
           tma_load_3d(st, &P.ty, &full[s], o, t, 0);
           tma_load_3d(st + kABytes / 2, &P.ty, &full[s], o + 64, t, 0);
           tma_load_3d(st + kABytes, &P.tq, &full[s], j.i0 + rank * 128, t, 0);
+          tma_load_3d(st + kOffE, &P.te, &full[s], (j.i0 + rank * 128) / 512 * kEBytesRow, t, 0);
           ++loads;
           if (++s == kStages) s = 0, par ^= 1u;
         }
@@ -290,34 +303,24 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     }
   } else if (warp < kFirstEpi) {
     // ------------------------------------------------------------ restore
-    // Warp w owns tokens 8w .. 8w+7 of a k-block. A quarter warp reads 64 bytes of token p
-    // and of token p ^ 5: with both layouts swizzled by the token's low 3 bits, its 16-byte
-    // reads of q and its 16-byte writes of bf16 then touch all 32 banks.
-    const int w = warp - 2;
-    const int p = lane >> 3, tok = 8 * w + ((lane & 4) ? p ^ 5 : p), pc = lane & 3;
-    int s = 0;
-    uint32_t par = 0;
+    // Two teams of four warps take the k-blocks in turn, so that a team has the time of two
+    // k-blocks for its loads, fence and signal. Warp w of a team owns tokens 16w .. 16w+15. A
+    // quarter warp reads 64 bytes of token p and of token p ^ 5: with both layouts swizzled by
+    // the token's low 3 bits, its 16-byte reads of q and its 16-byte writes of bf16 then touch
+    // all 32 banks.
+    const int team = (warp - 2) / kTeamWarps, w = (warp - 2) % kTeamWarps;
+    const int p = lane >> 3, tok = 16 * w + ((lane & 4) ? p ^ 5 : p), pc = lane & 3;
+    int64_t q0 = 0;  // k-blocks of the units before this one
     bool ok = true;
     for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
       const Job j = job_of(P, u);
-      if (j.nkb == 0) continue;
-      const int col = j.i0 + rank * 128;
-      // exponent bytes of this thread's two 16-column pieces (columns 16 pc + 64 h), one
-      // k-block ahead of their use
-      const int g0 = (col >> 5) + (pc >> 1), ng = static_cast<int>((a.in + 31) >> 5);
-      uint32_t next[2];
-      auto fetch = [&](int kb) {
-        const int t = j.t0 + kb * kTok + tok;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          next[h] = t < j.t1 && g0 + 2 * h < ng
-                        ? __ldg(a.exps + static_cast<int64_t>(t) * a.ld_e + g0 + 2 * h) : 1u;
-      };
-      fetch(0);
-      for (int kb = 0; kb < j.nkb; ++kb) {
-        uint32_t sc[2] = {scale_bf16x2(next[0]), scale_bf16x2(next[1])};
-        if (kb + 1 < j.nkb) fetch(kb + 1);
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], par, abort_flag))) {
+      // the team's k-blocks of this unit: the pair's k-blocks q0 + kb with its parity
+      int kb = static_cast<int>((team - q0) & 1);
+      const int sel = (j.i0 + rank * 128) / 32 % kEBytesRow;  // its exponents within a stage's row
+      for (; kb < j.nkb; kb += kTeams) {
+        const int64_t q = q0 + kb;
+        const int s = static_cast<int>(q % kStages);
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], static_cast<uint32_t>((q / kStages) & 1), abort_flag))) {
           ok = false;
           if (lane == 0) {
             set_error(a.status_dev, MUON_ERR_TIMEOUT);
@@ -326,21 +329,31 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           break;
         }
         uint8_t* st = smem + s * kStageBytes;
-        const bool live = j.t0 + kb * kTok + tok < j.t1;
+        uint4 v[4];
+        uint32_t e[2];  // exponents of the 128 columns for each of the thread's two tokens
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 q = *reinterpret_cast<const uint4*>(st + kABytes + tok * 128 + (((4 * h + pc) ^ (tok & 7)) << 4));
+        for (int i = 0; i < 2; ++i)
+          e[i] = *reinterpret_cast<const uint32_t*>(st + kOffE + (tok + 8 * i) * kEBytesRow + sel);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // token 8 (i / 2) further, columns 64 (i % 2) further
+          v[i] = *reinterpret_cast<const uint4*>(st + kABytes + (tok + 4 * (i & 2)) * 128 +
+                                                 (((4 * (i & 1) + pc) ^ (tok & 7)) << 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int h = i & 1, tk = tok + 4 * (i & 2);
+          const bool live = j.t0 + kb * kTok + tk < j.t1;
+          const uint32_t sc = scale_bf16x2((e[i >> 1] >> (8 * (2 * h + (pc >> 1)))) & 0xFFu);
           uint4 x0, x1;
-          restore4(q.x, sc[h], &x0.x, &x0.y);
-          restore4(q.y, sc[h], &x0.z, &x0.w);
-          restore4(q.z, sc[h], &x1.x, &x1.y);
-          restore4(q.w, sc[h], &x1.z, &x1.w);
+          restore4(v[i].x, sc, &x0.x, &x0.y);
+          restore4(v[i].y, sc, &x0.z, &x0.w);
+          restore4(v[i].z, sc, &x1.x, &x1.y);
+          restore4(v[i].w, sc, &x1.z, &x1.w);
           if (!live) x0 = x1 = make_uint4(0, 0, 0, 0);
-          uint8_t* row = st + kABytes + kQBytes + h * (64 * kTok * 2) + tok * 128;
+          uint8_t* row = st + kABytes + kQBytes + h * (64 * kTok * 2) + tk * 128;
           *reinterpret_cast<uint4*>(row + (((2 * pc) ^ (tok & 7)) << 4)) = x0;
           *reinterpret_cast<uint4*>(row + (((2 * pc + 1) ^ (tok & 7)) << 4)) = x1;
           if (!live) {  // the dY of tokens past the group: zeros too
-            uint8_t* y = st + h * (64 * kTok * 2) + tok * 128 + 32 * pc;
+            uint8_t* y = st + h * (64 * kTok * 2) + tk * 128 + 32 * pc;
             *reinterpret_cast<uint4*>(y) = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(y + 16) = make_uint4(0, 0, 0, 0);
           }
@@ -349,10 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) {
           if (rank == 0) mbar_arrive(&ready[s]);
-          else mbar_arrive_cluster(peer_addr(&ready[s], 0));
+          else mbar_arrive_peer(peer_addr(&ready[s], 0));
         }
-        if (++s == kStages) s = 0, par ^= 1u;
       }
+      q0 += j.nkb;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -471,18 +484,19 @@ __global__ void __launch_bounds__(kTile) wgrad_join_kernel(const __grid_constant
   }
 }
 
-// Tensor map of one operand: tokens x cols, boxes of 128 bytes x 64 tokens (the third axis has
-// one entry, its stride is never used).
-bool encode_tokens_map(CUtensorMap* out, CUtensorMapDataType type, int elem, const void* base,
+// Tensor map of one operand: tokens x cols, boxes of `row` bytes x 64 tokens, with the 128B
+// swizzle for rows of 128 bytes (the third axis has one entry, its stride is never used).
+bool encode_tokens_map(CUtensorMap* out, CUtensorMapDataType type, int elem, int row, const void* base,
                        int64_t cols, int64_t tokens, int64_t ld) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(tokens), 1};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * elem), static_cast<cuuint64_t>(ld * elem)};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem), kTok, 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(row / elem), kTok, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return encode(out, type, 3, const_cast<void*>(base), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -496,7 +510,7 @@ muon_status_t validate_weight_grad(const muon_weight_grad_t* p) {
     return MUON_ERR_SHAPE;
   if (a.ld_dy < a.out || a.ld_q < a.in || a.ld_e < (a.in + 31) / 32 || a.ld_w < a.in ||
       a.ld_dy >= lim || a.ld_q >= lim || a.ld_e >= lim || a.ld_w >= lim ||
-      a.ld_dy % 8 || a.ld_q % 16 || a.ld_e % 4)
+      a.ld_dy % 8 || a.ld_q % 16 || a.ld_e % 16)
     return MUON_ERR_SHAPE;
   if (a.groups > 1 && (a.stride_w < (a.out - 1) * a.ld_w + a.in || a.stride_w >= (int64_t(1) << 44)))
     return MUON_ERR_SHAPE;
@@ -509,7 +523,7 @@ muon_status_t validate_weight_grad(const muon_weight_grad_t* p) {
   if (a.tokens > 0) {
     if (a.dY == nullptr || a.q == nullptr || a.exps == nullptr) return MUON_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(a.dY) % 16 || reinterpret_cast<uintptr_t>(a.q) % 16 ||
-        reinterpret_cast<uintptr_t>(a.exps) % 4)
+        reinterpret_cast<uintptr_t>(a.exps) % 16)
       return MUON_ERR_INVALID_ARG;
   }
   const int64_t gs = a.groups > 1 ? a.stride_w : 0;
@@ -550,8 +564,10 @@ extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, 
   const muon_status_t d = current_device(&dev, &sms);
   if (d != MUON_OK) return d;
   if (a->tokens > 0 &&
-      !(encode_tokens_map(&P.ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a->dY, a->out, a->tokens, a->ld_dy) &&
-        encode_tokens_map(&P.tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->q, a->in, a->tokens, a->ld_q)))
+      !(encode_tokens_map(&P.ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 128, a->dY, a->out, a->tokens, a->ld_dy) &&
+        encode_tokens_map(&P.tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, a->q, a->in, a->tokens, a->ld_q) &&
+        encode_tokens_map(&P.te, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kEBytesRow, a->exps, (a->in + 31) / 32, a->tokens,
+                          a->ld_e)))
     return MUON_ERR_CUDA;
   // the shared-memory opt-in is a per-device attribute: set it once on each device
   static std::atomic<uint64_t> attr_devices{0};

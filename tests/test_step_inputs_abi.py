@@ -18,7 +18,7 @@ def lib():
 
 
 def act8(**kw):
-    a = dict(X=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, rows=100, cols=70, ld_x=70, ld_q=80, ld_e=4, dtype=1,
+    a = dict(X=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, rows=100, cols=70, ld_x=70, ld_q=80, ld_e=16, dtype=1,
              reserved=0)
     a.update(kw)
     return B.MuonAct8(**a)
@@ -26,9 +26,9 @@ def act8(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), 3), (dict(rows=-1), 2), (dict(cols=0), 2), (dict(cols=(1 << 26) + 1, ld_x=1 << 27, ld_q=1 << 27), 2),
-    (dict(ld_x=69), 2), (dict(ld_q=64), 2), (dict(ld_q=72), 2), (dict(ld_e=3), 2), (dict(ld_e=6), 2),
+    (dict(ld_x=69), 2), (dict(ld_q=64), 2), (dict(ld_q=72), 2), (dict(ld_e=2), 2), (dict(ld_e=24), 2),
     (dict(X=None), 1), (dict(q=None), 1), (dict(exps=None), 1), (dict(X=FAKE + 1), 1), (dict(q=FAKE + GB + 8), 1),
-    (dict(exps=FAKE + 2 * GB + 1), 1), (dict(dtype=0, X=FAKE + 2), 1), (dict(q=FAKE + 64), 4),
+    (dict(exps=FAKE + 2 * GB + 8), 1), (dict(dtype=0, X=FAKE + 2), 1), (dict(q=FAKE + 64), 4),
     (dict(exps=FAKE + 64), 4), (dict(rows=1 << 41), 2), (dict(rows=1 << 39, ld_x=1 << 30), 2)])
 def test_act8_refusals(lib, kw, status):
     for f in (lib.muon_act8_store, lib.muon_act8_restore):
@@ -47,7 +47,7 @@ def test_act8_aliases_between_items(lib):
 
 def wgrad(**kw):
     a = dict(dY=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, dW=FAKE + 3 * GB, offsets=FAKE + 4 * GB, status_dev=None,
-             tokens=100, out=50, in_=70, ld_dy=56, ld_q=80, ld_e=4, ld_w=70, stride_w=3500, groups=3, w_dtype=1,
+             tokens=100, out=50, in_=70, ld_dy=56, ld_q=80, ld_e=16, ld_w=70, stride_w=3500, groups=3, w_dtype=1,
              accumulate=0, reserved=0)
     a.update(kw)
     return B.MuonWeightGrad(**a)
@@ -55,10 +55,10 @@ def wgrad(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(w_dtype=4), 3), (dict(tokens=-1), 2), (dict(out=0), 2), (dict(in_=0), 2), (dict(groups=0), 2),
-    (dict(ld_dy=50), 2), (dict(ld_dy=48), 2), (dict(ld_q=64), 2), (dict(ld_q=72), 2), (dict(ld_e=2), 2),
+    (dict(ld_dy=50), 2), (dict(ld_dy=48), 2), (dict(ld_q=64), 2), (dict(ld_q=72), 2), (dict(ld_e=8), 2),
     (dict(ld_w=69), 2), (dict(stride_w=3499), 2), (dict(accumulate=2), 1), (dict(dW=None), 1), (dict(offsets=None), 1),
     (dict(dY=None), 1), (dict(q=None), 1), (dict(exps=None), 1), (dict(dY=FAKE + 8), 1), (dict(q=FAKE + GB + 4), 1),
-    (dict(exps=FAKE + 2 * GB + 2), 1), (dict(dW=FAKE + 3 * GB + 1), 1), (dict(offsets=FAKE + 4 * GB + 2), 1),
+    (dict(exps=FAKE + 2 * GB + 4), 1), (dict(dW=FAKE + 3 * GB + 1), 1), (dict(offsets=FAKE + 4 * GB + 2), 1),
     (dict(status_dev=FAKE + 2), 1), (dict(dW=FAKE + 64), 4), (dict(dW=FAKE + GB + 64), 4),
     (dict(dW=FAKE + 2 * GB + 64), 4), (dict(dW=FAKE + 4 * GB), 4), (dict(status_dev=FAKE + 3 * GB + 400), 4),
     (dict(tokens=1 << 31), 2), (dict(out=1 << 20, in_=1 << 20, ld_w=1 << 20, ld_dy=1 << 20, ld_q=1 << 20,
