@@ -294,8 +294,8 @@ MUON_API muon_status_t muon_qk_clip(const muon_qk_slice_t* slices, int n, const 
  *   q = clamp(round_half_even(x 2^-E), -127, 127),      restored value = q 2^E
  * |x - q 2^E| <= 2^E / 2 (2^E where |x| rounds past 127), 2^E <= amax / 64. A restored
  * value has 7 significant bits, so BF16 and F32 hold it exactly. A group with a NaN or an
- * infinity gets byte 255 and restores as NaN throughout. Byte 0 stands for 2^-127; store
- * never writes it.
+ * infinity gets byte 255 and zeros: byte 255 stands for an infinite scale, so the group
+ * restores as NaN throughout. Byte 0 stands for a scale of zero; store never writes it.
  * q and exps are 16-byte aligned, ld_q and ld_e multiples of 16. rows may be 0. Bytes of q
  * and exps beyond cols are neither read nor written. */
 typedef struct {

@@ -151,12 +151,6 @@ __global__ void __launch_bounds__(kThreads) act8_store_kernel(const __grid_const
   }
 }
 
-// 2^(byte - 127) as fp32: byte 0 is a subnormal, byte 255 is NaN.
-__device__ __forceinline__ float act8_scale(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7FC00000u)
-                      : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
-}
-
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_constant__ Act8Launch L) {
   const int it = find_item(L);
   const muon_act8_t& a = L.a[it];
@@ -189,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_con
   for (int u = 0; u < kUnits; ++u) {
     const Unit t = unit_at(a, row0, rem0, upr, u);
     if (!t.live || t.col >= a.cols) continue;
-    const float s = act8_scale(byte[u]);
+    const float s = __uint_as_float(byte[u] << 23);  // byte 0: zero, byte 255: infinity, times 0 NaN
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)

@@ -1,22 +1,29 @@
 // Weight gradients from 8-bit activation checkpoints (muon_weight_grad_t):
 //   dW_g[o, i] (+)= sum over the tokens t of group g of dY[t, o] q[t, i] 2^E[t, i/32]
 //
-// A GEMM whose reduction axis is the outer axis of both operands: A = dY^T and B = X^T are
-// both MN-major tiles (64 columns x 64 tokens a chunk, 128B swizzle), which tcgen05.mma takes
-// without a transpose. X is restored on the way: q 2^E has 7 significant bits, so it is exact
-// in bf16, and every product dY q 2^E is exact in the fp32 accumulator.
+// A GEMM whose reduction axis is the outer axis of both operands. dY is taken as it lies in
+// memory: an MN-major tile (64 columns x 64 tokens a chunk, 128B swizzle) as the B operand of
+// tcgen05.mma. X^T is the A operand and lives in tensor memory, where a lane is a column of X
+// and a 32-bit column two consecutive tokens: ldmatrix transposes 16 x 16 bytes of q on the
+// way to the registers in just the fragment that tcgen05.st takes, so the restored tile never
+// passes through shared memory. (The first form restored into a shared-memory operand: 16 KB
+// written and 16 KB read per k-block and CTA, 80 KB of shared-memory traffic in all against
+// 128 B a cycle, which held it at 850 cycles a k-block where the MMAs need 512.)
+// q 2^E has 7 significant bits and is exact in bf16, so every product dY q 2^E is exact and
+// sums are fp32 in tensor memory.
 //
-// Tile 256 (out) x 256 (in) per CTA pair (cta_group::2): each CTA loads its 128 columns of
-// dY and restores its 128 columns of X, so a restored element serves 256 output rows and the
-// restoring work per MMA is half that of single CTAs. Persistent, one CTA per SM, warps:
-//   0      TMA producer: per 64-token k-block 16 KB of dY, 8 KB of q and 1 KB of exponents into
-//          a ring of 5 stages, on the CTA's own barrier
-//   1      TMEM allocator and (first CTA) MMA issuer, fp32 accumulators double-buffered
-//   2-9    restore: int8 to bf16 by byte permutes (below), into the stage's B operand; the
-//          last k-block of a group also clears the rows past its end in both operands, so
-//          that a neighbouring group's NaN cannot reach this one's sums
-//   10-13  epilogue: TMEM to registers, transposed through shared memory so that any
-//          alignment of dW is written in whole rows
+// Tile 256 (in) x 256 (out) per CTA pair (cta_group::2): each CTA restores its 128 columns of
+// X and loads its 128 columns of dY, so a restored element serves 256 output rows. Persistent,
+// one CTA per SM, warps:
+//   0      TMA producer: per 64-token k-block 16 KB of dY, 8 KB of q and 1 KB of exponents
+//          into a ring of 8 stages
+//   1      TMEM allocator and (first CTA) MMA issuer
+//   2-9    restore, two teams that take the k-blocks in turn; the last k-block of a group also
+//          clears the rows past its end in both operands, so that a neighbouring group's NaN
+//          cannot reach this one's sums
+//   10-17  epilogue: a lane is a column of dW's row, so the accumulator's registers are
+//          written in whole 128-byte rows at any alignment, without a transpose
+// Tensor memory: 256 columns of accumulator and 8 stages of X^T of 32 columns.
 // Split of the work: tiles are dealt to the 74 CTA pairs in whole rounds; the tiles left over
 // for the last round are split along the tokens into as many parts as keep all pairs busy,
 // whose fp32 partial sums a second kernel adds in order (no atomics).
@@ -41,24 +48,23 @@ namespace {
 
 constexpr int kTile = 256;                    // tile rows (out) and columns (in) of a CTA pair
 constexpr int kTok = 64;                      // tokens per k-block
-constexpr int kABytes = 128 * kTok * 2;       // a CTA's dY columns of one k-block
+constexpr int kYBytes = 128 * kTok * 2;       // a CTA's dY columns of one k-block
 constexpr int kQBytes = 128 * kTok;           // its stored X columns
-constexpr int kBBytes = 128 * kTok * 2;       // and the restored ones
 constexpr int kEBytesRow = 16;                // exponents of 512 columns, the smallest TMA row
 constexpr int kEBytes = kEBytesRow * kTok;
-constexpr int kOffE = kABytes + kQBytes + kBBytes;
+constexpr int kOffE = kYBytes + kQBytes;
 constexpr int kStageBytes = kOffE + kEBytes;
-constexpr int kStages = 5;
-constexpr int kTeams = 2, kTeamWarps = 4;  // restore teams take k-blocks in turn
-constexpr int kRestoreWarps = kTeams * kTeamWarps, kEpiWarps = 4;
+constexpr int kStages = 8;
+constexpr int kTeams = 2, kTeamWarps = 4;     // restore teams take k-blocks in turn
+constexpr int kRestoreWarps = kTeams * kTeamWarps, kEpiWarps = 8;
 constexpr int kFirstEpi = 2 + kRestoreWarps;
 constexpr int kThreads = 32 * (2 + kRestoreWarps + kEpiWarps);
-constexpr int kStgRow = 33;                   // padded row of the epilogue's transpose box
-constexpr int kStgBytes = kEpiWarps * 32 * kStgRow * 4;
-constexpr int kOffStg = kStages * kStageBytes;
-constexpr int kOffBar = kOffStg + kStgBytes;
+constexpr int kOffBar = kStages * kStageBytes;
 constexpr int kSmemBytes = kOffBar + 256 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kTmemX = 256;                   // first tensor-memory column of the X^T stages
+constexpr int kXCols = kTok / 2;              // columns of one stage
+static_assert(kTmemX + kStages * kXCols <= 512, "tensor memory");
 constexpr int kPairs = 74;                    // CTA pairs of a B200 (148 SMs)
 constexpr size_t kPartBytes = size_t(kTile) * kTile * 4;
 
@@ -159,38 +165,68 @@ __device__ __forceinline__ Job job_of(const WgradParams& P, int64_t u) {
   return j;
 }
 
-// 2^(byte - 127) in bf16, twice: byte 0 is a subnormal, byte 255 is NaN.
-__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t byte) {
-  const uint32_t s = byte == 255u ? 0x7FC0u : byte == 0u ? 0x0040u : byte << 7;
-  return s | (s << 16);
-}
-
-// Four int8 to bf16 times a power of two. Low 7 bits under the exponent of 128 give
-// 128 + low7, the sign bit there gives 128 or 256; their difference is the value, exactly.
-__device__ __forceinline__ void restore4(uint32_t w, uint32_t s2, uint32_t* lo, uint32_t* hi) {
+// Four int8 (tokens t .. t+3 of one column) to bf16 times their tokens' scales. Low 7 bits
+// under the exponent of 128 give 128 + low7, the sign bit there gives 128 or 256; their
+// difference is the value, exactly.
+__device__ __forceinline__ void restore4(uint32_t w, const uint32_t (&s)[2], uint32_t* lo, uint32_t* hi) {
   const uint32_t v = w & 0x7F7F7F7Fu, g = w & 0x80808080u, m = 0x43434343u;
   const uint32_t a0 = __byte_perm(v, m, 0x4140), a1 = __byte_perm(v, m, 0x4342);
   const uint32_t c0 = __byte_perm(g, m, 0x4140), c1 = __byte_perm(g, m, 0x4342);
   auto bf2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
-  const __nv_bfloat162 r0 = __hmul2(__hsub2(bf2(a0), bf2(c0)), bf2(s2));
-  const __nv_bfloat162 r1 = __hmul2(__hsub2(bf2(a1), bf2(c1)), bf2(s2));
+  const __nv_bfloat162 r0 = __hmul2(__hsub2(bf2(a0), bf2(c0)), bf2(s[0]));
+  const __nv_bfloat162 r1 = __hmul2(__hsub2(bf2(a1), bf2(c1)), bf2(s[1]));
   *lo = *reinterpret_cast<const uint32_t*>(&r0);
   *hi = *reinterpret_cast<const uint32_t*>(&r1);
+}
+
+// Two 16 x 16 byte matrices, transposed: lanes 0-15 and 16-31 give their rows' addresses.
+// Lane l gets of each matrix the rows 4 (l % 4) .. + 3 of column l / 4 and of column l / 4 + 8.
+__device__ __forceinline__ void ldmatrix_b8_x2_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// 16 lanes x 32 columns of tensor memory; register 4 n + i holds, for lane l of the warp,
+// column 8 n + 2 (l % 4) + (i & 1) of row l / 4 + 8 (i >> 1).
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D (both CTAs' tensor memory) (+)= A (both CTAs' tensor memory, M split) * B (both CTAs'
+// shared memory, N split)^T.
+__device__ __forceinline__ void umma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constant__ WgradParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* stg = reinterpret_cast<float*>(smem + kOffStg);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // this CTA's dY and q have landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // this CTA's loads have landed
   uint64_t* ready = full + kStages;   // first CTA's: both CTAs' operands are in place
   uint64_t* empty = ready + kStages;  // the MMAs have read the stage
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* done = tempty + 2;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(8 * (3 * kStages + 3) + 8 <= 256, "barrier region");
 
   const muon_weight_grad_t& a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -203,10 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       mbar_init(&ready[s], 2 * kTeamWarps);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kEpiWarps);
-    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * kEpiWarps);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -236,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
             break;
           }
           uint8_t* st = smem + s * kStageBytes;
-          const int t = j.t0 + kb * kTok, o = j.o0 + rank * 128;
-          mbar_expect_tx(&full[s], kABytes + kQBytes + kEBytes);
+          const int t = j.t0 + kb * kTok, o = j.o0 + rank * 128, i = j.i0 + rank * 128;
+          mbar_expect_tx(&full[s], kStageBytes);
+          tma_load_3d(st + kYBytes, &P.tq, &full[s], i, t, 0);
+          tma_load_3d(st + kOffE, &P.te, &full[s], i / 512 * kEBytesRow, t, 0);
           tma_load_3d(st, &P.ty, &full[s], o, t, 0);
-          tma_load_3d(st + kABytes / 2, &P.ty, &full[s], o + 64, t, 0);
-          tma_load_3d(st + kABytes, &P.tq, &full[s], j.i0 + rank * 128, t, 0);
-          tma_load_3d(st + kOffE, &P.te, &full[s], (j.i0 + rank * 128) / 512 * kEBytesRow, t, 0);
+          tma_load_3d(st + kYBytes / 2, &P.ty, &full[s], o + 64, t, 0);
           ++loads;
           if (++s == kStages) s = 0, par ^= 1u;
         }
@@ -257,42 +291,38 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(256, 256, true) | (1u << 15);  // A and B MN-major
+      const uint32_t idesc = idesc_bf16_f32(256, 256, true);  // A from tensor memory, B MN-major
       const uint64_t mn = smem_desc_sw128(0, 64 * kTok * 2, 1024);
-      int s = 0, it = 0;
-      uint32_t par = 0;
+      int s = 0;
+      uint32_t par = 0, tpar = 0;
       bool ok = true;
       for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
         const Job j = job_of(P, u);
         if (j.nkb == 0) continue;
-        const int ab = it & 1;
-        const uint32_t apar = static_cast<uint32_t>((it >> 1) & 1);
-        ++it;
-        if (!mbar_wait(&tempty[ab], apar ^ 1u, abort_flag)) {
+        if (!mbar_wait(tempty, tpar ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
+        tpar ^= 1u;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(ab * 256);
         for (int kb = 0; kb < j.nkb; ++kb) {
           if (!mbar_wait(&ready[s], par, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kABytes + kQBytes;
-          const uint64_t ad = mn | static_cast<uint64_t>((sa >> 4) & 0x3FFFu);
-          const uint64_t bd = mn | static_cast<uint64_t>((sb >> 4) & 0x3FFFu);
+          const uint64_t bd = mn | static_cast<uint64_t>((smem_u32(smem + s * kStageBytes) >> 4) & 0x3FFFu);
+          const uint32_t at = tmem + kTmemX + s * kXCols;
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens are 2 KB of a chunk
-            umma_f16_pair(d, ad + 128u * kk, bd + 128u * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
+          for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens: 8 columns, 2 KB of a chunk
+            umma_f16_pair_ts(tmem, at + 8u * kk, bd + 128u * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
           umma_commit_pair(smem_u32(&empty[s]));
           umma_commit_pair(peer_addr(&empty[s], 1));
           if (++s == kStages) s = 0, par ^= 1u;
         }
         if (!ok) break;
-        umma_commit_pair(smem_u32(&tfull[ab]));
-        umma_commit_pair(peer_addr(&tfull[ab], 1));
+        umma_commit_pair(smem_u32(tfull));
+        umma_commit_pair(peer_addr(tfull, 1));
       }
       if (!ok) {
         set_error(a.status_dev, MUON_ERR_TIMEOUT);
@@ -303,21 +333,18 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     }
   } else if (warp < kFirstEpi) {
     // ------------------------------------------------------------ restore
-    // Two teams of four warps take the k-blocks in turn, so that a team has the time of two
-    // k-blocks for its loads, fence and signal. Warp w of a team owns tokens 16w .. 16w+15. A
-    // quarter warp reads 64 bytes of token p and of token p ^ 5: with both layouts swizzled by
-    // the token's low 3 bits, its 16-byte reads of q and its 16-byte writes of bf16 then touch
-    // all 32 banks.
-    const int team = (warp - 2) / kTeamWarps, w = (warp - 2) % kTeamWarps;
-    const int p = lane >> 3, tok = 16 * w + ((lane & 4) ? p ^ 5 : p), pc = lane & 3;
+    // A team's warp owns the 32 columns of X of its tensor-memory lane quarter: one group of
+    // the checkpoint. Its exponents go through ldmatrix as well: row g of the transposed
+    // exponent tile holds group g, whose bytes a shuffle hands to the lanes of their tokens.
+    const int team = (warp - 2) / kTeamWarps, w = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     int64_t q0 = 0;  // k-blocks of the units before this one
     bool ok = true;
     for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
       const Job j = job_of(P, u);
-      // the team's k-blocks of this unit: the pair's k-blocks q0 + kb with its parity
-      int kb = static_cast<int>((team - q0) & 1);
-      const int sel = (j.i0 + rank * 128) / 32 % kEBytesRow;  // its exponents within a stage's row
-      for (; kb < j.nkb; kb += kTeams) {
+      const int grp = ((j.i0 + rank * 128) / 32 + w) % kEBytesRow;  // within a stage's exponent row
+      const int src = (grp & 7) * 4 + (lane & 3);
+      for (int kb = static_cast<int>((team - q0) & 1); kb < j.nkb; kb += kTeams) {
         const int64_t q = q0 + kb;
         const int s = static_cast<int>(q % kStages);
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], static_cast<uint32_t>((q / kStages) & 1), abort_flag))) {
@@ -329,36 +356,50 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           break;
         }
         uint8_t* st = smem + s * kStageBytes;
-        uint4 v[4];
-        uint32_t e[2];  // exponents of the 128 columns for each of the thread's two tokens
+        const int live = j.t1 - (j.t0 + kb * kTok);  // tokens of the group from this k-block on
+        uint32_t sc[4][2];  // scales of tokens 16 b + 4 (lane % 4) + {0, 1}, {2, 3}
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          e[i] = *reinterpret_cast<const uint32_t*>(st + kOffE + (tok + 8 * i) * kEBytesRow + sel);
+        for (int b = 0; b < 4; b += 2) {
+          uint32_t e[4];
+          ldmatrix_b8_x2_trans(smem_u32(st + kOffE + (16 * b + lane) * kEBytesRow), e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // token 8 (i / 2) further, columns 64 (i % 2) further
-          v[i] = *reinterpret_cast<const uint4*>(st + kABytes + (tok + 4 * (i & 2)) * 128 +
-                                                 (((4 * (i & 1) + pc) ^ (tok & 7)) << 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int h = i & 1, tk = tok + 4 * (i & 2);
-          const bool live = j.t0 + kb * kTok + tk < j.t1;
-          const uint32_t sc = scale_bf16x2((e[i >> 1] >> (8 * (2 * h + (pc >> 1)))) & 0xFFu);
-          uint4 x0, x1;
-          restore4(v[i].x, sc, &x0.x, &x0.y);
-          restore4(v[i].y, sc, &x0.z, &x0.w);
-          restore4(v[i].z, sc, &x1.x, &x1.y);
-          restore4(v[i].w, sc, &x1.z, &x1.w);
-          if (!live) x0 = x1 = make_uint4(0, 0, 0, 0);
-          uint8_t* row = st + kABytes + kQBytes + h * (64 * kTok * 2) + tk * 128;
-          *reinterpret_cast<uint4*>(row + (((2 * pc) ^ (tok & 7)) << 4)) = x0;
-          *reinterpret_cast<uint4*>(row + (((2 * pc + 1) ^ (tok & 7)) << 4)) = x1;
-          if (!live) {  // the dY of tokens past the group: zeros too
-            uint8_t* y = st + h * (64 * kTok * 2) + tk * 128 + 32 * pc;
-            *reinterpret_cast<uint4*>(y) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(y + 16) = make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x0 = __shfl_sync(0xffffffffu, e[2 * h], src), x1 = __shfl_sync(0xffffffffu, e[2 * h + 1], src);
+            const uint32_t x = grp < 8 ? x0 : x1;
+            sc[b + h][0] = __byte_perm(x, 0, 0x4140) << 7;
+            sc[b + h][1] = __byte_perm(x, 0, 0x4342) << 7;
           }
         }
-        fence_proxy_async_smem();
+        if (live < kTok) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int t = 16 * b + 4 * (lane & 3) + 2 * h;
+              sc[b][h] &= (t < live ? 0xFFFFu : 0u) | (t + 1 < live ? 0xFFFF0000u : 0u);
+            }
+          // the dY of tokens past the group: zeros too
+          for (int t = live + w; t < kTok; t += kTeamWarps)
+            *reinterpret_cast<uint2*>(st + (lane >> 4) * (kYBytes / 2) + t * 128 + (lane & 15) * 8) = make_uint2(0, 0);
+          fence_proxy_async_smem();
+        }
+        uint32_t x[2][16];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int t = 16 * b + (lane & 15);
+          uint32_t v[4];
+          ldmatrix_b8_x2_trans(smem_u32(st + kYBytes + t * 128 + (((2 * w + (lane >> 4)) ^ (t & 7)) << 4)), v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            restore4(v[2 * h], sc[b], &x[h][4 * b], &x[h][4 * b + 1]);
+            restore4(v[2 * h + 1], sc[b], &x[h][4 * b + 2], &x[h][4 * b + 3]);
+          }
+        }
+        const uint32_t at = tmem + kTmemX + s * kXCols + lanes;
+        tmem_st_16x256b_x4(at, x[0]);
+        tmem_st_16x256b_x4(at + (16u << 16), x[1]);
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (rank == 0) mbar_arrive(&ready[s]);
@@ -369,18 +410,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3;  // the TMEM lane quarter this warp may access
-    float* box = stg + (warp - kFirstEpi) * 32 * kStgRow;
-    int it = 0;
+    const int w = warp & 3;                          // the TMEM lane quarter this warp may access
+    const int half = (warp - kFirstEpi) / 4 * 128;   // and its half of the tile's rows of dW
+    uint32_t tpar = 0;
     bool ok = true;
     for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
       const Job j = job_of(P, u);
       if (j.nkb == 0 && (j.part >= 0 || a.accumulate)) continue;
-      const int ab = it & 1;
       if (j.nkb > 0) {
-        const uint32_t apar = static_cast<uint32_t>((it >> 1) & 1);
-        ++it;
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[ab], apar, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(tfull, tpar, abort_flag))) {
           ok = false;
           if (lane == 0) {
             set_error(a.status_dev, MUON_ERR_TIMEOUT);
@@ -388,55 +426,64 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           }
           break;
         }
+        tpar ^= 1u;
         tc_fence_after();
       }
-      const int r0 = rank * 128 + quad * 32;                    // first tile row of this warp
-      const int nrow = min(32, static_cast<int>(a.out) - j.o0 - r0);
+      const int c0 = rank * 128 + w * 32 + lane, col = j.i0 + c0;
+      const int rows = min(128, static_cast<int>(a.out) - j.o0 - half);
 #pragma unroll 1
-      for (int c = 0; c < kTile / 32; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
         if (j.nkb > 0) {
-          tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(ab * 256 + c * 32), v);
+          tmem_ld32(tmem + (static_cast<uint32_t>(w * 32) << 16) + static_cast<uint32_t>(half + c * 32), v);
           tmem_wait_ld();
-          if (c == kTile / 32 - 1) {
+          if (c == 3) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              if (rank == 0) mbar_arrive(&tempty[ab]);
-              else mbar_arrive_cluster(peer_addr(&tempty[ab], 0));
+              if (rank == 0) mbar_arrive(tempty);
+              else mbar_arrive_peer(peer_addr(tempty, 0));
             }
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
+        if (col >= a.in) continue;
+        const int n = rows - c * 32;
+        if (j.part >= 0) {
+          float* p = P.parts + static_cast<int64_t>(j.part) * (kTile * kTile) + (half + c * 32) * kTile + c0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) box[lane * kStgRow + i] = __uint_as_float(v[i]);
-        __syncwarp();
-        const int col = j.i0 + c * 32 + lane;
-        if (col < a.in) {
-          if (j.part >= 0) {
-            float* p = P.parts + static_cast<int64_t>(j.part) * (kTile * kTile) + r0 * kTile + c * 32 + lane;
-            for (int r = 0; r < nrow; ++r) p[r * kTile] = box[r * kStgRow + lane];
-          } else {
-            const int64_t at = j.g * a.stride_w + (j.o0 + r0) * a.ld_w + col;
-            if (a.w_dtype == MUON_F32) {
-              float* p = static_cast<float*>(a.dW) + at;
-              if (a.accumulate)
-                for (int r = 0; r < nrow; ++r) p[r * a.ld_w] += box[r * kStgRow + lane];
-              else
-                for (int r = 0; r < nrow; ++r) p[r * a.ld_w] = box[r * kStgRow + lane];
-            } else {
-              uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
-              if (a.accumulate)
-                for (int r = 0; r < nrow; ++r)
-                  p[r * a.ld_w] = f32_to_bf16(bf16_to_f32(p[r * a.ld_w]) + box[r * kStgRow + lane]);
-              else
-                for (int r = 0; r < nrow; ++r) p[r * a.ld_w] = f32_to_bf16(box[r * kStgRow + lane]);
+          for (int i = 0; i < 32; ++i)
+            if (i < n) p[i * kTile] = __uint_as_float(v[i]);
+        } else {
+          const int64_t at = j.g * a.stride_w + (j.o0 + half + c * 32) * a.ld_w + col;
+          if (a.w_dtype == MUON_F32) {
+            float* p = static_cast<float*>(a.dW) + at;
+            if (a.accumulate) {
+              float old[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) old[i] = i < n ? p[i * a.ld_w] : 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + old[i]);
             }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < n) p[i * a.ld_w] = __uint_as_float(v[i]);
+          } else {
+            uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
+            if (a.accumulate) {
+              uint16_t old[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) old[i] = i < n ? p[i * a.ld_w] : 0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + bf16_to_f32(old[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < n) p[i * a.ld_w] = f32_to_bf16(__uint_as_float(v[i]));
           }
         }
-        __syncwarp();
       }
     }
   }

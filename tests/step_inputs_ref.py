@@ -30,7 +30,8 @@ def store(x):
 def restore(q, byte):
     """Restored values in float64."""
     q, byte = q.double().cpu(), byte.cpu().double()
-    s = torch.where(byte == 255, torch.full_like(byte, math.nan), torch.exp2(byte - 127))
+    s = torch.where(byte == 255, torch.full_like(byte, math.inf), torch.exp2(byte - 127))
+    s = torch.where(byte == 0, torch.zeros_like(byte), s)
     return q * s.repeat_interleave(32, 1)[:, :q.shape[1]]
 
 
