@@ -14,17 +14,6 @@
 namespace muon {
 namespace {
 
-__device__ __forceinline__ float warp_max(float v) {
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-// Raises *p to v; the bit patterns of positive floats order as integers, of negative ones
-// in reverse as unsigned integers. The maximum does not depend on the order of the calls.
-__device__ __forceinline__ void atomic_max_float(float* p, float v) {
-  if (v >= 0.f) atomicMax(reinterpret_cast<int*>(p), __float_as_int(v));
-  else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
-}
-
 // The sequence of a row, or -1.
 __device__ int row_seq(const int32_t* off, int n_seq, int32_t tokens, int row) {
   if (off == nullptr) return 0;
@@ -45,34 +34,6 @@ __device__ __forceinline__ void load_row(const uint16_t* p, int d, int lane, flo
 }
 __device__ __forceinline__ float dot(const float (&x)[4], const float (&y)[4]) {
   return warp_sum(x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3]);
-}
-
-__global__ void attention_simple_kernel(const __grid_constant__ muon_attention_t a) {
-  const int lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
-  if (i >= a.q_tokens) return;
-  const int s = row_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), i);
-  if (s < 0) return;
-  const SeqRange r = seq_range(a, s);
-  const int kh = h / (a.heads / a.kv_heads);
-  const int vis = a.causal ? min(r.n, i - r.q0 + r.n - r.m + 1) : r.n;
-  float q[4], acc[4] = {}, m = -INFINITY, l = 0.f;
-  load_row(at(a.q, i, h), a.head_dim, lane, q);
-  for (int j = 0; j < vis; ++j) {
-    float k[4], v[4];
-    load_row(at(a.k, r.k0 + j, kh), a.head_dim, lane, k);
-    load_row(at(a.v, r.k0 + j, kh), a.head_dim, lane, v);
-    const float x = dot(q, k) * a.scale, mn = fmaxf(m, x);
-    const float c = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
-    l = l * c + p;
-    for (int e = 0; e < 4; ++e) acc[e] = acc[e] * c + p * v[e];
-    m = mn;
-  }
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < a.head_dim) at_w(a.o, i, h)[lane + 32 * e] = f32_to_bf16(vis > 0 ? acc[e] / l : 0.f);
-  if (lane == 0) {
-    a.lse[h * a.q_tokens + i] = vis > 0 ? m + logf(l) : -INFINITY;
-    if (a.s_max != nullptr && vis > 0) atomic_max_float(a.s_max + h, m);
-  }
 }
 
 __global__ void attention_dq_simple_kernel(const __grid_constant__ muon_attention_t a, float* delta) {
@@ -235,8 +196,7 @@ extern "C" MUON_API muon_status_t muon_attention_forward(const muon_attention_t*
   int dev = 0, sms = 0;
   const muon_status_t d = current_device(&dev, &sms);
   if (d != MUON_OK) return d;
-  attention_simple_kernel<<<dim3((a->q_tokens + 3) / 4, a->heads), 128, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return launch_attention_forward(*a, dev, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 extern "C" MUON_API size_t muon_attention_workspace_size(const muon_attention_t* a) {

@@ -57,8 +57,15 @@ __device__ __forceinline__ int tile_seq(const int32_t* off, int n_seq, int32_t t
   return lo;
 }
 
+// Tensor map of tokens x heads x head_dim, boxes of 64 columns of one head x `rows` tokens
+// (128B swizzle; columns past head_dim and tokens past the tensor read as zeros). Without
+// tokens the map is left alone and must not be used.
+bool encode_heads_map(CUtensorMap* out, const muon_heads_t& t, int64_t tokens, int heads, int dim, int rows);
+
 inline int64_t tile_slots(const int32_t* off, int n_seq, int64_t tokens, int rows) {
   return off == nullptr ? (tokens + rows - 1) / rows : tokens / rows + n_seq;
 }
+
+cudaError_t launch_attention_forward(const muon_attention_t& a, int dev, cudaStream_t st);
 
 }  // namespace muon

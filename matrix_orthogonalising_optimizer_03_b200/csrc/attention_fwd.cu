@@ -1,0 +1,409 @@
+// Forward pass of softmax attention over packed sequences, with the log-sum-exp of every row
+// and the largest logit of every head (muon_attention_forward).
+//
+// One pass over the keys with a running maximum and sum per row. A CTA owns 256 query rows of
+// one head as two tiles of 128, whose softmax and products alternate on the tensor core:
+//   S_i = Q_i K^T (128 x 128, fp32 in tensor memory), P = exp2(S scale log2 e - m) as bf16 over
+//   the same columns, O_i += P V with P as the tensor-memory operand
+// Warps: 0 TMA producer (Q once, then K and V blocks of 128 keys through a ring), 1 TMEM
+// allocator and MMA issuer, 4-7 and 8-11 the softmax of tile 0 and 1, one thread per row. While
+// one tile's softmax runs, the other tile's products do.
+// m is the row's running maximum, moved only when a block exceeds it by more than 2^8 in the
+// exponent: until then P stays below 2^8 and nothing overflows (fp32 sums, bf16 P), and the
+// accumulator, which a thread would have to read and write back, is left alone. P is rounded
+// to bf16 for the product (relative 2^-9 on average errors of either sign); the row's sum
+// adds the unrounded values.
+// Bound by the exponentials: 16 per cycle and SM, 2048 cycles for a block of both tiles, as
+// many as the products of head dimension 128 take (1024 for 64).
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "attention.h"
+#include "muon.h"
+#include "ns_tc.h"
+#include "ptx.cuh"
+
+namespace muon {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+bool encode_heads_map(CUtensorMap* out, const muon_heads_t& t, int64_t tokens, int heads, int dim, int rows) {
+  if (tokens == 0) return true;
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  // strides of axes of one element are never used, and may be anything
+  const int64_t head = heads > 1 ? t.head : dim, ld = tokens > 1 ? t.ld : dim;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head) * 2, static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.ptr, dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int kRows = 128;          // query rows of a tile, and keys of a block
+constexpr int kThreads = 384;
+constexpr int kChunk = kRows * 128; // bytes of 64 columns of a tile
+constexpr float kLazy = 8.f;        // the running maximum moves when exceeded by this (log2)
+
+template <int HD>
+struct FwdCfg {
+  static constexpr int kTileBytes = kRows * HD * 2;
+  static constexpr int kStages = HD == 128 ? 4 : 8;   // K and V blocks in flight
+  static constexpr int kOffKv = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static constexpr int kO = 256;                      // first accumulator column
+};
+
+struct FwdParams {
+  CUtensorMap tq, tk, tv;
+  muon_attention_t a;
+};
+
+// Raises *p to v: positive floats order as integers, negative ones in reverse as unsigned.
+// The result does not depend on the order of the calls; NaN changes nothing.
+__device__ __forceinline__ void atomic_max_float(float* p, float v) {
+  if (v >= 0.f) atomicMax(reinterpret_cast<int*>(p), __float_as_int(v));
+  else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int HD>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
+  mbar_expect_tx(bar, FwdCfg<HD>::kTileBytes);
+#pragma unroll
+  for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * kChunk, map, bar, c * 64, head, token);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid_constant__ FwdParams P) {
+  using C = FwdCfg<HD>;
+  const muon_attention_t& a = P.a;
+  const int heads = a.heads;
+  const int head = static_cast<int>(blockIdx.x % heads);
+  // later rows see more keys: the long tiles of a causal sequence start first
+  const int slot = static_cast<int>(gridDim.x / heads - 1 - blockIdx.x / heads);
+  int row0;
+  const SeqRange r = seq_range(a, tile_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), 2 * kRows, slot, &row0));
+  if (row0 >= r.m) return;
+  const int shift = r.n - r.m;  // causal: row i sees keys j <= i + shift
+  auto blocks_of = [&](int i) {  // key blocks of tile i
+    const int first = row0 + i * kRows, last = min(first + kRows, r.m) - 1;
+    const int keys = first >= r.m ? 0 : a.causal ? min(r.n, last + shift + 1) : r.n;
+    return keys > 0 ? (keys + kRows - 1) / kRows : 0;
+  };
+  const int nb0 = blocks_of(0), nb1 = blocks_of(1), nmax = max(nb0, nb1);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // ring: K0, V0, K1, V1, ...
+  uint64_t* empty = full + C::kStages;
+  uint64_t* q_full = empty + C::kStages;
+  uint64_t* s_full = q_full + 1;   // per tile: S is complete (and the product before it)
+  uint64_t* p_full = s_full + 2;   // per tile: P is in place, S has been read
+  uint64_t* o_full = p_full + 2;   // per tile: the last product is complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(8 * (2 * C::kStages + 7) + 8 <= 256, "barrier region");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Registers: 384 x 168 at launch; 128 x 56 + 256 x 224 is the same total.
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0 && nmax > 0) {
+      const int kvh = head / (heads / a.kv_heads);
+      mbar_expect_tx(q_full, 2 * C::kTileBytes);
+      for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(smem + i * C::kTileBytes + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
+      bool ok = true;
+      int loads = 0;
+      for (int t = 0; t < 2 * nmax; ++t) {
+        const int s = t % C::kStages;
+        if (!mbar_wait(&empty[s], static_cast<uint32_t>((t / C::kStages) & 1) ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        load_tile<HD>(smem + C::kOffKv + s * C::kTileBytes, (t & 1) ? &P.tv : &P.tk, &full[s], kvh,
+                      r.k0 + (t >> 1) * kRows);
+        ++loads;
+      }
+      if (!ok) {
+        set_error(a.status_dev, MUON_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // never leave with bulk copies still landing in shared memory
+      mbar_wait(q_full, 0, nullptr);
+      for (int t = loads > C::kStages ? loads - C::kStages : 0; t < loads; ++t)
+        mbar_wait(&full[t % C::kStages], static_cast<uint32_t>((t / C::kStages) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (nmax > 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, HD, true);
+      const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), mn = smem_desc_sw128(0, kChunk, 1024);
+      auto ring = [&](int t) { return smem_u32(smem + C::kOffKv + (t % C::kStages) * C::kTileBytes); };
+      auto wait_ring = [&](int t) {
+        return __all_sync(0xffffffffu, mbar_wait(&full[t % C::kStages], static_cast<uint32_t>((t / C::kStages) & 1), abort_flag));
+      };
+      auto qk = [&](int i, int j) {  // S_i = Q_i K_j^T
+        if (lane == 0) {
+          const uint64_t qd = kmaj | ((smem_u32(smem + i * C::kTileBytes) >> 4) & 0x3FFFu);
+          const uint64_t kd = kmaj | ((ring(2 * j) >> 4) & 0x3FFFu);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint64_t off = static_cast<uint64_t>((k >> 2) * (kChunk >> 4) + (k & 3) * 2);
+            umma_f16(tmem + i * kRows, qd + off, kd + off, idesc_s, k != 0);
+          }
+          umma_commit(&s_full[i]);
+        }
+      };
+      bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag)) && wait_ring(0);
+      if (ok) {
+        tc_fence_after();
+        if (nb0 > 0) qk(0, 0);
+        if (nb1 > 0) qk(1, 0);
+        if (lane == 0) umma_commit(&empty[0]);
+      }
+      for (int j = 0; j < nmax && ok; ++j) {
+        const int tv = 2 * j + 1, tk = 2 * j + 2;
+        ok = wait_ring(tv);
+        if (!ok) break;
+        const int live = r.n - j * kRows;
+        if (live < kRows) {
+          // keys past the sequence: their probabilities are 0, and their V must not be NaN
+          uint8_t* v = smem + C::kOffKv + (tv % C::kStages) * C::kTileBytes;
+          for (int t = live * 8 + lane; t < kRows * 8; t += 32)
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+              *reinterpret_cast<uint4*>(v + c * kChunk + t * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        for (int i = 0; i < 2 && ok; ++i) {
+          const int nbi = i == 0 ? nb0 : nb1;
+          if (j < nbi) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&p_full[i], static_cast<uint32_t>(j & 1), abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {  // O_i += P_i V_j
+              const uint64_t vd = mn | ((ring(tv) >> 4) & 0x3FFFu);
+#pragma unroll
+              for (int k = 0; k < kRows / 16; ++k)
+                umma_f16_ts(tmem + C::kO + i * HD, tmem + i * kRows + k * 8, vd + 128u * k, idesc_o, (j | k) != 0);
+              if (j + 1 == nbi) umma_commit(&o_full[i]);
+            }
+          }
+          if (i == 1 && lane == 0) umma_commit(&empty[tv % C::kStages]);
+          if (j + 1 < nmax && i == 0) ok = wait_ring(tk);
+          if (ok && j + 1 < nbi) qk(i, j + 1);
+          if (ok && j + 1 < nmax && i == 1 && lane == 0) umma_commit(&empty[tk % C::kStages]);
+        }
+      }
+      if (!ok && lane == 0) {
+        set_error(a.status_dev, MUON_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax, one thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int i = (warp - 4) / 4, w = warp & 3, nbi = i == 0 ? nb0 : nb1;
+    const int row = row0 + i * kRows + w * 32 + lane;  // within the sequence
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * kRows, to = tmem + lanes + C::kO + i * HD;
+    const float sl = a.scale * 1.4426950408889634f;
+    float top = -INFINITY;            // largest logit so far, unscaled
+    float ref = 0.f;                  // the exponent's reference, scaled
+    float sum = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nbi; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[i], static_cast<uint32_t>(j & 1), abort_flag))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
+      tmem_wait_ld();
+      // keys of this block that the row sees
+      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows;
+      if (__any_sync(0xffffffffu, vis < kRows)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= vis) s[c][e] = 0xFF800000u;
+      }
+      float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m[c] = fmaxf(m[c], __uint_as_float(s[c][e]));
+      top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+      const float want = top == -INFINITY ? 0.f : top * sl;
+      if (j == 0) {
+        ref = want;
+      } else {
+        // a row that sees any key sees the first, so ref is a maximum from block 0 on
+        const bool move = want > ref + kLazy;
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? ex2(ref - want) : 1.f;
+          if (move) ref = want;
+          sum *= f;
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(to + c * 32, o);
+          }
+        }
+      }
+      float add[4] = {sum, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = 2 * h + (e >> 4), k = 2 * (e & 15);
+          const float p0 = ex2(fmaf(__uint_as_float(s[c][k]), sl, -ref));
+          const float p1 = ex2(fmaf(__uint_as_float(s[c][k + 1]), sl, -ref));
+          add[2 * (e & 1)] += p0;
+          add[2 * (e & 1) + 1] += p1;
+          pk[e] = pack_bf16x2(p0, p1);
+        }
+        tmem_st32(ts + h * 32, pk);
+      }
+      sum = (add[0] + add[1]) + (add[2] + add[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i]);
+    }
+    if (!ok && lane == 0) {
+      set_error(a.status_dev, MUON_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (nbi > 0 && ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, abort_flag));
+      if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
+      tc_fence_after();
+    }
+    const bool live = row < r.m, seen = top > -INFINITY || sum != 0.f;
+    const float inv = seen ? 1.f / sum : 0.f;
+    uint16_t* out = static_cast<uint16_t*>(a.o.ptr) + static_cast<int64_t>(r.q0 + row) * a.o.ld + head * a.o.head;
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) {
+      uint32_t o[32];
+      if (nbi > 0) {
+        tmem_ld32(to + c * 32, o);
+        tmem_wait_ld();
+      }
+      if (!seen || nbi == 0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          pk[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+        if (live && ok && c * 32 + e < a.head_dim)
+          *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+    }
+    if (live && ok)
+      a.lse[static_cast<int64_t>(head) * a.q_tokens + r.q0 + row] =
+          seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (a.s_max != nullptr) {
+      float best = live && ok ? top : -INFINITY;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      if (lane == 0 && best > -INFINITY) atomic_max_float(a.s_max + head, best * a.scale);
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+cudaError_t launch(const FwdParams& P, int dev, int64_t grid, cudaStream_t st) {
+  // the shared-memory opt-in is a per-device attribute: set it once on each device
+  static std::atomic<uint64_t> attr_devices{0};
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(attention_fwd_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               FwdCfg<HD>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_devices.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  attention_fwd_kernel<HD><<<static_cast<unsigned>(grid), kThreads, FwdCfg<HD>::kSmemBytes, st>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_forward(const muon_attention_t& a, int dev, cudaStream_t st) {
+  FwdParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.a = a;
+  if (!encode_heads_map(&P.tq, a.q, a.q_tokens, a.heads, a.head_dim, kRows) ||
+      !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, kRows) ||
+      !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, kRows))
+    return cudaErrorInvalidValue;
+  const int64_t grid = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, 2 * kRows) * a.heads;
+  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  return a.head_dim <= 64 ? launch<64>(P, dev, grid, st) : launch<128>(P, dev, grid, st);
+}
+
+}  // namespace muon
