@@ -10,6 +10,13 @@ namespace muon {
 // Host checks of an attention call (no CUDA call); backward: the gradients' tensors too.
 muon_status_t validate_attention(const muon_attention_t* a, bool backward);
 
+// Two fp32 values rounded to bf16, the first in the low half, in one instruction.
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // One sequence's rows and keys, clamped to the tensors.
 struct SeqRange {
   int32_t q0, m;  // first query row, queries

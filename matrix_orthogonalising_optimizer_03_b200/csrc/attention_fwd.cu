@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           const float p1 = ex2(fmaf(__uint_as_float(s[c][k + 1]), sl, -ref));
           add[2 * (e & 1)] += p0;
           add[2 * (e & 1) + 1] += p1;
-          pk[e] = pack_bf16x2(p0, p1);
+          pk[e] = round_bf16x2(p0, p1);
         }
         tmem_st32(ts + h * 32, pk);
       }
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         uint32_t pk[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          pk[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+          pk[k] = round_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
         if (live && ok && c * 32 + e < a.head_dim)
           *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
