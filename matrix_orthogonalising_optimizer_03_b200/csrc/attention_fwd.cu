@@ -63,6 +63,11 @@ struct FwdCfg {
   static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
   static constexpr int kO = 256;                      // first accumulator column
+  // Head dimension 64 leaves 128 columns for P of its own, so that S is free for the next
+  // product as soon as it has been read; with 128, P lies over the first half of S.
+  static constexpr bool kOwnP = HD == 64;
+  static constexpr int kP = kOwnP ? kO + 2 * HD : 0;  // P of tile 0
+  static constexpr int kPStep = kOwnP ? 64 : kRows;   // to P of tile 1
 };
 
 struct FwdParams {
@@ -81,6 +86,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 
 template <int HD>
@@ -112,15 +123,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // ring: K0, V0, K1, V1, ...
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // ring of K and V blocks
   uint64_t* empty = full + C::kStages;
   uint64_t* q_full = empty + C::kStages;
   uint64_t* s_full = q_full + 1;   // per tile: S is complete (and the product before it)
-  uint64_t* p_full = s_full + 2;   // per tile: P is in place, S has been read
-  uint64_t* o_full = p_full + 2;   // per tile: the last product is complete
+  uint64_t* s_read = s_full + 2;   // per tile: S is in registers
+  uint64_t* p_full = s_read + 2;   // per tile and half: P of 64 keys is in place
+  uint64_t* o_full = p_full + 4;   // per tile: the product with V is complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (2 * C::kStages + 7) + 8 <= 256, "barrier region");
+  static_assert(8 * (2 * C::kStages + 11) + 8 <= 256, "barrier region");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -131,7 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&s_read[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
     *abort_flag = 0;
@@ -164,8 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           ok = false;
           break;
         }
-        load_tile<HD>(smem + C::kOffKv + s * C::kTileBytes, (t & 1) ? &P.tv : &P.tk, &full[s], kvh,
-                      r.k0 + (t >> 1) * kRows);
+        const bool is_v = C::kOwnP ? (t > 0 && (t & 1) == 0) || t == 2 * nmax - 1 : (t & 1) != 0;
+        const int j = !C::kOwnP ? t >> 1 : is_v ? (t == 2 * nmax - 1 ? nmax - 1 : t / 2 - 1) : (t + 1) / 2;
+        load_tile<HD>(smem + C::kOffKv + s * C::kTileBytes, is_v ? &P.tv : &P.tk, &full[s], kvh, r.k0 + j * kRows);
         ++loads;
       }
       if (!ok) {
@@ -182,14 +197,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     if (nmax > 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, HD, true);
       const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), mn = smem_desc_sw128(0, kChunk, 1024);
-      auto ring = [&](int t) { return smem_u32(smem + C::kOffKv + (t % C::kStages) * C::kTileBytes); };
-      auto wait_ring = [&](int t) {
-        return __all_sync(0xffffffffu, mbar_wait(&full[t % C::kStages], static_cast<uint32_t>((t / C::kStages) & 1), abort_flag));
+      // Ring positions, in the order of use. Own P: the next block's S is computed while this
+      // block's softmax runs, so K_{j+1} comes before V_j.
+      auto pos_k = [&](int j) { return C::kOwnP ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
+      auto pos_v = [&](int j) { return C::kOwnP ? (j + 1 < nmax ? 2 * j + 2 : 2 * nmax - 1) : 2 * j + 1; };
+      auto ring = [&](int t) { return smem + C::kOffKv + (t % C::kStages) * C::kTileBytes; };
+      auto wait_bar = [&](uint64_t* bar, int phase) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag));
+        tc_fence_after();
+        return got;
+      };
+      auto wait_ring = [&](int t) { return wait_bar(&full[t % C::kStages], t / C::kStages); };
+      auto free_ring = [&](int t) {
+        if (elect_one()) umma_commit(&empty[t % C::kStages]);
       };
       auto qk = [&](int i, int j) {  // S_i = Q_i K_j^T
-        if (lane == 0) {
+        if (elect_one()) {
           const uint64_t qd = kmaj | ((smem_u32(smem + i * C::kTileBytes) >> 4) & 0x3FFFu);
-          const uint64_t kd = kmaj | ((ring(2 * j) >> 4) & 0x3FFFu);
+          const uint64_t kd = kmaj | ((smem_u32(ring(pos_k(j))) >> 4) & 0x3FFFu);
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
             const uint64_t off = static_cast<uint64_t>((k >> 2) * (kChunk >> 4) + (k & 3) * 2);
@@ -198,21 +223,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           umma_commit(&s_full[i]);
         }
       };
-      bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag)) && wait_ring(0);
-      if (ok) {
-        tc_fence_after();
-        if (nb0 > 0) qk(0, 0);
-        if (nb1 > 0) qk(1, 0);
-        if (lane == 0) umma_commit(&empty[0]);
-      }
-      for (int j = 0; j < nmax && ok; ++j) {
-        const int tv = 2 * j + 1, tk = 2 * j + 2;
-        ok = wait_ring(tv);
-        if (!ok) break;
+      auto pv = [&](int i, int j) {  // O_i += P_i V_j, by halves of the keys as P arrives
+        bool got = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          got = got && wait_bar(&p_full[2 * i + h], j);
+          if (got && elect_one()) {
+            const uint64_t vd = mn | ((smem_u32(ring(pos_v(j))) >> 4) & 0x3FFFu);
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              umma_f16_ts(tmem + C::kO + i * HD, tmem + C::kP + i * C::kPStep + k * 8, vd + 128u * k, idesc_o, (j | k) != 0);
+            if (h == 1) umma_commit(&o_full[i]);
+          }
+        }
+        return got;
+      };
+      // V_j has landed; keys past the sequence have probability 0, and their V must not be NaN
+      auto take_v = [&](int j) {
+        if (!wait_ring(pos_v(j))) return false;
         const int live = r.n - j * kRows;
         if (live < kRows) {
-          // keys past the sequence: their probabilities are 0, and their V must not be NaN
-          uint8_t* v = smem + C::kOffKv + (tv % C::kStages) * C::kTileBytes;
+          uint8_t* v = ring(pos_v(j));
           for (int t = live * 8 + lane; t < kRows * 8; t += 32)
 #pragma unroll
             for (int c = 0; c < HD / 64; ++c)
@@ -220,29 +251,48 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           fence_proxy_async_smem();
           __syncwarp();
         }
-        for (int i = 0; i < 2 && ok; ++i) {
-          const int nbi = i == 0 ? nb0 : nb1;
-          if (j < nbi) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&p_full[i], static_cast<uint32_t>(j & 1), abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {  // O_i += P_i V_j
-              const uint64_t vd = mn | ((ring(tv) >> 4) & 0x3FFFu);
-#pragma unroll
-              for (int k = 0; k < kRows / 16; ++k)
-                umma_f16_ts(tmem + C::kO + i * HD, tmem + i * kRows + k * 8, vd + 128u * k, idesc_o, (j | k) != 0);
-              if (j + 1 == nbi) umma_commit(&o_full[i]);
+        return true;
+      };
+      bool ok = wait_bar(q_full, 0) && wait_ring(pos_k(0));
+      if (ok) {
+        if (nb0 > 0) qk(0, 0);
+        if (nb1 > 0) qk(1, 0);
+        free_ring(pos_k(0));
+      }
+      for (int j = 0; j < nmax && ok; ++j) {
+        if (C::kOwnP) {
+          if (j + 1 < nmax) {
+            ok = wait_ring(pos_k(j + 1));
+            if (ok && j + 1 < nb0) {
+              ok = wait_bar(&s_read[0], j);
+              if (ok) qk(0, j + 1);
             }
+            if (ok && j + 1 < nb1) {
+              ok = wait_bar(&s_read[1], j);
+              if (ok) qk(1, j + 1);
+            }
+            if (ok) free_ring(pos_k(j + 1));
           }
-          if (i == 1 && lane == 0) umma_commit(&empty[tv % C::kStages]);
-          if (j + 1 < nmax && i == 0) ok = wait_ring(tk);
-          if (ok && j + 1 < nbi) qk(i, j + 1);
-          if (ok && j + 1 < nmax && i == 1 && lane == 0) umma_commit(&empty[tk % C::kStages]);
+          ok = ok && take_v(j) && (j >= nb0 || pv(0, j)) && (j >= nb1 || pv(1, j));
+          if (ok) free_ring(pos_v(j));
+        } else {
+          ok = take_v(j) && (j >= nb0 || pv(0, j));
+          if (ok && j + 1 < nmax) ok = wait_ring(pos_k(j + 1));
+          if (ok && j + 1 < nb0) qk(0, j + 1);
+          ok = ok && (j >= nb1 || pv(1, j));
+          if (ok) free_ring(pos_v(j));
+          if (ok && j + 1 < nb1) qk(1, j + 1);
+          if (ok && j + 1 < nmax) free_ring(pos_k(j + 1));
         }
       }
       if (!ok && lane == 0) {
         set_error(a.status_dev, MUON_ERR_TIMEOUT);
         *abort_flag = 1;
+      }
+      // never leave with products still running
+      for (int i = 0; i < 2; ++i) {
+        const int nbi = i == 0 ? nb0 : nb1;
+        if (ok && nbi > 0) wait_bar(&o_full[i], nbi - 1);
       }
     }
   } else if (warp >= 4) {
@@ -251,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     const int i = (warp - 4) / 4, w = warp & 3, nbi = i == 0 ? nb0 : nb1;
     const int row = row0 + i * kRows + w * 32 + lane;  // within the sequence
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * kRows, to = tmem + lanes + C::kO + i * HD;
+    const uint32_t ts = tmem + lanes + i * kRows, to = tmem + lanes + C::kO + i * HD, tp = tmem + lanes + C::kP + i * C::kPStep;
     const float sl = a.scale * 1.4426950408889634f;
     float top = -INFINITY;            // largest logit so far, unscaled
     float ref = 0.f;                  // the exponent's reference, scaled
@@ -267,6 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
       tmem_wait_ld();
+      if (C::kOwnP) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[i]);
+      }
       // keys of this block that the row sees
       const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows;
       if (__any_sync(0xffffffffu, vis < kRows)) {
@@ -278,14 +333,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       }
       float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
+      for (int e = 0; e < 32; e += 2)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) m[c] = fmaxf(m[c], __uint_as_float(s[c][e]));
+        for (int c = 0; c < 4; ++c) m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
       top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
       const float want = top == -INFINITY ? 0.f : top * sl;
       if (j == 0) {
         ref = want;
       } else {
+        // the product of the block before is long complete: O may be rescaled, P written
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], static_cast<uint32_t>((j - 1) & 1), abort_flag));
+        if (!ok) break;
+        tc_fence_after();
         // a row that sees any key sees the first, so ref is a maximum from block 0 on
         const bool move = want > ref + kLazy;
         if (__any_sync(0xffffffffu, move)) {
@@ -316,20 +375,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           add[2 * (e & 1) + 1] += p1;
           pk[e] = round_bf16x2(p0, p1);
         }
-        tmem_st32(ts + h * 32, pk);
+        tmem_st32(tp + h * 32, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * i + h]);
       }
       sum = (add[0] + add[1]) + (add[2] + add[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
     }
     if (!ok && lane == 0) {
       set_error(a.status_dev, MUON_ERR_TIMEOUT);
       *abort_flag = 1;
     }
     if (nbi > 0 && ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], 0, abort_flag));
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], static_cast<uint32_t>((nbi - 1) & 1), abort_flag));
       if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
       tc_fence_after();
     }
