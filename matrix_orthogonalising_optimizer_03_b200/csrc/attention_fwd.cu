@@ -5,8 +5,8 @@
 // one head as two tiles of 128, whose softmax and products alternate on the tensor core:
 //   S_i = Q_i K^T (128 x 128, fp32 in tensor memory), P = exp2(S scale log2 e - m) as bf16 over
 //   the same columns, O_i += P V with P as the tensor-memory operand
-// Warps: 0 TMA producer (Q once, then K and V blocks of 128 keys through a ring), 1 TMEM
-// allocator and MMA issuer, 4-7 and 8-11 the softmax of tile 0 and 1, one thread per row. While
+// Warps: 0 TMA producer (Q once, then K and V blocks of 128 keys through a ring), 1 and 2 MMA
+// issuers, one per tile (one issuer for both spent all its time issuing and waiting), 4-7 and 8-11 the softmax of tile 0 and 1, one thread per row. While
 // one tile's softmax runs, the other tile's products do.
 // m is the row's running maximum, moved only when a block exceeds it by more than 2^8 in the
 // exponent: until then P stays below 2^8 and nothing overflows (fp32 sums, bf16 P), and the
@@ -61,7 +61,7 @@ struct FwdCfg {
   static constexpr int kStages = HD == 128 ? 4 : 8;   // K and V blocks in flight
   static constexpr int kOffKv = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
   static constexpr int kO = 256;                      // first accumulator column
   // Head dimension 64 leaves 128 columns for P of its own, so that S is free for the next
   // product as soon as it has been read; with 128, P lies over the first half of S.
@@ -130,15 +130,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   uint64_t* s_read = s_full + 2;   // per tile: S is in registers
   uint64_t* p_full = s_read + 2;   // per tile and half: P of 64 keys is in place
   uint64_t* o_full = p_full + 4;   // per tile: the product with V is complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+  uint64_t* turn = o_full + 2;     // per tile and warp: its exponentials of the block are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (2 * C::kStages + 11) + 8 <= 256, "barrier region");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(8 * (2 * C::kStages + 19) + 8 <= 512, "barrier region");
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], (nb0 > 0 ? 1 : 0) + (nb1 > 0 ? 1 : 0));
     }
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       mbar_init(&p_full[2 * i], 4);
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&turn[4 * i + w], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -158,7 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+  // Ring positions of the K and V blocks, in the order of use. With P of its own the next
+  // block's S is computed while this block's softmax runs, so K_{j+1} comes before V_j.
+  auto pos_k = [&](int j) { return C::kOwnP ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
+  auto pos_v = [&](int j) { return C::kOwnP ? (j + 1 < nmax ? 2 * j + 2 : 2 * nmax - 1) : 2 * j + 1; };
 
   // Registers: 384 x 168 at launch; 128 x 56 + 256 x 224 is the same total.
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -171,16 +178,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         for (int c = 0; c < HD / 64; ++c)
           tma_load_3d(smem + i * C::kTileBytes + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
       bool ok = true;
-      int loads = 0;
+      int loads = 0, j[2] = {0, 0};  // the next K and V block
       for (int t = 0; t < 2 * nmax; ++t) {
         const int s = t % C::kStages;
+        const bool is_v = j[1] < nmax && t == pos_v(j[1]);
         if (!mbar_wait(&empty[s], static_cast<uint32_t>((t / C::kStages) & 1) ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
-        const bool is_v = C::kOwnP ? (t > 0 && (t & 1) == 0) || t == 2 * nmax - 1 : (t & 1) != 0;
-        const int j = !C::kOwnP ? t >> 1 : is_v ? (t == 2 * nmax - 1 ? nmax - 1 : t / 2 - 1) : (t + 1) / 2;
-        load_tile<HD>(smem + C::kOffKv + s * C::kTileBytes, is_v ? &P.tv : &P.tk, &full[s], kvh, r.k0 + j * kRows);
+        load_tile<HD>(smem + C::kOffKv + s * C::kTileBytes, is_v ? &P.tv : &P.tk, &full[s], kvh,
+                      r.k0 + (is_v ? j[1]++ : j[0]++) * kRows);
         ++loads;
       }
       if (!ok) {
@@ -192,107 +199,85 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       for (int t = loads > C::kStages ? loads - C::kStages : 0; t < loads; ++t)
         mbar_wait(&full[t % C::kStages], static_cast<uint32_t>((t / C::kStages) & 1), nullptr);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (nmax > 0) {
+  } else if (warp < 3) {
+    // ------------------------------------------------------------ MMA issuers, one per tile
+    const int i = warp - 1, n = i == 0 ? nb0 : nb1;
+    if (n > 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, HD, true);
-      const uint64_t kmaj = smem_desc_sw128(0, 16, 1024), mn = smem_desc_sw128(0, kChunk, 1024);
-      // Ring positions, in the order of use. Own P: the next block's S is computed while this
-      // block's softmax runs, so K_{j+1} comes before V_j.
-      auto pos_k = [&](int j) { return C::kOwnP ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
-      auto pos_v = [&](int j) { return C::kOwnP ? (j + 1 < nmax ? 2 * j + 2 : 2 * nmax - 1) : 2 * j + 1; };
-      auto ring = [&](int t) { return smem + C::kOffKv + (t % C::kStages) * C::kTileBytes; };
+      // low words of the operand descriptors: address and leading offset, both / 16
+      constexpr uint32_t kmaj = 1u << 16, mn = static_cast<uint32_t>(kChunk >> 4) << 16;
+      const uint32_t base = smem_u32(smem) >> 4;
+      const uint32_t qd = kmaj | (base + i * (C::kTileBytes >> 4));
+      const uint32_t ts = tmem + i * kRows, tp = tmem + C::kP + i * C::kPStep, to = tmem + C::kO + i * HD;
+      auto slot_of = [&](int t) { return t % C::kStages; };
       auto wait_bar = [&](uint64_t* bar, int phase) {
         const bool got = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag));
         tc_fence_after();
         return got;
       };
-      auto wait_ring = [&](int t) { return wait_bar(&full[t % C::kStages], t / C::kStages); };
-      auto free_ring = [&](int t) {
-        if (elect_one()) umma_commit(&empty[t % C::kStages]);
-      };
-      auto qk = [&](int i, int j) {  // S_i = Q_i K_j^T
+      auto qk = [&](int j) {  // S = Q K_j^T, then K_j is free
+        const int t = pos_k(j);
+        if (!wait_bar(&full[slot_of(t)], t / C::kStages)) return false;
+        if (C::kOwnP && j > 0 && !wait_bar(&s_read[i], j - 1)) return false;
         if (elect_one()) {
-          const uint64_t qd = kmaj | ((smem_u32(smem + i * C::kTileBytes) >> 4) & 0x3FFFu);
-          const uint64_t kd = kmaj | ((smem_u32(ring(pos_k(j))) >> 4) & 0x3FFFu);
+          const uint32_t kd = kmaj | (base + ((C::kOffKv + slot_of(t) * C::kTileBytes) >> 4));
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
-            const uint64_t off = static_cast<uint64_t>((k >> 2) * (kChunk >> 4) + (k & 3) * 2);
-            umma_f16(tmem + i * kRows, qd + off, kd + off, idesc_s, k != 0);
+            const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
+            umma_f16_lo(ts, qd + off, kd + off, kDescHi, idesc_s, k != 0);
           }
           umma_commit(&s_full[i]);
-        }
-      };
-      auto pv = [&](int i, int j) {  // O_i += P_i V_j, by halves of the keys as P arrives
-        bool got = true;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          got = got && wait_bar(&p_full[2 * i + h], j);
-          if (got && elect_one()) {
-            const uint64_t vd = mn | ((smem_u32(ring(pos_v(j))) >> 4) & 0x3FFFu);
-#pragma unroll
-            for (int k = 4 * h; k < 4 * h + 4; ++k)
-              umma_f16_ts(tmem + C::kO + i * HD, tmem + C::kP + i * C::kPStep + k * 8, vd + 128u * k, idesc_o, (j | k) != 0);
-            if (h == 1) umma_commit(&o_full[i]);
-          }
-        }
-        return got;
-      };
-      // V_j has landed; keys past the sequence have probability 0, and their V must not be NaN
-      auto take_v = [&](int j) {
-        if (!wait_ring(pos_v(j))) return false;
-        const int live = r.n - j * kRows;
-        if (live < kRows) {
-          uint8_t* v = ring(pos_v(j));
-          for (int t = live * 8 + lane; t < kRows * 8; t += 32)
-#pragma unroll
-            for (int c = 0; c < HD / 64; ++c)
-              *reinterpret_cast<uint4*>(v + c * kChunk + t * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
+          umma_commit(&empty[slot_of(t)]);
         }
         return true;
       };
-      bool ok = wait_bar(q_full, 0) && wait_ring(pos_k(0));
-      if (ok) {
-        if (nb0 > 0) qk(0, 0);
-        if (nb1 > 0) qk(1, 0);
-        free_ring(pos_k(0));
-      }
-      for (int j = 0; j < nmax && ok; ++j) {
-        if (C::kOwnP) {
-          if (j + 1 < nmax) {
-            ok = wait_ring(pos_k(j + 1));
-            if (ok && j + 1 < nb0) {
-              ok = wait_bar(&s_read[0], j);
-              if (ok) qk(0, j + 1);
-            }
-            if (ok && j + 1 < nb1) {
-              ok = wait_bar(&s_read[1], j);
-              if (ok) qk(1, j + 1);
-            }
-            if (ok) free_ring(pos_k(j + 1));
-          }
-          ok = ok && take_v(j) && (j >= nb0 || pv(0, j)) && (j >= nb1 || pv(1, j));
-          if (ok) free_ring(pos_v(j));
-        } else {
-          ok = take_v(j) && (j >= nb0 || pv(0, j));
-          if (ok && j + 1 < nmax) ok = wait_ring(pos_k(j + 1));
-          if (ok && j + 1 < nb0) qk(0, j + 1);
-          ok = ok && (j >= nb1 || pv(1, j));
-          if (ok) free_ring(pos_v(j));
-          if (ok && j + 1 < nb1) qk(1, j + 1);
-          if (ok && j + 1 < nmax) free_ring(pos_k(j + 1));
+      auto pv = [&](int j) {  // O += P V_j, by halves of the keys as P arrives, then V_j is free
+        const int t = pos_v(j), s = slot_of(t), live = r.n - j * kRows;
+        if (!wait_bar(&full[s], t / C::kStages)) return false;
+        if (live < kRows) {
+          // Keys past the sequence have probability 0, and their V must not be NaN. Both
+          // issuers write these zeros; whichever is later writes over zeros.
+          uint8_t* v = smem + C::kOffKv + s * C::kTileBytes;
+          for (int e = live * 8 + lane; e < kRows * 8; e += 32)
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+              *reinterpret_cast<uint4*>(v + c * kChunk + e * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
+        const uint32_t vd = mn | (base + ((C::kOffKv + s * C::kTileBytes) >> 4));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!wait_bar(&p_full[2 * i + h], j)) return false;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              umma_f16_ts_lo(to, tp + k * 8, vd + 128u * k, kDescHi, idesc_o, (j | k) != 0);
+            if (h == 1) {
+              umma_commit(&o_full[i]);
+              umma_commit(&empty[s]);
+            }
+          }
+        }
+        return true;
+      };
+      // what the tile does not use itself, it still has to free
+      auto skip = [&](int t) {
+        if (!wait_bar(&full[slot_of(t)], t / C::kStages)) return false;
+        if (elect_one()) mbar_arrive(&empty[slot_of(t)]);
+        return true;
+      };
+      bool ok = wait_bar(q_full, 0) && qk(0);
+      for (int j = 0; j < nmax && ok; ++j) {
+        if (C::kOwnP && j + 1 < nmax) ok = j + 1 < n ? qk(j + 1) : skip(pos_k(j + 1));
+        ok = ok && (j < n ? pv(j) : skip(pos_v(j)));
+        if (!C::kOwnP && ok && j + 1 < nmax) ok = j + 1 < n ? qk(j + 1) : skip(pos_k(j + 1));
       }
+      // never leave with products still running
+      ok = ok && wait_bar(&o_full[i], n - 1);
       if (!ok && lane == 0) {
         set_error(a.status_dev, MUON_ERR_TIMEOUT);
         *abort_flag = 1;
-      }
-      // never leave with products still running
-      for (int i = 0; i < 2; ++i) {
-        const int nbi = i == 0 ? nb0 : nb1;
-        if (ok && nbi > 0) wait_bar(&o_full[i], nbi - 1);
       }
     }
   } else if (warp >= 4) {
@@ -362,6 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           }
         }
       }
+      // Two warps, one of each tile, share a scheduler and its exponential unit: they take
+      // turns, so that one's maximum and transfers overlap the other's exponentials.
+      if (i == 0 ? j > 0 && j <= nb1 : j < nb0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&turn[4 * (1 - i) + w], static_cast<uint32_t>((i == 0 ? j - 1 : j) & 1), abort_flag));
+        if (!ok) break;
+      }
       float add[4] = {sum, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -374,6 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           add[2 * (e & 1)] += p0;
           add[2 * (e & 1) + 1] += p1;
           pk[e] = round_bf16x2(p0, p1);
+        }
+        if (h == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&turn[4 * i + w]);
         }
         tmem_st32(tp + h * 32, pk);
         tmem_wait_st();
