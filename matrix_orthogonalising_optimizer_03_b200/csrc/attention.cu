@@ -1,6 +1,5 @@
-// Softmax attention of packed sequences and its backward pass (muon_attention_t): host
-// checks and, for now, simple kernels: one warp per query row and head (o, lse, dQ) or per
-// key and key head (dK, dV), in fp32 on the CUDA cores.
+// Softmax attention of packed sequences and its backward pass (muon_attention_t): host checks
+// and C entry points.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -8,88 +7,10 @@
 
 #include "attention.h"
 #include "muon.h"
-#include "ptx.cuh"
 #include "validate.h"
 
 namespace muon {
 namespace {
-
-// The sequence of a row, or -1.
-__device__ int row_seq(const int32_t* off, int n_seq, int32_t tokens, int row) {
-  if (off == nullptr) return 0;
-  for (int s = 0; s < n_seq; ++s)
-    if (row >= clamp_offset(off, s, tokens) && row < clamp_offset(off, s + 1, tokens)) return s;
-  return -1;
-}
-
-__device__ __forceinline__ const uint16_t* at(const muon_heads_t& h, int64_t t, int head) {
-  return static_cast<const uint16_t*>(h.ptr) + t * h.ld + head * h.head;
-}
-__device__ __forceinline__ uint16_t* at_w(const muon_heads_t& h, int64_t t, int head) {
-  return static_cast<uint16_t*>(h.ptr) + t * h.ld + head * h.head;
-}
-
-__device__ __forceinline__ void load_row(const uint16_t* p, int d, int lane, float (&x)[4]) {
-  for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < d ? bf16_to_f32(p[lane + 32 * i]) : 0.f;
-}
-__device__ __forceinline__ float dot(const float (&x)[4], const float (&y)[4]) {
-  return warp_sum(x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3]);
-}
-
-__global__ void attention_dq_simple_kernel(const __grid_constant__ muon_attention_t a, float* delta) {
-  const int lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y;
-  if (i >= a.q_tokens) return;
-  const int s = row_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), i);
-  if (s < 0) return;
-  const SeqRange r = seq_range(a, s);
-  const int kh = h / (a.heads / a.kv_heads);
-  const int vis = a.causal ? min(r.n, i - r.q0 + r.n - r.m + 1) : r.n;
-  float q[4], o[4], d[4], acc[4] = {};
-  load_row(at(a.q, i, h), a.head_dim, lane, q);
-  load_row(at(a.o, i, h), a.head_dim, lane, o);
-  load_row(at(a.dout, i, h), a.head_dim, lane, d);
-  const float dl = dot(o, d), lse = a.lse[h * a.q_tokens + i];
-  if (lane == 0) delta[h * a.q_tokens + i] = dl;
-  for (int j = 0; j < vis; ++j) {
-    float k[4], v[4];
-    load_row(at(a.k, r.k0 + j, kh), a.head_dim, lane, k);
-    load_row(at(a.v, r.k0 + j, kh), a.head_dim, lane, v);
-    const float p = expf(dot(q, k) * a.scale - lse), ds = p * (dot(d, v) - dl) * a.scale;
-    for (int e = 0; e < 4; ++e) acc[e] += ds * k[e];
-  }
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < a.head_dim) at_w(a.dq, i, h)[lane + 32 * e] = f32_to_bf16(acc[e]);
-}
-
-__global__ void attention_dkv_simple_kernel(const __grid_constant__ muon_attention_t a, const float* delta) {
-  const int lane = threadIdx.x & 31, kt = blockIdx.x * 4 + (threadIdx.x >> 5), kh = blockIdx.y;
-  if (kt >= a.k_tokens) return;
-  const int s = row_seq(a.k_offsets, a.n_seq, static_cast<int>(a.k_tokens), kt);
-  if (s < 0) return;
-  const SeqRange r = seq_range(a, s);
-  const int j = kt - r.k0, per = a.heads / a.kv_heads;
-  const int first = a.causal ? max(0, j - (r.n - r.m)) : 0;  // the first row that sees key j
-  float k[4], v[4], ak[4] = {}, av[4] = {};
-  load_row(at(a.k, kt, kh), a.head_dim, lane, k);
-  load_row(at(a.v, kt, kh), a.head_dim, lane, v);
-  for (int h = kh * per; h < (kh + 1) * per; ++h)
-    for (int i = r.q0 + first; i < r.q0 + r.m; ++i) {
-      float q[4], d[4];
-      load_row(at(a.q, i, h), a.head_dim, lane, q);
-      load_row(at(a.dout, i, h), a.head_dim, lane, d);
-      const float p = expf(dot(q, k) * a.scale - a.lse[h * a.q_tokens + i]);
-      const float ds = p * (dot(d, v) - delta[h * a.q_tokens + i]) * a.scale;
-      for (int e = 0; e < 4; ++e) {
-        av[e] += p * d[e];
-        ak[e] += ds * q[e];
-      }
-    }
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < a.head_dim) {
-      at_w(a.dk, kt, kh)[lane + 32 * e] = f32_to_bf16(ak[e]);
-      at_w(a.dv, kt, kh)[lane + 32 * e] = f32_to_bf16(av[e]);
-    }
-}
 
 // ------------------------------------------------------------------ host checks
 // A BF16 tensor tokens x heads x head_dim as the checks see it (strides of axes of one
@@ -215,11 +136,7 @@ extern "C" MUON_API muon_status_t muon_attention_backward(const muon_attention_t
   int dev = 0, sms = 0;
   const muon_status_t d = current_device(&dev, &sms);
   if (d != MUON_OK) return d;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  float* delta = static_cast<float*>(workspace);
-  if (a->q_tokens > 0)
-    attention_dq_simple_kernel<<<dim3((a->q_tokens + 3) / 4, a->heads), 128, 0, st>>>(*a, delta);
-  if (a->k_tokens > 0)
-    attention_dkv_simple_kernel<<<dim3((a->k_tokens + 3) / 4, a->kv_heads), 128, 0, st>>>(*a, delta);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return launch_attention_backward(*a, static_cast<float*>(workspace), dev, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? MUON_OK : MUON_ERR_CUDA;
 }

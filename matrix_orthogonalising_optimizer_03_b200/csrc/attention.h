@@ -17,6 +17,12 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One sequence's rows and keys, clamped to the tensors.
 struct SeqRange {
   int32_t q0, m;  // first query row, queries
@@ -74,5 +80,7 @@ inline int64_t tile_slots(const int32_t* off, int n_seq, int64_t tokens, int row
 }
 
 cudaError_t launch_attention_forward(const muon_attention_t& a, int dev, cudaStream_t st);
+// delta: heads x q_tokens floats of scratch, written by the first kernel, read by the second.
+cudaError_t launch_attention_backward(const muon_attention_t& a, float* delta, int dev, cudaStream_t st);
 
 }  // namespace muon

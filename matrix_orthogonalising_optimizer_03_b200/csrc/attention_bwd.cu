@@ -1,0 +1,646 @@
+// Backward pass of softmax attention over packed sequences (muon_attention_backward). The
+// probabilities are recomputed from the forward pass's log-sum-exp:
+//   P = exp(S - lse), delta_i = o_i . dout_i, dS = P (dout V^T - delta)
+//   dV = P^T dout, dK = scale dS^T Q, dQ = scale dS K
+//
+// Two kernels, each of whose outputs is summed by one CTA in a fixed order, so that equal
+// calls give equal bits: one per 128 query rows for dQ (and delta), one per 128 keys for dK
+// and dV, over all query heads of the key head. S and dout V^T are computed in both: seven
+// products instead of five, against fp32 atomics on dQ, whose order changes its sums.
+// In both, 8 warps own a 128 x 128 block in tensor memory, a thread 64 elements of one lane's
+// row. P and dS are rounded to bf16 (relative 2^-9, errors of either sign) and written back
+// over the scores they came from, where the next product takes them as its tensor-memory
+// operand; the transposes that dV and dK need cost nothing, because the second kernel computes
+// S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
+// Two warps issue the products, one for each chain of products that wait for one another.
+// Bound by the tensor core: an M = 128 product whose operands both come from shared memory
+// runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "attention.h"
+#include "muon.h"
+#include "ptx.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kRows = 128;            // rows and keys of a block
+constexpr int kChunk = kRows * 128;   // bytes of 64 columns of a tile
+constexpr int kThreads = 384;         // 4 warps that move and issue, 8 that compute
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int HD>
+struct BwdCfg {
+  static constexpr int kTile = kRows * HD * 2;
+  static constexpr int kRing3 = 3, kRing2 = 2;  // the operand of two chains, and of one
+  static constexpr int kOffRing3 = 2 * kTile;
+  static constexpr int kOffRing2 = kOffRing3 + kRing3 * kTile;
+  static constexpr int kOffVec = kOffRing2 + kRing2 * kTile;  // lse and delta of a block of rows
+  static constexpr int kVecBytes = 2 * kRows * 4;
+  static constexpr int kOffBar = kOffVec + 2 * kVecBytes;
+  static constexpr int kSmemBytes = kOffBar + 512;
+};
+
+struct BwdParams {
+  CUtensorMap tq, tk, tv, tdo;
+  muon_attention_t a;
+  float* delta;
+};
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, int phase, volatile int* abort_flag) {
+  const bool got = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag));
+  tc_fence_after();
+  return got;
+}
+
+template <int HD>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
+  mbar_expect_tx(bar, BwdCfg<HD>::kTile);
+#pragma unroll
+  for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * kChunk, map, bar, c * 64, head, token);
+}
+
+// Zeros the rows from `live` on of a tile in shared memory (one warp): another sequence's rows
+// that a product would sum over, with factors of zero but perhaps NaN themselves.
+template <int HD>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int live, int lane) {
+  for (int e = live * 8 + lane; e < kRows * 8; e += 32)
+#pragma unroll
+    for (int c = 0; c < HD / 64; ++c) *reinterpret_cast<uint4*>(tile + c * kChunk + e * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// D (+)= A B^T over the head dimension: both operands K-major tiles in shared memory.
+template <int HD>
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+  const uint32_t ad = (1u << 16) | (a_addr >> 4), bd = (1u << 16) | (b_addr >> 4);
+#pragma unroll
+  for (int k = 0; k < HD / 16; ++k) {
+    const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
+    umma_f16_lo(d, ad + off, bd + off, kDescHi, idesc, k != 0);
+  }
+}
+
+// D (+)= A B over the 128 rows or keys of a block: A bf16 in tensor memory (the first 64 in
+// columns 0-31, the others in columns 64-95), B an MN-major tile in shared memory.
+template <int HD>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
+  const uint32_t bd = (static_cast<uint32_t>(kChunk >> 4) << 16) | (b_addr >> 4);
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)
+    umma_f16_ts_lo(d, a_tmem + (k >> 2) * 64 + (k & 3) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
+}
+
+// Writes `cols` accumulator columns of this thread's row, times f, as bf16.
+__device__ __forceinline__ void store_row(uint32_t taddr, int cols, float f, bool zero, bool live, uint16_t* out, int col0,
+                                          int dim) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t v[32];
+    if (!zero) {
+      tmem_ld32(taddr + c, v);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      uint32_t pk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        pk[k] = round_bf16x2(__uint_as_float(v[e + 2 * k]) * f, __uint_as_float(v[e + 2 * k + 1]) * f);
+      if (live && col0 + c + e < dim)
+        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dQ and delta
+// Chain A: S_j = Q K_j^T (two buffers), dQ += dS_j K_j.  Chain B: dP_j = dout V_j^T.
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_constant__ BwdParams P) {
+  using C = BwdCfg<HD>;
+  const muon_attention_t& a = P.a;
+  const int heads = a.heads, head = static_cast<int>(blockIdx.x % heads);
+  // later rows see more keys: the long tiles of a causal sequence start first
+  const int slot = static_cast<int>(gridDim.x / heads - 1 - blockIdx.x / heads);
+  int row0;
+  const SeqRange r = seq_range(a, tile_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), kRows, slot, &row0));
+  if (row0 >= r.m) return;
+  const int shift = r.n - r.m;  // causal: row i sees keys j <= i + shift
+  const int keys = a.causal ? min(r.n, min(row0 + kRows, r.m) + shift) : r.n;
+  const int n = keys > 0 ? (keys + kRows - 1) / kRows : 0;  // key blocks
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_full = q_full + 1;    // ring of K blocks
+  uint64_t* k_empty = k_full + 3;
+  uint64_t* v_full = k_empty + 3;   // ring of V blocks
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* s_full = v_empty + 2;   // per block parity
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* dp_read = dp_full + 1;
+  uint64_t* ds_full = dp_read + 1;  // per block parity
+  uint64_t* done = ds_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&ds_full[s], 8);
+    }
+    mbar_init(dp_full, 1);
+    mbar_init(dp_read, 8);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  constexpr uint32_t kDp = 256, kDq = 384;  // columns of dP and dQ; S at 128 (j & 1)
+  uint8_t *sq = smem, *sdo = smem + C::kTile, *sk = smem + C::kOffRing3, *sv = smem + C::kOffRing2;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {
+      const int kvh = head / (heads / a.kv_heads);
+      mbar_expect_tx(q_full, 2 * C::kTile);
+      for (int c = 0; c < HD / 64; ++c) {
+        tma_load_3d(sq + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0);
+        tma_load_3d(sdo + c * kChunk, &P.tdo, q_full, c * 64, head, r.q0 + row0);
+      }
+      int kl = 0, vl = 0;
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait(&k_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        load_tile<HD>(sk + j % 3 * C::kTile, &P.tk, &k_full[j % 3], kvh, r.k0 + j * kRows);
+        ++kl;
+        ok = mbar_wait(&v_empty[j & 1], static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        load_tile<HD>(sv + (j & 1) * C::kTile, &P.tv, &v_full[j & 1], kvh, r.k0 + j * kRows);
+        ++vl;
+      }
+      // never leave with bulk copies still landing in shared memory
+      mbar_wait(q_full, 0, nullptr);
+      for (int j = kl > 3 ? kl - 3 : 0; j < kl; ++j) mbar_wait(&k_full[j % 3], static_cast<uint32_t>((j / 3) & 1), nullptr);
+      for (int j = vl > 2 ? vl - 2 : 0; j < vl; ++j) mbar_wait(&v_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    if (n > 0) {
+      auto score = [&](int j) {  // S_j; the buffer's dS_{j-2} went into a product issued before
+        if (!wait_all(&k_full[j % 3], j / 3, abort_flag)) return false;
+        const int live = r.n - j * kRows;
+        if (live < kRows) clear_rows<HD>(sk + j % 3 * C::kTile, live, lane);
+        if (elect_one()) {
+          product_ss<HD>(tmem + (j & 1) * 128, smem_u32(sq), smem_u32(sk) + j % 3 * C::kTile);
+          umma_commit(&s_full[j & 1]);
+        }
+        return true;
+      };
+      ok = wait_all(q_full, 0, abort_flag) && score(0) && (n < 2 || score(1));
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait_all(&ds_full[j & 1], j >> 1, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
+          product_ts<HD>(tmem + kDq, tmem + (j & 1) * 128, smem_u32(sk) + j % 3 * C::kTile, j > 0);
+          umma_commit(&k_empty[j % 3]);
+          if (j + 1 == n) umma_commit(done);
+        }
+        if (j + 2 < n) ok = score(j + 2);
+      }
+      ok = ok && wait_all(done, 0, abort_flag);  // never leave with products still running
+    }
+  } else if (warp == 2) {
+    if (n > 0) {
+      ok = wait_all(q_full, 0, abort_flag);
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait_all(&v_full[j & 1], j >> 1, abort_flag) && (j == 0 || wait_all(dp_read, j - 1, abort_flag));
+        if (ok && elect_one()) {
+          product_ss<HD>(tmem + kDp, smem_u32(sdo), smem_u32(sv) + (j & 1) * C::kTile);
+          umma_commit(dp_full);
+          umma_commit(&v_empty[j & 1]);
+        }
+      }
+      ok = ok && wait_all(dp_full, n - 1, abort_flag);
+    }
+  } else if (warp >= 4) {
+    const int w = warp & 3, half = (warp - 4) >> 2;     // lane quarter, and half of a block's keys
+    const int row = row0 + w * 32 + lane;               // within the sequence
+    const bool live = row < r.m;
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const int64_t token = r.q0 + row, vec = static_cast<int64_t>(head) * a.q_tokens + token;
+    float delta = 0.f, lse = INFINITY;  // of rows without keys, or none: P = 0
+    if (live) {
+      const uint4* o = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.ptr) + token * a.o.ld + head * a.o.head);
+      const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout.ptr) + token * a.dout.ld + head * a.dout.head);
+      float part[4] = {};
+#pragma unroll 4
+      for (int c = 0; c < a.head_dim / 8; ++c) {
+        const uint4 x = __ldg(o + c), y = __ldg(g + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          part[e] = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), part[e]);
+          part[e] = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), part[e]);
+        }
+      }
+      delta = (part[0] + part[1]) + (part[2] + part[3]);
+      if (half == 0) P.delta[vec] = delta;
+      const float l = __ldg(a.lse + vec);
+      if (l != -INFINITY) lse = l * kLog2e;
+    }
+    const float sl = a.scale * kLog2e;
+    for (int j = 0; j < n; ++j) {
+      ok = wait_all(&s_full[j & 1], j >> 1, abort_flag);
+      if (!ok) break;
+      const uint32_t ts = tmem + lanes + (j & 1) * 128 + half * 64;
+      uint32_t s[2][32], p[2][32];
+      tmem_ld32(ts, s[0]);
+      tmem_ld32(ts + 32, s[1]);
+      tmem_wait_ld();
+      // keys of this half block that the row sees
+      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows - half * 64;
+      const bool masked = __any_sync(0xffffffffu, vis < 64);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), sl, -lse)));
+      ok = wait_all(dp_full, j, abort_flag);
+      if (!ok) break;
+      tmem_ld32(tmem + lanes + kDp + half * 64, p[0]);
+      tmem_ld32(tmem + lanes + kDp + half * 64 + 32, p[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dp_read);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * (__uint_as_float(p[c][e]) - delta));
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= vis) s[c][e] = 0;
+      }
+      uint32_t pk[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        pk[e] = round_bf16x2(__uint_as_float(s[e >> 4][2 * (e & 15)]), __uint_as_float(s[e >> 4][2 * (e & 15) + 1]));
+      tmem_st32(ts, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[j & 1]);
+    }
+    if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
+    store_row(tmem + lanes + kDq + half * (HD / 2), HD / 2, a.scale, n == 0, live && ok,
+              static_cast<uint16_t*>(a.dq.ptr) + token * a.dq.ld + head * a.dq.head + half * (HD / 2), half * (HD / 2),
+              a.head_dim);
+    tc_fence_before();
+  }
+  if (!ok && lane == 0) {
+    set_error(a.status_dev, MUON_ERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dK and dV
+// Chain A: S^T_j = K Q_j^T, dV += P^T_j dout_j.  Chain B: dP^T_j = V dout_j^T, dK += dS^T_j Q_j.
+// Block j runs over the row tiles that see the keys, head after head.
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
+  using C = BwdCfg<HD>;
+  const muon_attention_t& a = P.a;
+  const int kvh = static_cast<int>(blockIdx.x % a.kv_heads), per = a.heads / a.kv_heads;
+  // earlier keys are seen by more rows, and come first
+  const int slot = static_cast<int>(blockIdx.x / a.kv_heads);
+  int key0;
+  const SeqRange r = seq_range(a, tile_seq(a.k_offsets, a.n_seq, static_cast<int>(a.k_tokens), kRows, slot, &key0));
+  if (key0 >= r.n) return;
+  const int shift = r.n - r.m;
+  const int tile0 = a.causal ? max(0, key0 - shift) / kRows : 0;  // the first row tile that sees a key
+  const int tiles = max(0, (r.m + kRows - 1) / kRows - tile0), n = tiles * per;
+
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_full = kv_full + 1;    // ring of Q blocks: landed
+  uint64_t* q_ready = q_full + 3;    // and with rows past the sequence cleared, lse and delta in place
+  uint64_t* q_empty = q_ready + 3;
+  uint64_t* do_full = q_empty + 3;   // ring of dout blocks
+  uint64_t* do_ready = do_full + 2;
+  uint64_t* do_empty = do_ready + 2;
+  uint64_t* s_full = do_empty + 2;
+  uint64_t* p_full = s_full + 1;
+  uint64_t* dp_full = p_full + 1;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* done = ds_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_ready[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_ready[s], 1);
+      mbar_init(&do_empty[s], 2);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(done, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  constexpr uint32_t kDp = 128, kDv = 256, kDk = 256 + HD;  // columns; S at 0
+  uint8_t *sk = smem, *sv = smem + C::kTile, *sq = smem + C::kOffRing3, *sdo = smem + C::kOffRing2;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {
+      mbar_expect_tx(kv_full, 2 * C::kTile);
+      for (int c = 0; c < HD / 64; ++c) {
+        tma_load_3d(sk + c * kChunk, &P.tk, kv_full, c * 64, kvh, r.k0 + key0);
+        tma_load_3d(sv + c * kChunk, &P.tv, kv_full, c * 64, kvh, r.k0 + key0);
+      }
+      int ql = 0, dl = 0, h = kvh * per, t = tile0;
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait(&q_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        load_tile<HD>(sq + j % 3 * C::kTile, &P.tq, &q_full[j % 3], h, r.q0 + t * kRows);
+        ++ql;
+        ok = mbar_wait(&do_empty[j & 1], static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        load_tile<HD>(sdo + (j & 1) * C::kTile, &P.tdo, &do_full[j & 1], h, r.q0 + t * kRows);
+        ++dl;
+        if (++t == tile0 + tiles) t = tile0, ++h;
+      }
+      // never leave with bulk copies still landing in shared memory
+      mbar_wait(kv_full, 0, nullptr);
+      for (int j = ql > 3 ? ql - 3 : 0; j < ql; ++j) mbar_wait(&q_full[j % 3], static_cast<uint32_t>((j / 3) & 1), nullptr);
+      for (int j = dl > 2 ? dl - 2 : 0; j < dl; ++j) mbar_wait(&do_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), nullptr);
+    }
+  } else if (warp == 1) {
+    if (n > 0) {
+      auto score = [&](int j) {  // S^T_j; P^T_{j-1} over it went into a product issued before
+        if (!wait_all(&q_ready[j % 3], j / 3, abort_flag)) return false;
+        if (elect_one()) {
+          product_ss<HD>(tmem, smem_u32(sk), smem_u32(sq) + j % 3 * C::kTile);
+          umma_commit(s_full);
+        }
+        return true;
+      };
+      ok = wait_all(kv_full, 0, abort_flag) && score(0);
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait_all(p_full, j, abort_flag) && wait_all(&do_ready[j & 1], j >> 1, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
+          product_ts<HD>(tmem + kDv, tmem, smem_u32(sdo) + (j & 1) * C::kTile, j > 0);
+          umma_commit(&do_empty[j & 1]);
+          if (j + 1 == n) umma_commit(done);
+        }
+        if (j + 1 < n) ok = score(j + 1);
+      }
+      ok = ok && wait_all(done, 0, abort_flag);  // never leave with products still running
+    }
+  } else if (warp == 2) {
+    if (n > 0) {
+      auto dprob = [&](int j) {  // dP^T_j; dS^T_{j-1} over it went into a product issued before
+        if (!wait_all(&do_ready[j & 1], j >> 1, abort_flag)) return false;
+        if (elect_one()) {
+          product_ss<HD>(tmem + kDp, smem_u32(sv), smem_u32(sdo) + (j & 1) * C::kTile);
+          umma_commit(dp_full);
+          umma_commit(&do_empty[j & 1]);
+        }
+        return true;
+      };
+      ok = wait_all(kv_full, 0, abort_flag) && dprob(0);
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait_all(ds_full, j, abort_flag) && wait_all(&q_ready[j % 3], j / 3, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
+          product_ts<HD>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kTile, j > 0);
+          umma_commit(&q_empty[j % 3]);
+          if (j + 1 == n) umma_commit(done);
+        }
+        if (j + 1 < n) ok = dprob(j + 1);
+      }
+      ok = ok && wait_all(done, 0, abort_flag);
+    }
+  } else if (warp == 3) {
+    // Stages what the copies do not bring: lse (times log2 e) and delta of the block's rows, and
+    // zeros over the rows past the sequence. Such rows, and rows that see no key, get lse = inf:
+    // P = 0.
+    int h = kvh * per, t = tile0;
+    for (int j = 0; j < n; ++j) {
+      const int live = r.m - t * kRows;
+      const int64_t at = static_cast<int64_t>(h) * a.q_tokens + r.q0 + t * kRows;
+      float l[4], d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = e * 32 + lane;
+        const float x = i < live ? __ldg(a.lse + at + i) : -INFINITY;
+        l[e] = x == -INFINITY ? INFINITY : x * kLog2e;
+        d[e] = i < live ? P.delta[at + i] : 0.f;
+      }
+      // two of these vectors: block j - 2 is done with its own once its last product is complete
+      ok = wait_all(&q_full[j % 3], j / 3, abort_flag) &&
+           (j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
+      if (!ok) break;
+      float* v = reinterpret_cast<float*>(smem + C::kOffVec + (j & 1) * C::kVecBytes);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e * 32 + lane] = l[e];
+        v[kRows + e * 32 + lane] = d[e];
+      }
+      if (live < kRows) clear_rows<HD>(sq + j % 3 * C::kTile, live, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_ready[j % 3]);
+      ok = wait_all(&do_full[j & 1], j >> 1, abort_flag);
+      if (!ok) break;
+      if (live < kRows) clear_rows<HD>(sdo + (j & 1) * C::kTile, live, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&do_ready[j & 1]);
+      if (++t == tile0 + tiles) t = tile0, ++h;
+    }
+  } else {
+    const int w = warp & 3, half = (warp - 4) >> 2;     // lane quarter, and half of a block's rows
+    const int key = key0 + w * 32 + lane;               // within the sequence
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    const float sl = a.scale * kLog2e;
+    int t = tile0;
+    for (int j = 0; j < n; ++j) {
+      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(s_full, j, abort_flag);
+      if (!ok) break;
+      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + (j & 1) * C::kVecBytes) + half * 16;
+      const float4* dlt = lse + kRows / 4;
+      const uint32_t ts = tmem + lanes + half * 64, tp = ts + kDp;
+      uint32_t s[2][32];
+      tmem_ld32(ts, s[0]);
+      tmem_ld32(ts + 32, s[1]);
+      tmem_wait_ld();
+      // the first row of this half block that sees the key (rows are columns here)
+      const int first = a.causal ? key - shift - t * kRows - half * 64 : 0;
+      if (++t == tile0 + tiles) t = tile0;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 l = lse[(c * 32 + e) / 4];
+          s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), sl, -l.x)));
+          s[c][e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e + 1]), sl, -l.y)));
+          s[c][e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e + 2]), sl, -l.z)));
+          s[c][e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e + 3]), sl, -l.w)));
+        }
+      if (__any_sync(0xffffffffu, first > 0)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e < first) s[c][e] = 0;
+      }
+      uint32_t pk[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        pk[e] = round_bf16x2(__uint_as_float(s[e >> 4][2 * (e & 15)]), __uint_as_float(s[e >> 4][2 * (e & 15) + 1]));
+      tmem_st32(ts, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      ok = wait_all(dp_full, j, abort_flag);
+      if (!ok) break;
+      uint32_t p[2][32];
+      tmem_ld32(tp, p[0]);
+      tmem_ld32(tp + 32, p[1]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 d = dlt[(c * 32 + e) / 4];
+          const float x0 = __uint_as_float(s[c][e]) * (__uint_as_float(p[c][e]) - d.x);
+          const float x1 = __uint_as_float(s[c][e + 1]) * (__uint_as_float(p[c][e + 1]) - d.y);
+          const float x2 = __uint_as_float(s[c][e + 2]) * (__uint_as_float(p[c][e + 2]) - d.z);
+          const float x3 = __uint_as_float(s[c][e + 3]) * (__uint_as_float(p[c][e + 3]) - d.w);
+          pk[(c * 32 + e) / 2] = round_bf16x2(x0, x1);
+          pk[(c * 32 + e) / 2 + 1] = round_bf16x2(x2, x3);
+        }
+      tmem_st32(tp, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
+    const bool live = key < r.n && ok;
+    const int64_t token = r.k0 + key;
+    if (half == 0)
+      store_row(tmem + lanes + kDv, HD, 1.f, n == 0, live,
+                static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head, 0, a.head_dim);
+    else
+      store_row(tmem + lanes + kDk, HD, a.scale, n == 0, live,
+                static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head, 0, a.head_dim);
+    tc_fence_before();
+  }
+  if (!ok && lane == 0) {
+    set_error(a.status_dev, MUON_ERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+cudaError_t launch(const BwdParams& P, int dev, int64_t grid_q, int64_t grid_k, cudaStream_t st) {
+  constexpr int smem = BwdCfg<HD>::kSmemBytes;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  // the shared-memory opt-in is a per-device attribute: set it once on each device
+  static std::atomic<uint64_t> attr_devices{0};
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(attention_dq_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attention_dkv_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_devices.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  if (P.a.q_tokens > 0) {
+    attention_dq_kernel<HD><<<static_cast<unsigned>(grid_q), kThreads, smem, st>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (P.a.k_tokens > 0) attention_dkv_kernel<HD><<<static_cast<unsigned>(grid_k), kThreads, smem, st>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_backward(const muon_attention_t& a, float* delta, int dev, cudaStream_t st) {
+  BwdParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.a = a;
+  P.delta = delta;
+  if (!encode_heads_map(&P.tq, a.q, a.q_tokens, a.heads, a.head_dim, kRows) ||
+      !encode_heads_map(&P.tdo, a.dout, a.q_tokens, a.heads, a.head_dim, kRows) ||
+      !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, kRows) ||
+      !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, kRows))
+    return cudaErrorInvalidValue;
+  const int64_t grid_q = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, kRows) * a.heads;
+  const int64_t grid_k = tile_slots(a.k_offsets, a.n_seq, a.k_tokens, kRows) * a.kv_heads;
+  if (grid_q >= (int64_t(1) << 31) || grid_k >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  return a.head_dim <= 64 ? launch<64>(P, dev, grid_q, grid_k, st) : launch<128>(P, dev, grid_q, grid_k, st);
+}
+
+}  // namespace muon

@@ -50,24 +50,31 @@ bool encode_heads_map(CUtensorMap* out, const muon_heads_t& t, int64_t tokens, i
 
 namespace {
 
-constexpr int kRows = 128;          // query rows of a tile, and keys of a block
+constexpr int kRows = 128;          // query rows of a tile
 constexpr int kThreads = 384;
-constexpr int kChunk = kRows * 128; // bytes of 64 columns of a tile
 constexpr float kLazy = 8.f;        // the running maximum moves when exceeded by this (log2)
 
 template <int HD>
 struct FwdCfg {
-  static constexpr int kTileBytes = kRows * HD * 2;
-  static constexpr int kStages = HD == 128 ? 4 : 8;   // K and V blocks in flight
-  static constexpr int kOffKv = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffKv + kStages * kTileBytes;
+  // Tensor memory: the two accumulators leave 256 columns (head dimension 128) or 384 (64).
+  //   128: S in blocks of 64 keys, two buffers a tile, P over the buffer it came from
+  //   64:  S in blocks of 128 keys, one buffer a tile, and P in columns of its own
+  // Either way the next block's S is computed while this block's softmax runs.
+  static constexpr bool kOwnP = HD == 64;
+  static constexpr int kKeys = kOwnP ? 128 : 64;      // keys of a block
+  static constexpr int kHalves = kKeys / 64;          // P is handed over by 64 keys
+  static constexpr int kQBytes = kRows * HD * 2;
+  static constexpr int kQChunk = kRows * 128;         // bytes of 64 columns of a Q tile
+  static constexpr int kKvBytes = kKeys * HD * 2;
+  static constexpr int kKvChunk = kKeys * 128;
+  static constexpr int kStages = 8;                   // K and V blocks in flight
+  static constexpr int kOffKv = 2 * kQBytes;
+  static constexpr int kOffBar = kOffKv + kStages * kKvBytes;
   static constexpr int kSmemBytes = kOffBar + 512 + 1024;
   static constexpr int kO = 256;                      // first accumulator column
-  // Head dimension 64 leaves 128 columns for P of its own, so that S is free for the next
-  // product as soon as it has been read; with 128, P lies over the first half of S.
-  static constexpr bool kOwnP = HD == 64;
-  static constexpr int kP = kOwnP ? kO + 2 * HD : 0;  // P of tile 0
-  static constexpr int kPStep = kOwnP ? 64 : kRows;   // to P of tile 1
+  static constexpr int kP = kO + 2 * HD;              // P of its own: 64 columns a tile
+  __host__ __device__ static constexpr uint32_t s_col(int i, int j) { return i * 128 + (kOwnP ? 0 : (j & 1) * 64); }
+  __host__ __device__ static constexpr uint32_t p_col(int i, int j) { return kOwnP ? kP + i * 64 : s_col(i, j); }
 };
 
 struct FwdParams {
@@ -82,23 +89,10 @@ __device__ __forceinline__ void atomic_max_float(float* p, float v) {
   else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
-}
-
-template <int HD>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
-  mbar_expect_tx(bar, FwdCfg<HD>::kTileBytes);
-#pragma unroll
-  for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * kChunk, map, bar, c * 64, head, token);
 }
 
 template <int HD>
@@ -116,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   auto blocks_of = [&](int i) {  // key blocks of tile i
     const int first = row0 + i * kRows, last = min(first + kRows, r.m) - 1;
     const int keys = first >= r.m ? 0 : a.causal ? min(r.n, last + shift + 1) : r.n;
-    return keys > 0 ? (keys + kRows - 1) / kRows : 0;
+    return keys > 0 ? (keys + C::kKeys - 1) / C::kKeys : 0;
   };
   const int nb0 = blocks_of(0), nb1 = blocks_of(1), nmax = max(nb0, nb1);
 
@@ -126,14 +120,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // ring of K and V blocks
   uint64_t* empty = full + C::kStages;
   uint64_t* q_full = empty + C::kStages;
-  uint64_t* s_full = q_full + 1;   // per tile: S is complete (and the product before it)
-  uint64_t* s_read = s_full + 2;   // per tile: S is in registers
-  uint64_t* p_full = s_read + 2;   // per tile and half: P of 64 keys is in place
-  uint64_t* o_full = p_full + 4;   // per tile: the product with V is complete
-  uint64_t* turn = o_full + 2;     // per tile and warp: its exponentials of the block are done
+  // A barrier that may complete for block j + 1 before block j has been waited for exists once
+  // per block parity.
+  uint64_t* s_full = q_full + 1;   // per tile and block parity: S is complete
+  uint64_t* s_read = s_full + 4;   // per tile: S is in registers (own P)
+  uint64_t* p_full = s_read + 2;   // per tile, and half (own P) or block parity: 64 keys of P
+  uint64_t* o_full = p_full + 4;   // per tile and block parity: the product with V is complete
+  uint64_t* turn = o_full + 4;     // per tile and warp: its exponentials of the block are done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (2 * C::kStages + 19) + 8 <= 512, "barrier region");
+  static_assert(8 * (2 * C::kStages + 23) + 8 <= 512, "barrier region");
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -143,11 +139,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     }
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[2 * i], 1);
+      mbar_init(&s_full[2 * i + 1], 1);
       mbar_init(&s_read[i], 4);
       mbar_init(&p_full[2 * i], 4);
       mbar_init(&p_full[2 * i + 1], 4);
-      mbar_init(&o_full[i], 1);
+      mbar_init(&o_full[2 * i], 1);
+      mbar_init(&o_full[2 * i + 1], 1);
       for (int w = 0; w < 4; ++w) mbar_init(&turn[4 * i + w], 1);
     }
     *abort_flag = 0;
@@ -162,10 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  // Ring positions of the K and V blocks, in the order of use. With P of its own the next
-  // block's S is computed while this block's softmax runs, so K_{j+1} comes before V_j.
-  auto pos_k = [&](int j) { return C::kOwnP ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
-  auto pos_v = [&](int j) { return C::kOwnP ? (j + 1 < nmax ? 2 * j + 2 : 2 * nmax - 1) : 2 * j + 1; };
+  // Ring positions of the K and V blocks, in the order of use: K_{j+1} before V_j.
+  auto pos_k = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
+  auto pos_v = [&](int j) { return j + 1 < nmax ? 2 * j + 2 : 2 * nmax - 1; };
 
   // Registers: 384 x 168 at launch; 128 x 56 + 256 x 224 is the same total.
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -173,10 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && nmax > 0) {
       const int kvh = head / (heads / a.kv_heads);
-      mbar_expect_tx(q_full, 2 * C::kTileBytes);
+      mbar_expect_tx(q_full, 2 * C::kQBytes);
       for (int i = 0; i < 2; ++i)
         for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(smem + i * C::kTileBytes + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
+          tma_load_3d(smem + i * C::kQBytes + c * C::kQChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
       bool ok = true;
       int loads = 0, j[2] = {0, 0};  // the next K and V block
       for (int t = 0; t < 2 * nmax; ++t) {
@@ -186,8 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           ok = false;
           break;
         }
-        load_tile<HD>(smem + C::kOffKv + s * C::kTileBytes, is_v ? &P.tv : &P.tk, &full[s], kvh,
-                      r.k0 + (is_v ? j[1]++ : j[0]++) * kRows);
+        uint8_t* dst = smem + C::kOffKv + s * C::kKvBytes;
+        const int key = r.k0 + (is_v ? j[1]++ : j[0]++) * C::kKeys;
+        mbar_expect_tx(&full[s], C::kKvBytes);
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(dst + c * C::kKvChunk, is_v ? &P.tv : &P.tk, &full[s], c * 64, kvh, key);
         ++loads;
       }
       if (!ok) {
@@ -203,58 +203,61 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     // ------------------------------------------------------------ MMA issuers, one per tile
     const int i = warp - 1, n = i == 0 ? nb0 : nb1;
     if (n > 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false), idesc_o = idesc_bf16_f32(128, HD, true);
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kKeys, false), idesc_o = idesc_bf16_f32(128, HD, true);
       // low words of the operand descriptors: address and leading offset, both / 16
-      constexpr uint32_t kmaj = 1u << 16, mn = static_cast<uint32_t>(kChunk >> 4) << 16;
+      constexpr uint32_t kmaj = 1u << 16, mn = static_cast<uint32_t>(C::kKvChunk >> 4) << 16;
       const uint32_t base = smem_u32(smem) >> 4;
-      const uint32_t qd = kmaj | (base + i * (C::kTileBytes >> 4));
-      const uint32_t ts = tmem + i * kRows, tp = tmem + C::kP + i * C::kPStep, to = tmem + C::kO + i * HD;
+      const uint32_t qd = kmaj | (base + i * (C::kQBytes >> 4));
+      const uint32_t to = tmem + C::kO + i * HD;
       auto slot_of = [&](int t) { return t % C::kStages; };
       auto wait_bar = [&](uint64_t* bar, int phase) {
         const bool got = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag));
         tc_fence_after();
         return got;
       };
-      auto qk = [&](int j) {  // S = Q K_j^T, then K_j is free
+      // S = Q K_j^T, then K_j is free. The buffer is: read (own P), or the P of two blocks ago,
+      // whose product was issued before.
+      auto qk = [&](int j) {
         const int t = pos_k(j);
         if (!wait_bar(&full[slot_of(t)], t / C::kStages)) return false;
         if (C::kOwnP && j > 0 && !wait_bar(&s_read[i], j - 1)) return false;
         if (elect_one()) {
-          const uint32_t kd = kmaj | (base + ((C::kOffKv + slot_of(t) * C::kTileBytes) >> 4));
+          const uint32_t kd = kmaj | (base + ((C::kOffKv + slot_of(t) * C::kKvBytes) >> 4));
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
-            umma_f16_lo(ts, qd + off, kd + off, kDescHi, idesc_s, k != 0);
+            const uint32_t in = (k & 3) * 2, c = k >> 2;
+            umma_f16_lo(tmem + C::s_col(i, j), qd + c * (C::kQChunk >> 4) + in, kd + c * (C::kKvChunk >> 4) + in,
+                        kDescHi, idesc_s, k != 0);
           }
-          umma_commit(&s_full[i]);
+          umma_commit(&s_full[2 * i + (j & 1)]);
           umma_commit(&empty[slot_of(t)]);
         }
         return true;
       };
       auto pv = [&](int j) {  // O += P V_j, by halves of the keys as P arrives, then V_j is free
-        const int t = pos_v(j), s = slot_of(t), live = r.n - j * kRows;
+        const int t = pos_v(j), s = slot_of(t), live = r.n - j * C::kKeys;
         if (!wait_bar(&full[s], t / C::kStages)) return false;
-        if (live < kRows) {
+        if (live < C::kKeys) {
           // Keys past the sequence have probability 0, and their V must not be NaN. Both
           // issuers write these zeros; whichever is later writes over zeros.
-          uint8_t* v = smem + C::kOffKv + s * C::kTileBytes;
-          for (int e = live * 8 + lane; e < kRows * 8; e += 32)
+          uint8_t* v = smem + C::kOffKv + s * C::kKvBytes;
+          for (int e = live * 8 + lane; e < C::kKeys * 8; e += 32)
 #pragma unroll
             for (int c = 0; c < HD / 64; ++c)
-              *reinterpret_cast<uint4*>(v + c * kChunk + e * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + c * C::kKvChunk + e * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint32_t vd = mn | (base + ((C::kOffKv + s * C::kTileBytes) >> 4));
+        const uint32_t vd = mn | (base + ((C::kOffKv + s * C::kKvBytes) >> 4));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait_bar(&p_full[2 * i + h], j)) return false;
+        for (int h = 0; h < C::kHalves; ++h) {
+          if (!(C::kOwnP ? wait_bar(&p_full[2 * i + h], j) : wait_bar(&p_full[2 * i + (j & 1)], j >> 1))) return false;
           if (elect_one()) {
 #pragma unroll
             for (int k = 4 * h; k < 4 * h + 4; ++k)
-              umma_f16_ts_lo(to, tp + k * 8, vd + 128u * k, kDescHi, idesc_o, (j | k) != 0);
-            if (h == 1) {
-              umma_commit(&o_full[i]);
+              umma_f16_ts_lo(to, tmem + C::p_col(i, j) + k * 8, vd + 128u * k, kDescHi, idesc_o, (j | k) != 0);
+            if (h == C::kHalves - 1) {
+              umma_commit(&o_full[2 * i + (j & 1)]);
               umma_commit(&empty[s]);
             }
           }
@@ -269,12 +272,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       };
       bool ok = wait_bar(q_full, 0) && qk(0);
       for (int j = 0; j < nmax && ok; ++j) {
-        if (C::kOwnP && j + 1 < nmax) ok = j + 1 < n ? qk(j + 1) : skip(pos_k(j + 1));
+        if (j + 1 < nmax) ok = j + 1 < n ? qk(j + 1) : skip(pos_k(j + 1));
         ok = ok && (j < n ? pv(j) : skip(pos_v(j)));
-        if (!C::kOwnP && ok && j + 1 < nmax) ok = j + 1 < n ? qk(j + 1) : skip(pos_k(j + 1));
       }
       // never leave with products still running
-      ok = ok && wait_bar(&o_full[i], n - 1);
+      ok = ok && wait_bar(&o_full[2 * i + ((n - 1) & 1)], (n - 1) >> 1);
       if (!ok && lane == 0) {
         set_error(a.status_dev, MUON_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -286,21 +288,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     const int i = (warp - 4) / 4, w = warp & 3, nbi = i == 0 ? nb0 : nb1;
     const int row = row0 + i * kRows + w * 32 + lane;  // within the sequence
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * kRows, to = tmem + lanes + C::kO + i * HD, tp = tmem + lanes + C::kP + i * C::kPStep;
+    const uint32_t to = tmem + lanes + C::kO + i * HD;
+    constexpr int kParts = C::kKeys / 32;
     const float sl = a.scale * 1.4426950408889634f;
     float top = -INFINITY;            // largest logit so far, unscaled
     float ref = 0.f;                  // the exponent's reference, scaled
     float sum = 0.f;
     bool ok = true;
+    auto wait_o = [&](int j) {  // the product of block j is complete
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&o_full[2 * i + (j & 1)], static_cast<uint32_t>((j >> 1) & 1), abort_flag));
+      tc_fence_after();
+      return got;
+    };
     for (int j = 0; j < nbi; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[i], static_cast<uint32_t>(j & 1), abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[2 * i + (j & 1)], static_cast<uint32_t>((j >> 1) & 1), abort_flag))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s[4][32];
+      uint32_t s[kParts][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
+      for (int c = 0; c < kParts; ++c) tmem_ld32(tmem + lanes + C::s_col(i, j) + c * 32, s[c]);
       tmem_wait_ld();
       if (C::kOwnP) {
         tc_fence_before();
@@ -308,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         if (lane == 0) mbar_arrive(&s_read[i]);
       }
       // keys of this block that the row sees
-      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows;
-      if (__any_sync(0xffffffffu, vis < kRows)) {
+      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * C::kKeys;
+      if (__any_sync(0xffffffffu, vis < C::kKeys)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < kParts; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (c * 32 + e >= vis) s[c][e] = 0xFF800000u;
@@ -320,19 +328,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
 #pragma unroll
       for (int e = 0; e < 32; e += 2)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+        for (int c = 0; c < kParts; ++c)
+          m[2 * (c & 1) + (e / 2 & 1)] = max3(m[2 * (c & 1) + (e / 2 & 1)], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
       top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
       const float want = top == -INFINITY ? 0.f : top * sl;
       if (j == 0) {
         ref = want;
       } else {
-        // the product of the block before is long complete: O may be rescaled, P written
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], static_cast<uint32_t>((j - 1) & 1), abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-        // a row that sees any key sees the first, so ref is a maximum from block 0 on
+        // The product that read the columns P goes to is complete (long ago).
+        const int jp = j - (C::kOwnP ? 1 : 2);
+        if (jp >= 0) {
+          ok = wait_o(jp);
+          if (!ok) break;
+        }
         const bool move = want > ref + kLazy;
         if (__any_sync(0xffffffffu, move)) {
+          if (!C::kOwnP) {  // and so is the one before this block: O may be rescaled
+            ok = wait_o(j - 1);
+            if (!ok) break;
+          }
           const float f = move ? ex2(ref - want) : 1.f;
           if (move) ref = want;
           sum *= f;
@@ -349,13 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       }
       // Two warps, one of each tile, share a scheduler and its exponential unit: they take
       // turns, so that one's maximum and transfers overlap the other's exponentials.
-      if (i == 0 ? j > 0 && j <= nb1 : j < nb0) {
+      if (C::kOwnP && (i == 0 ? j > 0 && j <= nb1 : j < nb0)) {
         ok = __all_sync(0xffffffffu, mbar_wait(&turn[4 * (1 - i) + w], static_cast<uint32_t>((i == 0 ? j - 1 : j) & 1), abort_flag));
         if (!ok) break;
       }
       float add[4] = {sum, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < C::kHalves; ++h) {
         uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -366,15 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           add[2 * (e & 1) + 1] += p1;
           pk[e] = round_bf16x2(p0, p1);
         }
-        if (h == 1) {
+        if (C::kOwnP && h == C::kHalves - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&turn[4 * i + w]);
         }
-        tmem_st32(tp + h * 32, pk);
+        tmem_st32(tmem + lanes + C::p_col(i, j) + h * 32, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * i + h]);
+        if (lane == 0) mbar_arrive(&p_full[2 * i + (C::kOwnP ? h : j & 1)]);
       }
       sum = (add[0] + add[1]) + (add[2] + add[3]);
     }
@@ -383,9 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       *abort_flag = 1;
     }
     if (nbi > 0 && ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[i], static_cast<uint32_t>((nbi - 1) & 1), abort_flag));
+      ok = wait_o(nbi - 1);
       if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
-      tc_fence_after();
     }
     const bool live = row < r.m, seen = top > -INFINITY || sum != 0.f;
     const float inv = seen ? 1.f / sum : 0.f;
@@ -451,9 +464,10 @@ cudaError_t launch_attention_forward(const muon_attention_t& a, int dev, cudaStr
   FwdParams P;
   std::memset(&P, 0, sizeof(P));
   P.a = a;
+  const int keys = a.head_dim <= 64 ? FwdCfg<64>::kKeys : FwdCfg<128>::kKeys;
   if (!encode_heads_map(&P.tq, a.q, a.q_tokens, a.heads, a.head_dim, kRows) ||
-      !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, kRows) ||
-      !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, kRows))
+      !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, keys) ||
+      !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, keys))
     return cudaErrorInvalidValue;
   const int64_t grid = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, 2 * kRows) * a.heads;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
