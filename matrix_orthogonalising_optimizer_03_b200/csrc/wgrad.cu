@@ -46,58 +46,85 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace {
 
-constexpr int kTile = 256;                    // tile rows (out) and columns (in) of a CTA pair
+constexpr int kIn = 256;                      // tile columns (in) of a CTA pair
 constexpr int kTok = 64;                      // tokens per k-block
-constexpr int kYBytes = 128 * kTok * 2;       // a CTA's dY columns of one k-block
-constexpr int kQBytes = 128 * kTok;           // its stored X columns
+constexpr int kQBytes = 128 * kTok;           // a CTA's stored X columns of one k-block
 constexpr int kEBytesRow = 16;                // exponents of 512 columns, the smallest TMA row
 constexpr int kEBytes = kEBytesRow * kTok;
-constexpr int kOffE = kYBytes + kQBytes;
-constexpr int kStageBytes = kOffE + kEBytes;
 constexpr int kStages = 8;
 constexpr int kTeams = 2, kTeamWarps = 4;     // restore teams take k-blocks in turn
 constexpr int kRestoreWarps = kTeams * kTeamWarps, kEpiWarps = 8;
 constexpr int kFirstEpi = 2 + kRestoreWarps;
 constexpr int kThreads = 32 * (2 + kRestoreWarps + kEpiWarps);
-constexpr int kOffBar = kStages * kStageBytes;
-constexpr int kSmemBytes = kOffBar + 256 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kTmemX = 256;                   // first tensor-memory column of the X^T stages
 constexpr int kXCols = kTok / 2;              // columns of one stage
 static_assert(kTmemX + kStages * kXCols <= 512, "tensor memory");
 constexpr int kPairs = 74;                    // CTA pairs of a B200 (148 SMs)
-constexpr size_t kPartBytes = size_t(kTile) * kTile * 4;
+
+// N: tile rows (out) of a CTA pair, half of them from each CTA's dY columns.
+template <int N>
+struct WgradCfg {
+  static constexpr int kAcc = 256 / N;        // accumulators in tensor memory
+  static constexpr int kYBytes = N / 2 * kTok * 2;
+  static constexpr int kOffE = kYBytes + kQBytes;
+  static constexpr int kStageBytes = kOffE + kEBytes;
+  static constexpr int kOffBar = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kOffBar + 256 + 1024;
+  static_assert(kSmemBytes <= 227 * 1024 && kStageBytes % 1024 == 0, "shared memory");
+};
 
 // How the tiles are dealt: `whole` tiles by one unit each, the `left` ones by `splits` units.
 struct WgradSplit {
+  int32_t n;                 // tile rows, 256 or 128
   int32_t tiles_o, tiles_i;
-  int64_t tiles, whole, left;
   int32_t splits;
+  int64_t whole, left;
   int64_t units;
+  size_t part_bytes;
 };
 
-// A k-block takes about 0.3 us of a pair; partial sums and the second launch cost about 4 us,
-// so the last round is split where that saves at least 16 k-blocks, into parts of 4 or more.
+// Picks the tile height and the split of the last round by a model of their time in cycles:
+// a round costs its k-blocks (620 cycles at 256 rows, where the products are the limit;
+// 400 at 128 rows, where restoring X is) and what its start and its epilogue add that
+// nothing hides (6000 and 3500: one accumulator of 256 columns against two of 128);
+// partial sums and the second launch cost about 7000. Tiles of 128 rows waste less of a small
+// or ragged `out`, and hide the epilogue of short groups.
 WgradSplit split_of(const muon_weight_grad_t& a) {
-  WgradSplit s;
-  s.tiles_o = static_cast<int32_t>((a.out + kTile - 1) / kTile);
-  s.tiles_i = static_cast<int32_t>((a.in + kTile - 1) / kTile);
-  s.tiles = static_cast<int64_t>(s.tiles_o) * s.tiles_i * a.groups;
-  s.whole = s.tiles / kPairs * kPairs;
-  s.left = s.tiles - s.whole;
-  s.splits = 1;
-  if (s.left > 0) {
-    const int64_t kb = (a.tokens / a.groups + kTok - 1) / kTok;  // of a mean group
-    int64_t n = kPairs / s.left;
-    if (n > kb / 4) n = kb / 4;
-    if (n > 1 && kb - kb / n >= 16) s.splits = static_cast<int32_t>(n);
+  const int64_t kb = (a.tokens / a.groups + kTok - 1) / kTok;  // of a mean group
+  WgradSplit best{};
+  double best_cost = 0;
+  for (int n = 256; n >= 128; n /= 2) {
+    const double per_kb = n == 256 ? 620. : 400., fixed = n == 256 ? 6000. : 3500.;
+    WgradSplit s{};
+    s.n = n;
+    s.tiles_o = static_cast<int32_t>((a.out + n - 1) / n);
+    s.tiles_i = static_cast<int32_t>((a.in + kIn - 1) / kIn);
+    s.part_bytes = static_cast<size_t>(n) * kIn * 4;
+    const int64_t tiles = static_cast<int64_t>(s.tiles_o) * s.tiles_i * a.groups;
+    for (int split = 0; split < 2; ++split) {
+      s.whole = tiles;
+      s.left = 0;
+      s.splits = 1;
+      double cost = static_cast<double>((tiles + kPairs - 1) / kPairs) * (kb * per_kb + fixed);
+      if (split) {
+        s.whole = tiles / kPairs * kPairs;
+        s.left = tiles - s.whole;
+        if (s.left == 0) break;
+        int64_t parts = kPairs / s.left;
+        if (parts > kb / 4) parts = kb / 4;  // at least 4 k-blocks each
+        if (parts < 2) break;
+        s.splits = static_cast<int32_t>(parts);
+        cost = static_cast<double>(s.whole / kPairs) * (kb * per_kb + fixed) +
+               (kb + parts - 1) / parts * per_kb + fixed + 7000.;
+      }
+      s.units = s.whole + s.left * s.splits;
+      if (best.n == 0 || cost < best_cost) {
+        best = s;
+        best_cost = cost;
+      }
+    }
   }
-  if (s.splits == 1) {
-    s.whole = s.tiles;
-    s.left = 0;
-  }
-  s.units = s.whole + s.left * s.splits;
-  return s;
+  return best;
 }
 
 struct WgradParams {
@@ -135,6 +162,7 @@ struct Job {
   int part;         // partial sum, or -1: dW
 };
 
+template <int N>
 __device__ __forceinline__ Job job_of(const WgradParams& P, int64_t u) {
   Job j;
   int64_t t = u;
@@ -149,8 +177,8 @@ __device__ __forceinline__ Job job_of(const WgradParams& P, int64_t u) {
   const int per = P.s.tiles_o * P.s.tiles_i;
   j.g = static_cast<int>(t / per);
   const int rem = static_cast<int>(t - static_cast<int64_t>(j.g) * per);
-  j.o0 = rem / P.s.tiles_i * kTile;
-  j.i0 = rem % P.s.tiles_i * kTile;
+  j.o0 = rem / P.s.tiles_i * N;
+  j.i0 = rem % P.s.tiles_i * kIn;
   int lo, hi;
   group_range(P.a, j.g, &lo, &hi);
   if (j.part >= 0) {
@@ -201,43 +229,74 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
 
 // D (both CTAs' tensor memory) (+)= A (both CTAs' tensor memory, M split) * B (both CTAs'
 // shared memory, N split)^T.
-__device__ __forceinline__ void umma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+__device__ __forceinline__ void umma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
       : "memory");
 }
 
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(uint16_t* p, float x) { *p = f32_to_bf16(x); }
+
+// Up to 32 rows of one column, ld apart: the lanes of a warp write 32 neighbours of each row.
+template <class T>
+__device__ __forceinline__ void write_rows(T* p, int64_t ld, int n, bool accumulate, uint32_t (&v)[32]) {
+  if (accumulate) {
+    T old[32];
+    const T* q = p;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, q += ld) old[i] = i < n ? *q : T(0);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + widen(old[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i, p += ld)
+    if (i < n) put(p, __uint_as_float(v[i]));
+}
+
+template <int N>
 __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constant__ WgradParams P) {
+  using C = WgradCfg<N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // this CTA's loads have landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // this CTA's loads have landed
   uint64_t* ready = full + kStages;   // first CTA's: both CTAs' operands are in place
   uint64_t* empty = ready + kStages;  // the MMAs have read the stage
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 1;
-  uint64_t* done = tempty + 1;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (3 * kStages + 3) + 8 <= 256, "barrier region");
+  static_assert(8 * (3 * kStages + 5) + 8 <= 256, "barrier region");
 
   const muon_weight_grad_t& a = P.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_cta_rank());
   const int64_t unit0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
+  if (threadIdx.x == 32 * kFirstEpi && a.tokens > 0) {
+    tma_prefetch(&P.tq);
+    tma_prefetch(&P.te);
+    tma_prefetch(&P.ty);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&ready[s], 2 * kTeamWarps);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * kEpiWarps);
+    for (int b = 0; b < C::kAcc; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);
+    }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -250,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -260,19 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       int64_t loads = 0;
       bool ok = true;
       for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
-        const Job j = job_of(P, u);
+        const Job j = job_of<N>(P, u);
         for (int kb = 0; kb < j.nkb; ++kb) {
           if (!mbar_wait(&empty[s], par ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * kStageBytes;
-          const int t = j.t0 + kb * kTok, o = j.o0 + rank * 128, i = j.i0 + rank * 128;
-          mbar_expect_tx(&full[s], kStageBytes);
-          tma_load_3d(st + kYBytes, &P.tq, &full[s], i, t, 0);
-          tma_load_3d(st + kOffE, &P.te, &full[s], i / 512 * kEBytesRow, t, 0);
-          tma_load_3d(st, &P.ty, &full[s], o, t, 0);
-          tma_load_3d(st + kYBytes / 2, &P.ty, &full[s], o + 64, t, 0);
+          uint8_t* st = smem + s * C::kStageBytes;
+          const int t = j.t0 + kb * kTok, o = j.o0 + rank * (N / 2), i = j.i0 + rank * 128;
+          mbar_expect_tx(&full[s], C::kStageBytes);
+          tma_load_3d(st + C::kYBytes, &P.tq, &full[s], i, t, 0);
+          tma_load_3d(st + C::kOffE, &P.te, &full[s], i / 512 * kEBytesRow, t, 0);
+#pragma unroll
+          for (int c = 0; c < N / 128; ++c)
+            tma_load_3d(st + c * (64 * kTok * 2), &P.ty, &full[s], o + 64 * c, t, 0);
           ++loads;
           if (++s == kStages) s = 0, par ^= 1u;
         }
@@ -287,45 +347,51 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(256, 256, true);  // A from tensor memory, B MN-major
-      const uint64_t mn = smem_desc_sw128(0, 64 * kTok * 2, 1024);
-      int s = 0;
-      uint32_t par = 0, tpar = 0;
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, N, true);  // A from tensor memory, B MN-major
+      constexpr uint32_t mn = static_cast<uint32_t>((64 * kTok * 2) >> 4) << 16;
+      const uint32_t base = smem_u32(smem) >> 4;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        tc_fence_after();
+        return got;
+      };
+      int s = 0, it = 0;
+      uint32_t par = 0;
       bool ok = true;
       for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
-        const Job j = job_of(P, u);
+        const Job j = job_of<N>(P, u);
         if (j.nkb == 0) continue;
-        if (!mbar_wait(tempty, tpar ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tpar ^= 1u;
-        tc_fence_after();
-        for (int kb = 0; kb < j.nkb; ++kb) {
-          if (!mbar_wait(&ready[s], par, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t bd = mn | static_cast<uint64_t>((smem_u32(smem + s * kStageBytes) >> 4) & 0x3FFFu);
-          const uint32_t at = tmem + kTmemX + s * kXCols;
+        const int acc = it % C::kAcc;
+        ok = wait(&tempty[acc], static_cast<uint32_t>((it / C::kAcc) & 1) ^ 1u);
+        ++it;
+        const uint32_t d = tmem + acc * N;
+        for (int kb = 0; kb < j.nkb && ok; ++kb) {
+          ok = wait(&ready[s], par);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t bd = mn | (base + s * (C::kStageBytes >> 4));
+            const uint32_t at = tmem + kTmemX + s * kXCols;
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens: 8 columns, 2 KB of a chunk
-            umma_f16_pair_ts(tmem, at + 8u * kk, bd + 128u * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
-          umma_commit_pair(smem_u32(&empty[s]));
-          umma_commit_pair(peer_addr(&empty[s], 1));
+            for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens: 8 columns, 2 KB of a chunk
+              umma_f16_pair_ts(d, at + 8u * kk, bd + 128u * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
+            umma_commit_pair(smem_u32(&empty[s]));
+            umma_commit_pair(peer_addr(&empty[s], 1));
+            if (kb + 1 == j.nkb) {
+              umma_commit_pair(smem_u32(&tfull[acc]));
+              umma_commit_pair(peer_addr(&tfull[acc], 1));
+            }
+          }
           if (++s == kStages) s = 0, par ^= 1u;
         }
-        if (!ok) break;
-        umma_commit_pair(smem_u32(tfull));
-        umma_commit_pair(peer_addr(tfull, 1));
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_error(a.status_dev, MUON_ERR_TIMEOUT);
         *abort_flag = 1;
       }
-      umma_commit_pair(smem_u32(done));
+      // never leave with products still running
+      if (elect_one()) umma_commit_pair(smem_u32(done));
+      __syncwarp();
       mbar_wait(done, 0, nullptr);
     }
   } else if (warp < kFirstEpi) {
@@ -338,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     int64_t q0 = 0;  // k-blocks of the units before this one
     bool ok = true;
     for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
-      const Job j = job_of(P, u);
+      const Job j = job_of<N>(P, u);
       const int grp = ((j.i0 + rank * 128) / 32 + w) % kEBytesRow;  // within a stage's exponent row
       const int src = (grp & 7) * 4 + (lane & 3);
       for (int kb = static_cast<int>((team - q0) & 1); kb < j.nkb; kb += kTeams) {
@@ -352,13 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           }
           break;
         }
-        uint8_t* st = smem + s * kStageBytes;
+        uint8_t* st = smem + s * C::kStageBytes;
         const int live = j.t1 - (j.t0 + kb * kTok);  // tokens of the group from this k-block on
         uint32_t sc[4][2];  // scales of tokens 16 b + 4 (lane % 4) + {0, 1}, {2, 3}
 #pragma unroll
         for (int b = 0; b < 4; b += 2) {
           uint32_t e[4];
-          ldmatrix_b8_x2_trans(smem_u32(st + kOffE + (16 * b + lane) * kEBytesRow), e);
+          ldmatrix_b8_x2_trans(smem_u32(st + C::kOffE + (16 * b + lane) * kEBytesRow), e);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t x0 = __shfl_sync(0xffffffffu, e[2 * h], src), x1 = __shfl_sync(0xffffffffu, e[2 * h + 1], src);
@@ -377,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
             }
           // the dY of tokens past the group: zeros too
           for (int t = live + w; t < kTok; t += kTeamWarps)
-            *reinterpret_cast<uint2*>(st + (lane >> 4) * (kYBytes / 2) + t * 128 + (lane & 15) * 8) = make_uint2(0, 0);
+            if (lane < N / 8) *reinterpret_cast<uint2*>(st + (lane >> 4) * (64 * kTok * 2) + t * 128 + (lane & 15) * 8) = make_uint2(0, 0);
           fence_proxy_async_smem();
         }
         uint32_t x[2][16];
@@ -385,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
         for (int b = 0; b < 4; ++b) {
           const int t = 16 * b + (lane & 15);
           uint32_t v[4];
-          ldmatrix_b8_x2_trans(smem_u32(st + kYBytes + t * 128 + (((2 * w + (lane >> 4)) ^ (t & 7)) << 4)), v);
+          ldmatrix_b8_x2_trans(smem_u32(st + C::kYBytes + t * 128 + (((2 * w + (lane >> 4)) ^ (t & 7)) << 4)), v);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             restore4(v[2 * h], sc[b], &x[h][4 * b], &x[h][4 * b + 1]);
@@ -407,15 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int w = warp & 3;                          // the TMEM lane quarter this warp may access
-    const int half = (warp - kFirstEpi) / 4 * 128;   // and its half of the tile's rows of dW
-    uint32_t tpar = 0;
+    const int w = warp & 3;                              // the TMEM lane quarter this warp may access
+    const int half = (warp - kFirstEpi) / 4 * (N / 2);   // and its half of the tile's rows of dW
+    int it = 0;
     bool ok = true;
     for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
-      const Job j = job_of(P, u);
+      const Job j = job_of<N>(P, u);
       if (j.nkb == 0 && (j.part >= 0 || a.accumulate)) continue;
+      const int acc = it % C::kAcc;
       if (j.nkb > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull, tpar, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], static_cast<uint32_t>((it / C::kAcc) & 1), abort_flag))) {
           ok = false;
           if (lane == 0) {
             set_error(a.status_dev, MUON_ERR_TIMEOUT);
@@ -423,63 +490,40 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           }
           break;
         }
-        tpar ^= 1u;
+        ++it;
         tc_fence_after();
       }
       const int c0 = rank * 128 + w * 32 + lane, col = j.i0 + c0;
-      const int rows = min(128, static_cast<int>(a.out) - j.o0 - half);
+      const int rows = min(N / 2, static_cast<int>(a.out) - j.o0 - half);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < N / 64; ++c) {
         uint32_t v[32];
         if (j.nkb > 0) {
-          tmem_ld32(tmem + (static_cast<uint32_t>(w * 32) << 16) + static_cast<uint32_t>(half + c * 32), v);
+          tmem_ld32(tmem + (static_cast<uint32_t>(w * 32) << 16) + static_cast<uint32_t>(acc * N + half + c * 32), v);
           tmem_wait_ld();
-          if (c == 3) {
+          if (c == N / 64 - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              if (rank == 0) mbar_arrive(tempty);
-              else mbar_arrive_peer(peer_addr(tempty, 0));
+              if (rank == 0) mbar_arrive(&tempty[acc]);
+              else mbar_arrive_peer(peer_addr(&tempty[acc], 0));
             }
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
-        if (col >= a.in) continue;
         const int n = rows - c * 32;
+        if (col >= a.in || n <= 0) continue;
         if (j.part >= 0) {
-          float* p = P.parts + static_cast<int64_t>(j.part) * (kTile * kTile) + (half + c * 32) * kTile + c0;
+          float* p = P.parts + static_cast<int64_t>(j.part) * (N * kIn) + (half + c * 32) * kIn + c0;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (i < n) p[i * kTile] = __uint_as_float(v[i]);
+            if (i < n) p[i * kIn] = __uint_as_float(v[i]);
         } else {
           const int64_t at = j.g * a.stride_w + (j.o0 + half + c * 32) * a.ld_w + col;
-          if (a.w_dtype == MUON_F32) {
-            float* p = static_cast<float*>(a.dW) + at;
-            if (a.accumulate) {
-              float old[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) old[i] = i < n ? p[i * a.ld_w] : 0.f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + old[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n) p[i * a.ld_w] = __uint_as_float(v[i]);
-          } else {
-            uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
-            if (a.accumulate) {
-              uint16_t old[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) old[i] = i < n ? p[i * a.ld_w] : 0;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + bf16_to_f32(old[i]));
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n) p[i * a.ld_w] = f32_to_bf16(__uint_as_float(v[i]));
-          }
+          if (a.w_dtype == MUON_F32) write_rows(static_cast<float*>(a.dW) + at, a.ld_w, n, a.accumulate != 0, v);
+          else write_rows(static_cast<uint16_t*>(a.dW) + at, a.ld_w, n, a.accumulate != 0, v);
         }
       }
     }
@@ -493,37 +537,51 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   }
 }
 
-// Adds the partial sums of the split tiles in order: a block per 8 rows of a tile, a thread
-// per column.
-__global__ void __launch_bounds__(kTile) wgrad_join_kernel(const __grid_constant__ WgradParams P) {
+// Adds the partial sums of the split tiles in order: a block per 4 rows of a tile, a thread per
+// 4 columns of one row, kBatch partial sums in flight.
+template <int N>
+__global__ void __launch_bounds__(kIn) wgrad_join_kernel(const __grid_constant__ WgradParams P) {
+  constexpr int kBatch = 8;
   const muon_weight_grad_t& a = P.a;
-  const int64_t r = blockIdx.x / (kTile / 8);
-  const int row0 = blockIdx.x % (kTile / 8) * 8;
-  const Job j = job_of(P, P.s.whole + r * P.s.splits);
+  const int64_t r = blockIdx.x / (N / 4);
+  const int row = blockIdx.x % (N / 4) * 4 + threadIdx.x / 64, c0 = threadIdx.x % 64 * 4;
+  const Job j = job_of<N>(P, P.s.whole + r * P.s.splits);
   int lo, hi;
   group_range(a, j.g, &lo, &hi);
-  const int64_t kb = (hi - lo + kTok - 1) / kTok;
-  const int col = j.i0 + threadIdx.x;
-  if (col >= a.in) return;
-  float sum[8] = {};
-  for (int s = 0; s < P.s.splits; ++s) {
-    if (kb * s / P.s.splits == kb * (s + 1) / P.s.splits) continue;  // a part without tokens
-    const float* p = P.parts + (r * P.s.splits + s) * (kTile * kTile) + row0 * kTile + threadIdx.x;
+  const int64_t o = j.o0 + row;
+  const int kb = (hi - lo + kTok - 1) / kTok, splits = P.s.splits, cols = static_cast<int>(a.in) - j.i0 - c0;
+  if (o >= a.out || cols <= 0) return;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* p = P.parts + r * splits * (N * kIn) + row * kIn + c0;
+  for (int s0 = 0; s0 < splits; s0 += kBatch) {
+    float4 v[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (j.o0 + row0 + i < a.out) sum[i] += __ldcs(p + i * kTile);
+    for (int b = 0; b < kBatch; ++b) {
+      const int s = s0 + b;
+      // a part without tokens has no partial sum
+      const bool have = s < splits && static_cast<int64_t>(kb) * s / splits != static_cast<int64_t>(kb) * (s + 1) / splits;
+      v[b] = have ? __ldcs(reinterpret_cast<const float4*>(p + static_cast<int64_t>(s) * (N * kIn)))
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      sum.x += v[b].x;
+      sum.y += v[b].y;
+      sum.z += v[b].z;
+      sum.w += v[b].w;
+    }
   }
+  const float x[4] = {sum.x, sum.y, sum.z, sum.w};
+  const int64_t at = j.g * a.stride_w + o * a.ld_w + j.i0 + c0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t o = j.o0 + row0 + i;
-    if (o >= a.out) return;
-    const int64_t at = j.g * a.stride_w + o * a.ld_w + col;
+  for (int i = 0; i < 4; ++i) {
+    if (i >= cols) break;
     if (a.w_dtype == MUON_F32) {
-      float* p = static_cast<float*>(a.dW) + at;
-      *p = a.accumulate ? *p + sum[i] : sum[i];
+      float* w = static_cast<float*>(a.dW) + at + i;
+      put(w, a.accumulate ? *w + x[i] : x[i]);
     } else {
-      uint16_t* p = static_cast<uint16_t*>(a.dW) + at;
-      *p = f32_to_bf16(a.accumulate ? bf16_to_f32(*p) + sum[i] : sum[i]);
+      uint16_t* w = static_cast<uint16_t*>(a.dW) + at + i;
+      put(w, a.accumulate ? widen(*w) + x[i] : x[i]);
     }
   }
 }
@@ -581,6 +639,36 @@ muon_status_t validate_weight_grad(const muon_weight_grad_t* p) {
   return MUON_OK;
 }
 
+template <int N>
+cudaError_t launch_wgrad(const WgradParams& P, int dev, int sms, cudaStream_t st) {
+  using C = WgradCfg<N>;
+  // the shared-memory opt-in is a per-device attribute: set it once on each device
+  static std::atomic<uint64_t> attr_devices{0};
+  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
+  if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_devices.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t pairs = P.s.units < sms / 2 ? P.s.units : sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, wgrad_kernel<N>, P);
+  if (e != cudaSuccess || P.s.left == 0) return e;
+  wgrad_join_kernel<N><<<static_cast<unsigned>(P.s.left * (N / 4)), kIn, 0, st>>>(P);
+  return cudaGetLastError();
+}
+
 }  // namespace
 }  // namespace muon
 
@@ -588,7 +676,7 @@ extern "C" MUON_API size_t muon_weight_grad_workspace_size(const muon_weight_gra
   using namespace muon;
   if (validate_weight_grad(a) != MUON_OK) return 0;
   const WgradSplit s = split_of(*a);
-  return static_cast<size_t>(s.left * s.splits) * kPartBytes;
+  return static_cast<size_t>(s.left * s.splits) * s.part_bytes;
 }
 
 extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, void* workspace,
@@ -600,7 +688,7 @@ extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, 
   std::memset(&P, 0, sizeof(P));
   P.a = *a;
   P.s = split_of(*a);
-  const size_t need = static_cast<size_t>(P.s.left * P.s.splits) * kPartBytes;
+  const size_t need = static_cast<size_t>(P.s.left * P.s.splits) * P.s.part_bytes;
   if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need))
     return MUON_ERR_WORKSPACE;
   P.parts = static_cast<float*>(workspace);
@@ -613,31 +701,7 @@ extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, 
         encode_tokens_map(&P.te, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kEBytesRow, a->exps, (a->in + 31) / 32, a->tokens,
                           a->ld_e)))
     return MUON_ERR_CUDA;
-  // the shared-memory opt-in is a per-device attribute: set it once on each device
-  static std::atomic<uint64_t> attr_devices{0};
-  const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
-  if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
-    if (cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
-      return MUON_ERR_CUDA;
-    attr_devices.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  const int64_t pairs = P.s.units < sms / 2 ? P.s.units : sms / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, wgrad_kernel, P) != cudaSuccess) return MUON_ERR_CUDA;
-  if (P.s.left > 0) {
-    wgrad_join_kernel<<<static_cast<unsigned>(P.s.left * (kTile / 8)), kTile, 0, cfg.stream>>>(P);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
-  }
-  return MUON_OK;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = P.s.n == 256 ? launch_wgrad<256>(P, dev, sms, st) : launch_wgrad<128>(P, dev, sms, st);
+  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
