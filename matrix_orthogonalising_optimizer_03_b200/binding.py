@@ -7,6 +7,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_void_p
@@ -165,9 +166,25 @@ def hparams(lr: float = 0.02, momentum: float = 0.95, weight_decay: float = 0.0,
     return hp
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _find_raw_stream():
+    try:
+        return getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    except ImportError:
+        return None
+
+
+_raw_stream = _find_raw_stream()
 
 
 def _dtype_code(t) -> int:
@@ -211,23 +228,31 @@ def _device_of(tensors):
     return tensors[0].device if len(tensors) else None
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
-    """Context that makes `device` current for one library call."""
-    import contextlib
-    return _torch().cuda.device(device) if device is not None else contextlib.nullcontext()
+    """Context that makes `device` current for one library call (none is needed where it is
+    current already, which saves a microsecond or two per call)."""
+    if device is None:
+        return _HERE
+    cuda = _torch().cuda
+    return _HERE if device.index == cuda.current_device() else cuda.device(device)
 
 
 def _stream_ptr(stream) -> Optional[int]:
-    torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    """The cudaStream_t of a torch stream, by default of the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    cuda = _torch().cuda
+    if _raw_stream is not None:  # without building a Stream object
+        return _raw_stream(cuda.current_device())
+    return cuda.current_stream().cuda_stream
 
 
 def _on_stream(stream):
     """Context that makes `stream` current, so that what a call allocates belongs to it."""
-    import contextlib
-    return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return _torch().cuda.stream(stream) if stream is not None else _HERE
 
 
 def _stats_ptr(stats) -> Optional[int]:
@@ -438,17 +463,14 @@ class Act8:
             raise MuonError(2, "q and exps are too small for the checkpoint")
         self.q, self.exps, self.cols = q, exps, int(cols)
         self.rows, self.device = q.size(0), q.device
+        self._q_ptr, self._e_ptr = q.data_ptr(), exps.data_ptr()
+        # leading dimensions of q and exps (a single row may carry any stride)
+        self.ld = ((q.stride(0), exps.stride(0)) if self.rows > 1 else
+                   ((self.cols + 15) // 16 * 16, (self.cols + 511) // 512 * 16))
 
     def rows_of(self, lo: int, hi: int) -> "Act8":
         """The checkpoint of rows [lo, hi) (a view)."""
         return Act8(self.q[lo:hi], self.exps[lo:hi], self.cols)
-
-    @property
-    def ld(self):
-        """Leading dimensions of q and exps (a single row may carry any stride)."""
-        if self.rows <= 1:
-            return (self.cols + 15) // 16 * 16, (self.cols + 511) // 512 * 16
-        return self.q.stride(0), self.exps.stride(0)
 
 
 def new_act8(rows: int, cols: int, device="cuda") -> Act8:
@@ -460,18 +482,22 @@ def new_act8(rows: int, cols: int, device="cuda") -> Act8:
 
 
 def _act8_array(xs, cks):
-    if len(xs) != len(cks):
+    n = len(xs)
+    if n != len(cks):
         raise MuonError(1, "activations and checkpoints must have the same length")
-    arr = (MuonAct8 * len(xs))()
-    for i, (x, c) in enumerate(zip(xs, cks)):
+    arr = (MuonAct8 * n)()
+    for i in range(n):
+        x, c = xs[i], cks[i]
         _check_2d(x, "X")
-        if x.device != cks[0].device or c.device != cks[0].device:
+        device = cks[0].device
+        if x.device != device or c.device != device:
             raise MuonError(1, "activations and checkpoints must be on the same device")
-        if x.size(0) != c.rows or x.size(1) != c.cols:
+        rows, cols = x.shape
+        if rows != c.rows or cols != c.cols:
             raise MuonError(2, "activation and checkpoint shapes differ")
-        ld_q, ld_e = c.ld
-        arr[i] = MuonAct8(x.data_ptr(), c.q.data_ptr(), c.exps.data_ptr(), c.rows, c.cols,
-                          max(x.stride(0), x.size(1)), ld_q, ld_e, _dtype_code(x), 0)
+        a, ld = arr[i], x.stride(0)
+        a.X, a.q, a.exps, a.ld_q, a.ld_e = x.data_ptr(), c._q_ptr, c._e_ptr, *c.ld
+        a.rows, a.cols, a.ld_x, a.dtype = rows, cols, ld if ld > cols else cols, _dtype_code(x)
     return arr
 
 

@@ -17,6 +17,7 @@
 
 #include <cstdint>
 
+#include "act8.cuh"
 #include "muon.h"
 #include "ptx.cuh"
 #include "validate.h"
@@ -24,18 +25,21 @@
 namespace muon {
 namespace {
 
-constexpr int kItemsPerLaunch = 128;  // kernel parameters stay below 32 KB
+// Items of one launch: kernel parameters stay below 32 KB, and a short list takes the form
+// with short ones, whose launch costs the host a microsecond less.
+constexpr int kItemsPerLaunch = 128, kFewItems = 4;
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;
 constexpr int kUnitsPerBlock = kThreads * kUnits;
 constexpr int64_t kMaxCols = int64_t(1) << 26;
 
+template <int kItems>
 struct Act8Launch {
-  muon_act8_t a[kItemsPerLaunch];
-  int32_t block_base[kItemsPerLaunch + 1];
+  muon_act8_t a[kItems];
+  int32_t block_base[kItems + 1];
   int32_t n;
 };
-static_assert(sizeof(Act8Launch) < 32000, "kernel parameter space");
+static_assert(sizeof(Act8Launch<kItemsPerLaunch>) < 32000, "kernel parameter space");
 
 // Units of a row: whole groups of four, so that a group's lanes stay together.
 __host__ __device__ inline int64_t units_per_row(int64_t cols) { return (cols + 31) / 32 * 4; }
@@ -46,7 +50,8 @@ struct Unit {
   bool live;       // inside the matrix's rows
 };
 
-__device__ __forceinline__ int find_item(const Act8Launch& L) {
+template <int kItems>
+__device__ __forceinline__ int find_item(const Act8Launch<kItems>& L) {
   int lo = 0, hi = L.n - 1;  // the item of this block: last base <= blockIdx.x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -55,88 +60,99 @@ __device__ __forceinline__ int find_item(const Act8Launch& L) {
   return lo;
 }
 
-__device__ __forceinline__ Unit unit_at(const muon_act8_t& a, int64_t row0, uint32_t rem0,
-                                        uint32_t upr, int u) {
-  const uint32_t r = rem0 + u * kThreads + threadIdx.x;
-  const uint32_t dr = r / upr;
+// Units of a block: from unit `rem` of row `row` on; `inv` divides by the units of a row.
+struct Span {
+  int64_t row;
+  uint32_t rem, upr, inv;
+};
+
+__device__ __forceinline__ Span block_span(const muon_act8_t& a, int64_t block) {
+  Span s;
+  s.upr = static_cast<uint32_t>(units_per_row(a.cols));
+  const int64_t base = block * kUnitsPerBlock;
+  s.row = base / s.upr;
+  s.rem = static_cast<uint32_t>(base - s.row * s.upr);
+  s.inv = 0xFFFFFFFFu / s.upr + 1;
+  return s;
+}
+
+__device__ __forceinline__ Unit unit_at(const muon_act8_t& a, const Span& s, int u) {
+  const uint32_t r = s.rem + u * kThreads + threadIdx.x, upr = s.upr;
+  // r / upr: r < 2 upr for long rows; for short ones r upr < 2^22 and the reciprocal is exact
+  const uint32_t dr = upr >= kUnitsPerBlock ? (r >= upr ? 1u : 0u) : __umulhi(r, s.inv);
   Unit t;
-  t.row = row0 + dr;
+  t.row = s.row + dr;
   t.col = static_cast<int32_t>(r - dr * upr) * 8;
   t.live = t.row < a.rows;
   return t;
 }
 
-// The 8 values of a unit as fp32; columns past the matrix read as 0.
-__device__ __forceinline__ void load_unit(const muon_act8_t& a, const Unit& t, bool vec,
-                                          float (&x)[8]) {
+// The 8 values of a unit as they are in memory (BF16: 4 words, F32: 8); columns past the matrix
+// read as 0.
+template <bool kBf16>
+__device__ __forceinline__ void load_unit(const muon_act8_t& a, const Unit& t, bool vec, uint32_t (&w)[kBf16 ? 4 : 8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
+  for (int i = 0; i < (kBf16 ? 4 : 8); ++i) w[i] = 0;
   if (!t.live || t.col >= a.cols) return;
   const int64_t off = t.row * a.ld_x + t.col;
-  if (a.dtype == MUON_BF16) {
+  if (kBf16) {
     const uint16_t* p = static_cast<const uint16_t*>(a.X) + off;
     if (vec && t.col + 8 <= a.cols) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(v[i] << 16);
-        x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-      }
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (t.col + i < a.cols) x[i] = bf16_to_f32(p[i]);
+        if (t.col + i < a.cols) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
     }
   } else {
-    const float* p = static_cast<const float*>(a.X) + off;
+    const uint32_t* p = static_cast<const uint32_t*>(a.X) + off;
     if (vec && t.col + 8 <= a.cols) {
-      const float4 v0 = __ldcs(reinterpret_cast<const float4*>(p));
-      const float4 v1 = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-      x[0] = v0.x; x[1] = v0.y; x[2] = v0.z; x[3] = v0.w;
-      x[4] = v1.x; x[5] = v1.y; x[6] = v1.z; x[7] = v1.w;
+      const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(p)), v1 = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+      w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
+      w[kBf16 ? 0 : 4] = v1.x; w[kBf16 ? 0 : 5] = v1.y; w[kBf16 ? 0 : 6] = v1.z; w[kBf16 ? 0 : 7] = v1.w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (t.col + i < a.cols) x[i] = p[i];
+        if (t.col + i < a.cols) w[kBf16 ? 0 : i] = p[i];
     }
   }
 }
 
-__device__ __forceinline__ bool rows_aligned(const muon_act8_t& a) {
-  const int64_t elem = a.dtype == MUON_BF16 ? 2 : 4;
-  return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && (a.ld_x * elem) % 16 == 0;
-}
-
-__global__ void __launch_bounds__(kThreads) act8_store_kernel(const __grid_constant__ Act8Launch L) {
-  const int it = find_item(L);
-  const muon_act8_t& a = L.a[it];
-  const uint32_t upr = static_cast<uint32_t>(units_per_row(a.cols));
-  const int64_t base = static_cast<int64_t>(blockIdx.x - L.block_base[it]) * kUnitsPerBlock;
-  const int64_t row0 = base / upr;
-  const uint32_t rem0 = static_cast<uint32_t>(base - row0 * upr);
-  const bool vec = rows_aligned(a);
-  float x[kUnits][8];
+// Stores units u0 .. u0 + kCount - 1 of the thread: all loads first.
+template <bool kBf16, int kCount>
+__device__ __forceinline__ void store_units(const muon_act8_t& a, const Span& sp, bool vec, int u0) {
+  uint32_t w[kCount][kBf16 ? 4 : 8];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) load_unit(a, unit_at(a, row0, rem0, upr, u), vec, x[u]);
+  for (int u = 0; u < kCount; ++u) load_unit<kBf16>(a, unit_at(a, sp, u0 + u), vec, w[u]);
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const Unit t = unit_at(a, row0, rem0, upr, u);
+  for (int u = 0; u < kCount; ++u) {
+    const Unit t = unit_at(a, sp, u0 + u);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = __uint_as_float(!kBf16 ? w[u][kBf16 ? 0 : i] : (i & 1) ? w[u][i >> 1] & 0xFFFF0000u : w[u][i >> 1] << 16);
     uint32_t top = 0;  // magnitudes compare as integers, NaN above infinity
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[u][i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int be = static_cast<int>(top >> 23);
     const uint32_t byte = be == 255 ? 255u : static_cast<uint32_t>(max(be - 6, 1));
     // 2^-E; a group with a NaN or an infinity stores zeros under byte 255
     const float inv = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
-    uint32_t pk[2] = {0, 0};
+    // Clamped before the rounding, which keeps whole numbers; adding 1.5 * 2^23 rounds half to
+    // even and leaves the integer in the low bits (a conversion instruction runs at a quarter
+    // of the rate).
+    uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int q = __float2int_rn(x[u][i] * inv);
-      q = byte == 255u ? 0 : min(max(q, -127), 127);
-      pk[i >> 2] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i)
+      v[i] = __float_as_uint(fminf(fmaxf(x[i] * inv, -127.f), 127.f) + 12582912.f);
+    uint32_t pk[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      pk[i] = __byte_perm(__byte_perm(v[4 * i], v[4 * i + 1], 0x0040), __byte_perm(v[4 * i + 2], v[4 * i + 3], 0x0040), 0x5410);
+      if (byte == 255u) pk[i] = 0;
     }
     if (!t.live || t.col >= a.cols) continue;
     int8_t* q = a.q + t.row * a.ld_q + t.col;
@@ -151,19 +167,36 @@ __global__ void __launch_bounds__(kThreads) act8_store_kernel(const __grid_const
   }
 }
 
-__global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_constant__ Act8Launch L) {
+__device__ __forceinline__ bool rows_aligned(const muon_act8_t& a) {
+  const int64_t elem = a.dtype == MUON_BF16 ? 2 : 4;
+  return reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && (a.ld_x * elem) % 16 == 0;
+}
+
+template <int kItems>
+__global__ void __launch_bounds__(kThreads, 5) act8_store_kernel(const __grid_constant__ Act8Launch<kItems> L) {
   const int it = find_item(L);
   const muon_act8_t& a = L.a[it];
-  const uint32_t upr = static_cast<uint32_t>(units_per_row(a.cols));
-  const int64_t base = static_cast<int64_t>(blockIdx.x - L.block_base[it]) * kUnitsPerBlock;
-  const int64_t row0 = base / upr;
-  const uint32_t rem0 = static_cast<uint32_t>(base - row0 * upr);
+  const Span sp = block_span(a, static_cast<int64_t>(blockIdx.x - L.block_base[it]));
+  const bool vec = rows_aligned(a);
+  if (a.dtype == MUON_BF16) {
+    store_units<true, kUnits>(a, sp, vec, 0);
+  } else {
+    store_units<false, kUnits / 2>(a, sp, vec, 0);
+    store_units<false, kUnits / 2>(a, sp, vec, kUnits / 2);
+  }
+}
+
+template <int kItems>
+__global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_constant__ Act8Launch<kItems> L) {
+  const int it = find_item(L);
+  const muon_act8_t& a = L.a[it];
+  const Span sp = block_span(a, static_cast<int64_t>(blockIdx.x - L.block_base[it]));
   const bool vec = rows_aligned(a);
   uint2 w[kUnits];
   uint32_t byte[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const Unit t = unit_at(a, row0, rem0, upr, u);
+    const Unit t = unit_at(a, sp, u);
     w[u] = make_uint2(0, 0);
     byte[u] = 1;
     if (!t.live || t.col >= a.cols) continue;
@@ -181,26 +214,27 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_con
   }
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const Unit t = unit_at(a, row0, rem0, upr, u);
+    const Unit t = unit_at(a, sp, u);
     if (!t.live || t.col >= a.cols) continue;
-    const float s = __uint_as_float(byte[u] << 23);  // byte 0: zero, byte 255: infinity, times 0 NaN
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? w[u].x : w[u].y) >> (8 * (i & 3)))) * s;
+    const uint32_t sc = act8_scale2(byte[u]);
+    uint32_t y[4];  // bf16 pairs
+    act8_restore4(w[u].x, sc, sc, &y[0], &y[1]);
+    act8_restore4(w[u].y, sc, sc, &y[2], &y[3]);
     const int64_t off = t.row * a.ld_x + t.col;
     const bool whole = vec && t.col + 8 <= a.cols;
     if (a.dtype == MUON_BF16) {
       uint16_t* p = static_cast<uint16_t*>(a.X) + off;
       if (whole) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                  pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        *reinterpret_cast<uint4*>(p) = make_uint4(y[0], y[1], y[2], y[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (t.col + i < a.cols) p[i] = f32_to_bf16(x[i]);
+          if (t.col + i < a.cols) p[i] = static_cast<uint16_t>(y[i >> 1] >> (16 * (i & 1)));
       }
     } else {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float((i & 1) ? y[i >> 1] & 0xFFFF0000u : y[i >> 1] << 16);
       float* p = static_cast<float*>(a.X) + off;
       if (whole) {
         reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -260,6 +294,23 @@ muon_status_t validate_act8(const muon_act8_t* items, int n, bool store) {
   return MUON_OK;
 }
 
+template <int kItems>
+muon_status_t launch_act8(const muon_act8_t* items, int n, bool store, cudaStream_t st) {
+  Act8Launch<kItems> L;
+  L.n = n;
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    L.a[i] = items[i];
+    L.block_base[i] = static_cast<int32_t>(blocks);
+    blocks += (units_per_row(items[i].cols) * items[i].rows + kUnitsPerBlock - 1) / kUnitsPerBlock;
+  }
+  L.block_base[n] = static_cast<int32_t>(blocks);
+  if (blocks == 0) return MUON_OK;
+  if (store) act8_store_kernel<kItems><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(L);
+  else act8_restore_kernel<kItems><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(L);
+  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
 muon_status_t run_act8(const muon_act8_t* items, int n, bool store, void* stream) {
   const muon_status_t v = validate_act8(items, n, store);
   if (v != MUON_OK || n == 0) return v;
@@ -270,21 +321,12 @@ muon_status_t run_act8(const muon_act8_t* items, int n, bool store, void* stream
     if (units_per_row(items[i].cols) * items[i].rows / kUnitsPerBlock >
         (int64_t(1) << 30) / kItemsPerLaunch)
       return MUON_ERR_SHAPE;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n <= kFewItems) return launch_act8<kFewItems>(items, n, store, st);
   for (int i0 = 0; i0 < n; i0 += kItemsPerLaunch) {
-    Act8Launch L;
-    L.n = n - i0 < kItemsPerLaunch ? n - i0 : kItemsPerLaunch;
-    int64_t blocks = 0;
-    for (int i = 0; i < L.n; ++i) {
-      L.a[i] = items[i0 + i];
-      L.block_base[i] = static_cast<int32_t>(blocks);
-      blocks += (units_per_row(L.a[i].cols) * L.a[i].rows + kUnitsPerBlock - 1) / kUnitsPerBlock;
-    }
-    L.block_base[L.n] = static_cast<int32_t>(blocks);
-    if (blocks == 0) continue;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (store) act8_store_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(L);
-    else act8_restore_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(L);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    const muon_status_t s =
+        launch_act8<kItemsPerLaunch>(items + i0, n - i0 < kItemsPerLaunch ? n - i0 : kItemsPerLaunch, store, st);
+    if (s != MUON_OK) return s;
   }
   return MUON_OK;
 }

@@ -18,10 +18,10 @@
 //   0      TMA producer: per 64-token k-block 16 KB of dY, 8 KB of q and 1 KB of exponents
 //          into a ring of 8 stages
 //   1      TMEM allocator and (first CTA) MMA issuer
-//   2-9    restore, two teams that take the k-blocks in turn; the last k-block of a group also
+//   2-13   restore, three teams that take the k-blocks in turn; the last k-block of a group also
 //          clears the rows past its end in both operands, so that a neighbouring group's NaN
 //          cannot reach this one's sums
-//   10-17  epilogue: a lane is a column of dW's row, so the accumulator's registers are
+//   14-21  epilogue: a lane is a column of dW's row, so the accumulator's registers are
 //          written in whole 128-byte rows at any alignment, without a transpose
 // Tensor memory: 256 columns of accumulator and 8 stages of X^T of 32 columns.
 // Split of the work: tiles are dealt to the 74 CTA pairs in whole rounds; the tiles left over
@@ -35,6 +35,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "act8.cuh"
 #include "muon.h"
 #include "ns_tc.h"
 #include "ptx.cuh"
@@ -52,7 +53,7 @@ constexpr int kQBytes = 128 * kTok;           // a CTA's stored X columns of one
 constexpr int kEBytesRow = 16;                // exponents of 512 columns, the smallest TMA row
 constexpr int kEBytes = kEBytesRow * kTok;
 constexpr int kStages = 8;
-constexpr int kTeams = 2, kTeamWarps = 4;     // restore teams take k-blocks in turn
+constexpr int kTeams = 3, kTeamWarps = 4;     // restore teams take k-blocks in turn
 constexpr int kRestoreWarps = kTeams * kTeamWarps, kEpiWarps = 8;
 constexpr int kFirstEpi = 2 + kRestoreWarps;
 constexpr int kThreads = 32 * (2 + kRestoreWarps + kEpiWarps);
@@ -60,6 +61,9 @@ constexpr int kTmemX = 256;                   // first tensor-memory column of t
 constexpr int kXCols = kTok / 2;              // columns of one stage
 static_assert(kTmemX + kStages * kXCols <= 512, "tensor memory");
 constexpr int kPairs = 74;                    // CTA pairs of a B200 (148 SMs)
+
+constexpr int kTileKb = 2;                    // what a tile costs beside its k-blocks, in k-blocks
+constexpr int kMaxBalanced = 1024;            // groups whose lengths every block adds up
 
 // N: tile rows (out) of a CTA pair, half of them from each CTA's dY columns.
 template <int N>
@@ -78,6 +82,7 @@ struct WgradSplit {
   int32_t n;                 // tile rows, 256 or 128
   int32_t tiles_o, tiles_i;
   int32_t splits;
+  int32_t balance;           // tiles dealt in contiguous runs of equal k-blocks
   int64_t whole, left;
   int64_t units;
   size_t part_bytes;
@@ -118,6 +123,7 @@ WgradSplit split_of(const muon_weight_grad_t& a) {
                (kb + parts - 1) / parts * per_kb + fixed + 7000.;
       }
       s.units = s.whole + s.left * s.splits;
+      s.balance = s.splits == 1 && a.groups > 1 && a.groups <= kMaxBalanced && tiles > kPairs;
       if (best.n == 0 || cost < best_cost) {
         best = s;
         best_cost = cost;
@@ -163,28 +169,28 @@ struct Job {
 };
 
 template <int N>
-__device__ __forceinline__ Job job_of(const WgradParams& P, int64_t u) {
+__device__ __forceinline__ Job job_of(const WgradParams& P, uint32_t u) {
   Job j;
-  int64_t t = u;
-  int split = 0;
+  uint32_t t = u, split = 0;
+  const uint32_t whole = static_cast<uint32_t>(P.s.whole), splits = static_cast<uint32_t>(P.s.splits);
   j.part = -1;
-  if (u >= P.s.whole) {
-    const int64_t r = (u - P.s.whole) / P.s.splits;
-    split = static_cast<int>(u - P.s.whole - r * P.s.splits);
-    t = P.s.whole + r;
-    j.part = static_cast<int>(u - P.s.whole);
+  if (u >= whole) {
+    const uint32_t r = (u - whole) / splits;
+    split = u - whole - r * splits;
+    t = whole + r;
+    j.part = static_cast<int>(u - whole);
   }
-  const int per = P.s.tiles_o * P.s.tiles_i;
+  const uint32_t ti = static_cast<uint32_t>(P.s.tiles_i), per = static_cast<uint32_t>(P.s.tiles_o) * ti;
   j.g = static_cast<int>(t / per);
-  const int rem = static_cast<int>(t - static_cast<int64_t>(j.g) * per);
-  j.o0 = rem / P.s.tiles_i * N;
-  j.i0 = rem % P.s.tiles_i * kIn;
+  const uint32_t rem = t - static_cast<uint32_t>(j.g) * per;
+  j.o0 = static_cast<int>(rem / ti) * N;
+  j.i0 = static_cast<int>(rem % ti) * kIn;
   int lo, hi;
   group_range(P.a, j.g, &lo, &hi);
   if (j.part >= 0) {
-    const int64_t kb = (hi - lo + kTok - 1) / kTok;
-    const int64_t b0 = kb * split / P.s.splits, b1 = kb * (split + 1) / P.s.splits;
-    if (b1 * kTok < hi - lo) hi = lo + static_cast<int>(b1) * kTok;
+    const uint32_t kb = static_cast<uint32_t>(hi - lo + kTok - 1) / kTok;  // at most 2^25, splits at most 74
+    const uint32_t b0 = kb * split / splits, b1 = kb * (split + 1) / splits;
+    if (static_cast<int>(b1) * kTok < hi - lo) hi = lo + static_cast<int>(b1) * kTok;
     lo += static_cast<int>(b0) * kTok;
   }
   j.t0 = lo;
@@ -193,18 +199,51 @@ __device__ __forceinline__ Job job_of(const WgradParams& P, int64_t u) {
   return j;
 }
 
-// Four int8 (tokens t .. t+3 of one column) to bf16 times their tokens' scales. Low 7 bits
-// under the exponent of 128 give 128 + low7, the sign bit there gives 128 or 256; their
-// difference is the value, exactly.
-__device__ __forceinline__ void restore4(uint32_t w, const uint32_t (&s)[2], uint32_t* lo, uint32_t* hi) {
-  const uint32_t v = w & 0x7F7F7F7Fu, g = w & 0x80808080u, m = 0x43434343u;
-  const uint32_t a0 = __byte_perm(v, m, 0x4140), a1 = __byte_perm(v, m, 0x4342);
-  const uint32_t c0 = __byte_perm(g, m, 0x4140), c1 = __byte_perm(g, m, 0x4342);
-  auto bf2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
-  const __nv_bfloat162 r0 = __hmul2(__hsub2(bf2(a0), bf2(c0)), bf2(s[0]));
-  const __nv_bfloat162 r1 = __hmul2(__hsub2(bf2(a1), bf2(c1)), bf2(s[1]));
-  *lo = *reinterpret_cast<const uint32_t*>(&r0);
-  *hi = *reinterpret_cast<const uint32_t*>(&r1);
+// The tiles [u[0], u[1]) of CTA pair `pair` out of `pairs`, by one warp: tiles in order, each
+// weighing its k-blocks and kTileKb, and dealt to the pair in whose share of the total weight
+// its middle lies. A router's groups differ in length: dealt in turn, 64 experts of 0 to 1487
+// tokens left the busiest pair with 1.6 times the mean, dealt so with 1.2.
+__device__ __forceinline__ void balanced_range(const WgradParams& P, int pair, int pairs, int lane, uint32_t* u) {
+  const int groups = P.a.groups;
+  const int64_t per = static_cast<int64_t>(P.s.tiles_o) * P.s.tiles_i;
+  auto weight = [&](int g) {
+    int lo = 0, hi = 0;
+    if (g < groups) group_range(P.a, g, &lo, &hi);
+    return g < groups ? static_cast<int64_t>((hi - lo + kTok - 1) / kTok + kTileKb) : int64_t(0);
+  };
+  int64_t total = 0;
+  for (int g0 = 0; g0 < groups; g0 += 32) total += weight(g0 + lane);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= per;
+  int64_t before = 0, count[2] = {0, 0};
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int64_t w = weight(g0 + lane);
+    int64_t upto = w * per;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const int64_t base = before + upto - w * per;
+    before += __shfl_sync(0xffffffffu, upto, 31);
+    if (w == 0) continue;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // tiles of the group whose middle base + i w + w / 2 lies before the share's end
+      const int64_t x = 2 * (total * (pair + e) / pairs - base) - w;
+      const int64_t n = x <= 0 ? 0 : (x + 2 * w - 1) / (2 * w);
+      count[e] += n < per ? n : per;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) count[e] += __shfl_xor_sync(0xffffffffu, count[e], o);
+  if (lane == 0) {
+    u[0] = static_cast<uint32_t>(count[0]);
+    u[1] = pair + 1 == pairs ? static_cast<uint32_t>(P.s.units) : static_cast<uint32_t>(count[1]);
+  }
 }
 
 // Two 16 x 16 byte matrices, transposed: lanes 0-15 and 16-31 give their rows' addresses.
@@ -275,12 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (3 * kStages + 5) + 8 <= 256, "barrier region");
+  uint32_t* range = tmem_slot + 2;    // this pair's units
+  static_assert(8 * (3 * kStages + 5) + 16 <= 256, "barrier region");
 
   const muon_weight_grad_t& a = P.a;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_cta_rank());
-  const int64_t unit0 = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (threadIdx.x == 32 * kFirstEpi && a.tokens > 0) {
     tma_prefetch(&P.tq);
@@ -305,11 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  if (warp == 2 && P.s.balance) balanced_range(P, blockIdx.x >> 1, gridDim.x >> 1, lane, range);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t unit0 = P.s.balance ? range[0] : blockIdx.x >> 1;
+  const uint32_t unit1 = P.s.balance ? range[1] : static_cast<uint32_t>(P.s.units);
+  const uint32_t stride = P.s.balance ? 1 : gridDim.x >> 1;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -318,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       uint32_t par = 0;
       int64_t loads = 0;
       bool ok = true;
-      for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+      for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
         const Job j = job_of<N>(P, u);
         for (int kb = 0; kb < j.nkb; ++kb) {
           if (!mbar_wait(&empty[s], par ^ 1u, abort_flag)) {
@@ -359,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       int s = 0, it = 0;
       uint32_t par = 0;
       bool ok = true;
-      for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+      for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
         const Job j = job_of<N>(P, u);
         if (j.nkb == 0) continue;
         const int acc = it % C::kAcc;
@@ -401,14 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     // exponent tile holds group g, whose bytes a shuffle hands to the lanes of their tokens.
     const int team = (warp - 2) / kTeamWarps, w = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-    int64_t q0 = 0;  // k-blocks of the units before this one
+    uint32_t q0 = 0;  // k-blocks of the units before this one
     bool ok = true;
-    for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+    for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
       const Job j = job_of<N>(P, u);
       const int grp = ((j.i0 + rank * 128) / 32 + w) % kEBytesRow;  // within a stage's exponent row
       const int src = (grp & 7) * 4 + (lane & 3);
-      for (int kb = static_cast<int>((team - q0) & 1); kb < j.nkb; kb += kTeams) {
-        const int64_t q = q0 + kb;
+      for (int kb = static_cast<int>((team + kTeams - q0 % kTeams) % kTeams); kb < j.nkb; kb += kTeams) {
+        const uint32_t q = q0 + kb;
         const int s = static_cast<int>(q % kStages);
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], static_cast<uint32_t>((q / kStages) & 1), abort_flag))) {
           ok = false;
@@ -454,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           ldmatrix_b8_x2_trans(smem_u32(st + C::kYBytes + t * 128 + (((2 * w + (lane >> 4)) ^ (t & 7)) << 4)), v);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            restore4(v[2 * h], sc[b], &x[h][4 * b], &x[h][4 * b + 1]);
-            restore4(v[2 * h + 1], sc[b], &x[h][4 * b + 2], &x[h][4 * b + 3]);
+            act8_restore4(v[2 * h], sc[b][0], sc[b][1], &x[h][4 * b], &x[h][4 * b + 1]);
+            act8_restore4(v[2 * h + 1], sc[b][0], sc[b][1], &x[h][4 * b + 2], &x[h][4 * b + 3]);
           }
         }
         const uint32_t at = tmem + kTmemX + s * kXCols + lanes;
@@ -477,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     const int half = (warp - kFirstEpi) / 4 * (N / 2);   // and its half of the tile's rows of dW
     int it = 0;
     bool ok = true;
-    for (int64_t u = unit0; u < P.s.units && ok; u += stride) {
+    for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
       const Job j = job_of<N>(P, u);
       if (j.nkb == 0 && (j.part >= 0 || a.accumulate)) continue;
       const int acc = it % C::kAcc;
@@ -545,7 +588,7 @@ __global__ void __launch_bounds__(kIn) wgrad_join_kernel(const __grid_constant__
   const muon_weight_grad_t& a = P.a;
   const int64_t r = blockIdx.x / (N / 4);
   const int row = blockIdx.x % (N / 4) * 4 + threadIdx.x / 64, c0 = threadIdx.x % 64 * 4;
-  const Job j = job_of<N>(P, P.s.whole + r * P.s.splits);
+  const Job j = job_of<N>(P, static_cast<uint32_t>(P.s.whole + r * P.s.splits));
   int lo, hi;
   group_range(a, j.g, &lo, &hi);
   const int64_t o = j.o0 + row;
@@ -688,6 +731,7 @@ extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, 
   std::memset(&P, 0, sizeof(P));
   P.a = *a;
   P.s = split_of(*a);
+  if (P.s.units >= (int64_t(1) << 31)) return MUON_ERR_SHAPE;
   const size_t need = static_cast<size_t>(P.s.left * P.s.splits) * P.s.part_bytes;
   if (need > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 || ws_bytes < need))
     return MUON_ERR_WORKSPACE;
