@@ -12,7 +12,6 @@
 // over the scores they came from, where the next product takes them as its tensor-memory
 // operand; the transposes that dV and dK need cost nothing, because the second kernel computes
 // S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
-// Two warps issue the products, one for each chain of products that wait for one another.
 // Bound by the tensor core: an M = 128 product whose operands both come from shared memory
 // runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles.
 #include <cuda.h>
@@ -101,31 +100,6 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t
     umma_f16_ts_lo(d, a_tmem + (k >> 2) * 64 + (k & 3) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
 }
 
-// Writes `cols` accumulator columns of this thread's row, times f, as bf16.
-__device__ __forceinline__ void store_row(uint32_t taddr, int cols, float f, bool zero, bool live, uint16_t* out, int col0,
-                                          int dim) {
-#pragma unroll 1
-  for (int c = 0; c < cols; c += 32) {
-    uint32_t v[32];
-    if (!zero) {
-      tmem_ld32(taddr + c, v);
-      tmem_wait_ld();
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0;
-    }
-#pragma unroll
-    for (int e = 0; e < 32; e += 8) {
-      uint32_t pk[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        pk[k] = round_bf16x2(__uint_as_float(v[e + 2 * k]) * f, __uint_as_float(v[e + 2 * k + 1]) * f);
-      if (live && col0 + c + e < dim)
-        *reinterpret_cast<uint4*>(out + c + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    }
-  }
-}
-
 // ------------------------------------------------------------------ dQ and delta
 // Chain A: S_j = Q K_j^T (two buffers), dQ += dS_j K_j.  Chain B: dP_j = dout V_j^T.
 template <int HD>
@@ -152,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   uint64_t* dp_full = s_full + 2;
   uint64_t* dp_read = dp_full + 1;
   uint64_t* ds_full = dp_read + 1;  // per block parity
-  uint64_t* done = ds_full + 2;
+  uint64_t* turn = ds_full + 2;     // per half and lane quarter: its exponentials are done
+  uint64_t* done = turn + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -169,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       mbar_init(&s_full[s], 1);
       mbar_init(&ds_full[s], 8);
     }
+    for (int e = 0; e < 8; ++e) mbar_init(&turn[e], 1);
     mbar_init(dp_full, 1);
     mbar_init(dp_read, 8);
     mbar_init(done, 1);
@@ -188,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       const int kvh = head / (heads / a.kv_heads);
       mbar_expect_tx(q_full, 2 * C::kTile);
       for (int c = 0; c < HD / 64; ++c) {
@@ -255,28 +231,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
     const bool live = row < r.m;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const int64_t token = r.q0 + row, vec = static_cast<int64_t>(head) * a.q_tokens + token;
-    float delta = 0.f, lse = INFINITY;  // of rows without keys, or none: P = 0
-    if (live) {
-      const uint4* o = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.ptr) + token * a.o.ld + head * a.o.head);
-      const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout.ptr) + token * a.dout.ld + head * a.dout.head);
-      float part[4] = {};
-#pragma unroll 4
-      for (int c = 0; c < a.head_dim / 8; ++c) {
-        const uint4 x = __ldg(o + c), y = __ldg(g + c);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    // delta = o . dout: each half of the threads sums half the columns, dout from its tile in
+    // shared memory, and hands its sum to the other
+    float lse = INFINITY;  // of rows without keys, or none: P = 0
+    float part[4] = {};
+    {
+      constexpr int kUnits = HD / 16;
+      uint4 o[kUnits];
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.ptr) + token * a.o.ld + head * a.o.head);
+#pragma unroll
+      for (int c = 0; c < kUnits; ++c)
+        o[c] = live && (half * kUnits + c) * 8 < a.head_dim ? __ldg(src + half * kUnits + c) : make_uint4(0, 0, 0, 0);
+      if (live) {
+        const float l = __ldg(a.lse + vec);
+        if (l != -INFINITY) lse = l * kLog2e;
+      }
+      const bool got = wait_all(q_full, 0, abort_flag);
+      const int rt = w * 32 + lane;
+#pragma unroll
+      for (int c = 0; c < kUnits; ++c) {
+        const int u = half * kUnits + c;
+        const uint4 g = *reinterpret_cast<const uint4*>(sdo + (u >> 3) * kChunk + rt * 128 + (((u & 7) ^ (rt & 7)) << 4));
+        const uint32_t xs[4] = {o[c].x, o[c].y, o[c].z, o[c].w}, ys[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           part[e] = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), part[e]);
           part[e] = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), part[e]);
         }
       }
-      delta = (part[0] + part[1]) + (part[2] + part[3]);
-      if (half == 0) P.delta[vec] = delta;
-      const float l = __ldg(a.lse + vec);
-      if (l != -INFINITY) lse = l * kLog2e;
+      ok = got;
     }
+    float* exchange = reinterpret_cast<float*>(smem + C::kOffVec);
+    const float mine = (part[0] + part[1]) + (part[2] + part[3]);
+    exchange[half * kRows + w * 32 + lane] = mine;
+    named_barrier(1, 256);
+    const float delta = exchange[w * 32 + lane] + exchange[kRows + w * 32 + lane];
+    if (live && half == 0) P.delta[vec] = delta;
     const float sl = a.scale * kLog2e;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < n && ok; ++j) {
       ok = wait_all(&s_full[j & 1], j >> 1, abort_flag);
       if (!ok) break;
       const uint32_t ts = tmem + lanes + (j & 1) * 128 + half * 64;
@@ -287,10 +279,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       // keys of this half block that the row sees
       const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows - half * 64;
       const bool masked = __any_sync(0xffffffffu, vis < 64);
+      // The two warps of a scheduler take turns at the exponentials: one's other work overlaps
+      // the other's.
+      if (half == 1 || j > 0) ok = wait_all(&turn[4 * (1 - half) + w], half == 1 ? j : j - 1, abort_flag);
+      if (!ok) break;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), sl, -lse)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&turn[4 * half + w]);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tmem + lanes + kDp + half * 64, p[0]);
@@ -322,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       if (lane == 0) mbar_arrive(&ds_full[j & 1]);
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
-    store_row(tmem + lanes + kDq + half * (HD / 2), HD / 2, a.scale, n == 0, live && ok,
-              static_cast<uint16_t*>(a.dq.ptr) + token * a.dq.ld + head * a.dq.head + half * (HD / 2), half * (HD / 2),
-              a.head_dim);
+    store_rows<HD / 2>(tmem + lanes + kDq + half * (HD / 2), sq, w, lane, half * (HD / 2), a.scale, n == 0,
+                       static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + half * (HD / 2),
+                       a.dq.ld, ok ? r.m - row0 - w * 32 : 0, a.head_dim);
     tc_fence_before();
   }
   if (!ok && lane == 0) {
@@ -339,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------ dK and dV
-// Chain A: S^T_j = K Q_j^T, dV += P^T_j dout_j.  Chain B: dP^T_j = V dout_j^T, dK += dS^T_j Q_j.
+// S^T_j = K Q_j^T, dP^T_j = V dout_j^T, dV += P^T_j dout_j, dK += dS^T_j Q_j.
 // Block j runs over the row tiles that see the keys, head after head.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
@@ -382,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     for (int s = 0; s < 2; ++s) {
       mbar_init(&do_full[s], 1);
       mbar_init(&do_ready[s], 1);
-      mbar_init(&do_empty[s], 2);
+      mbar_init(&do_empty[s], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(p_full, 8);
     mbar_init(dp_full, 1);
     mbar_init(ds_full, 8);
-    mbar_init(done, 2);
+    mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -429,6 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       for (int j = dl > 2 ? dl - 2 : 0; j < dl; ++j) mbar_wait(&do_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), nullptr);
     }
   } else if (warp == 1) {
+    // One issuer keeps the order dV_j, S_{j+1}, dK_j, dP_{j+1}: S_{j+1} is what the softmax waits
+    // for next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1}
+    // came 600 cycles later.
     if (n > 0) {
       auto score = [&](int j) {  // S^T_j; P^T_{j-1} over it went into a product issued before
         if (!wait_all(&q_ready[j % 3], j / 3, abort_flag)) return false;
@@ -438,33 +439,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
         }
         return true;
       };
-      ok = wait_all(kv_full, 0, abort_flag) && score(0);
-      for (int j = 0; j < n && ok; ++j) {
-        ok = wait_all(p_full, j, abort_flag) && wait_all(&do_ready[j & 1], j >> 1, abort_flag);
-        if (!ok) break;
-        if (elect_one()) {
-          product_ts<HD>(tmem + kDv, tmem, smem_u32(sdo) + (j & 1) * C::kTile, j > 0);
-          umma_commit(&do_empty[j & 1]);
-          if (j + 1 == n) umma_commit(done);
-        }
-        if (j + 1 < n) ok = score(j + 1);
-      }
-      ok = ok && wait_all(done, 0, abort_flag);  // never leave with products still running
-    }
-  } else if (warp == 2) {
-    if (n > 0) {
       auto dprob = [&](int j) {  // dP^T_j; dS^T_{j-1} over it went into a product issued before
         if (!wait_all(&do_ready[j & 1], j >> 1, abort_flag)) return false;
         if (elect_one()) {
           product_ss<HD>(tmem + kDp, smem_u32(sv), smem_u32(sdo) + (j & 1) * C::kTile);
           umma_commit(dp_full);
-          umma_commit(&do_empty[j & 1]);
         }
         return true;
       };
-      ok = wait_all(kv_full, 0, abort_flag) && dprob(0);
+      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0);
       for (int j = 0; j < n && ok; ++j) {
-        ok = wait_all(ds_full, j, abort_flag) && wait_all(&q_ready[j % 3], j / 3, abort_flag);
+        ok = wait_all(p_full, j, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
+          product_ts<HD>(tmem + kDv, tmem, smem_u32(sdo) + (j & 1) * C::kTile, j > 0);
+          umma_commit(&do_empty[j & 1]);
+        }
+        if (j + 1 < n) ok = score(j + 1);
+        ok = ok && wait_all(ds_full, j, abort_flag);
         if (!ok) break;
         if (elect_one()) {
           product_ts<HD>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kTile, j > 0);
@@ -473,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
         }
         if (j + 1 < n) ok = dprob(j + 1);
       }
-      ok = ok && wait_all(done, 0, abort_flag);
+      ok = ok && wait_all(done, 0, abort_flag);  // never leave with products still running
     }
   } else if (warp == 3) {
     // Stages what the copies do not bring: lse (times log2 e) and delta of the block's rows, and
@@ -511,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       if (lane == 0) mbar_arrive(&do_ready[j & 1]);
       if (++t == tile0 + tiles) t = tile0, ++h;
     }
-  } else {
+  } else if (warp >= 4) {
     const int w = warp & 3, half = (warp - 4) >> 2;     // lane quarter, and half of a block's rows
     const int key = key0 + w * 32 + lane;               // within the sequence
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
@@ -581,14 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
-    const bool live = key < r.n && ok;
-    const int64_t token = r.k0 + key;
+    // staged where V and K were: their products are complete
+    const int64_t token = r.k0 + key0 + w * 32;
+    const int rows = ok ? r.n - key0 - w * 32 : 0;
     if (half == 0)
-      store_row(tmem + lanes + kDv, HD, 1.f, n == 0, live,
-                static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head, 0, a.head_dim);
+      store_rows<HD>(tmem + lanes + kDv, sv, w, lane, 0, 1.f, n == 0,
+                     static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head, a.dv.ld, rows, a.head_dim);
     else
-      store_row(tmem + lanes + kDk, HD, a.scale, n == 0, live,
-                static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head, 0, a.head_dim);
+      store_rows<HD>(tmem + lanes + kDk, sk, w, lane, 0, a.scale, n == 0,
+                     static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head, a.dk.ld, rows, a.head_dim);
     tc_fence_before();
   }
   if (!ok && lane == 0) {

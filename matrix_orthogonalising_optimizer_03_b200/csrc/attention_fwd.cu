@@ -400,30 +400,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       ok = wait_o(nbi - 1);
       if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
     }
-    const bool live = row < r.m, seen = top > -INFINITY || sum != 0.f;
-    const float inv = seen ? 1.f / sum : 0.f;
-    uint16_t* out = static_cast<uint16_t*>(a.o.ptr) + static_cast<int64_t>(r.q0 + row) * a.o.ld + head * a.o.head;
-#pragma unroll
-    for (int c = 0; c < HD / 32; ++c) {
-      uint32_t o[32];
-      if (nbi > 0) {
-        tmem_ld32(to + c * 32, o);
-        tmem_wait_ld();
-      }
-      if (!seen || nbi == 0) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t pk[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          pk[k] = round_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-        if (live && ok && c * 32 + e < a.head_dim)
-          *reinterpret_cast<uint4*>(out + c * 32 + e) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      }
+    if (nbi == 0 && nmax > 0) {  // no copy may land over the staged zeros
+      ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag));
+      if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
     }
+    const bool live = row < r.m, seen = top > -INFINITY || sum != 0.f;
+    const float inv = seen ? 1.f / sum : 0.f;  // 0: the row is written as zeros
+    // staged where Q was: its products are complete
+    store_rows<HD>(to, smem + i * C::kQBytes, w, lane, 0, inv, nbi == 0,
+                   static_cast<uint16_t*>(a.o.ptr) + static_cast<int64_t>(r.q0 + row0 + i * kRows + w * 32) * a.o.ld + head * a.o.head,
+                   a.o.ld, ok ? r.m - row0 - i * kRows - w * 32 : 0, a.head_dim);
     if (live && ok)
       a.lse[static_cast<int64_t>(head) * a.q_tokens + r.q0 + row] =
           seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
