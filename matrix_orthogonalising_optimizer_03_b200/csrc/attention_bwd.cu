@@ -7,8 +7,8 @@
 // calls give equal bits: one per 128 query rows for dQ (and delta), one per 128 keys for dK
 // and dV, over all query heads of the key head. S and dout V^T are computed in both: seven
 // products instead of five, against fp32 atomics on dQ, whose order changes its sums.
-// In both, 8 warps own a 128 x 128 block in tensor memory, a thread 64 elements of one lane's
-// row. P and dS are rounded to bf16 (relative 2^-9, errors of either sign) and written back
+// In both, 16 warps own a 128 x 128 block in tensor memory, a thread 32 elements of one lane's
+// row (8 warps of 64 elements could not hide the waits and transfers of a block). P and dS are rounded to bf16 (relative 2^-9, errors of either sign) and written back
 // over the scores they came from, where the next product takes them as its tensor-memory
 // operand; the transposes that dV and dK need cost nothing, because the second kernel computes
 // S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kRows = 128;            // rows and keys of a block
 constexpr int kChunk = kRows * 128;   // bytes of 64 columns of a tile
-constexpr int kThreads = 384;         // 4 warps that move and issue, 8 that compute
+constexpr int kCompute = 16;          // warps that compute, four to a scheduler
+constexpr int kThreads = 32 * (4 + kCompute);  // and 4 that move and issue
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int HD>
@@ -89,15 +90,15 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t
   }
 }
 
-// D (+)= A B over the 128 rows or keys of a block: A bf16 in tensor memory (the first 64 in
-// columns 0-31, the others in columns 64-95), B an MN-major tile in shared memory.
+// D (+)= A B over the 128 rows or keys of a block: A bf16 in tensor memory (each 32 of them in
+// the first 16 of the 32 columns they came from), B an MN-major tile in shared memory.
 template <int HD>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
   const uint32_t bd = (static_cast<uint32_t>(kChunk >> 4) << 16) | (b_addr >> 4);
 #pragma unroll
   for (int k = 0; k < kRows / 16; ++k)
-    umma_f16_ts_lo(d, a_tmem + (k >> 2) * 64 + (k & 3) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
+    umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
 }
 
 // ------------------------------------------------------------------ dQ and delta
@@ -126,8 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   uint64_t* dp_full = s_full + 2;
   uint64_t* dp_read = dp_full + 1;
   uint64_t* ds_full = dp_read + 1;  // per block parity
-  uint64_t* turn = ds_full + 2;     // per half and lane quarter: its exponentials are done
-  uint64_t* done = turn + 8;
+  uint64_t* done = ds_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -142,11 +142,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&ds_full[s], 8);
+      mbar_init(&ds_full[s], kCompute);
     }
-    for (int e = 0; e < 8; ++e) mbar_init(&turn[e], 1);
     mbar_init(dp_full, 1);
-    mbar_init(dp_read, 8);
+    mbar_init(dp_read, kCompute);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -226,103 +225,87 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       ok = ok && wait_all(dp_full, n - 1, abort_flag);
     }
   } else if (warp >= 4) {
-    const int w = warp & 3, half = (warp - 4) >> 2;     // lane quarter, and half of a block's keys
+    const int w = warp & 3, part = (warp - 4) >> 2;     // lane quarter, and quarter of a block's keys
     const int row = row0 + w * 32 + lane;               // within the sequence
     const bool live = row < r.m;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const int64_t token = r.q0 + row, vec = static_cast<int64_t>(head) * a.q_tokens + token;
-    // delta = o . dout: each half of the threads sums half the columns, dout from its tile in
-    // shared memory, and hands its sum to the other
+    // delta = o . dout: the four threads of a row sum a quarter of the columns each, dout from
+    // its tile in shared memory
     float lse = INFINITY;  // of rows without keys, or none: P = 0
-    float part[4] = {};
+    float sum[4] = {};
     {
-      constexpr int kUnits = HD / 16;
+      constexpr int kUnits = HD / 32;
       uint4 o[kUnits];
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.ptr) + token * a.o.ld + head * a.o.head);
 #pragma unroll
       for (int c = 0; c < kUnits; ++c)
-        o[c] = live && (half * kUnits + c) * 8 < a.head_dim ? __ldg(src + half * kUnits + c) : make_uint4(0, 0, 0, 0);
+        o[c] = live && (part * kUnits + c) * 8 < a.head_dim ? __ldg(src + part * kUnits + c) : make_uint4(0, 0, 0, 0);
       if (live) {
         const float l = __ldg(a.lse + vec);
         if (l != -INFINITY) lse = l * kLog2e;
       }
-      const bool got = wait_all(q_full, 0, abort_flag);
+      ok = wait_all(q_full, 0, abort_flag);
       const int rt = w * 32 + lane;
 #pragma unroll
       for (int c = 0; c < kUnits; ++c) {
-        const int u = half * kUnits + c;
+        const int u = part * kUnits + c;
         const uint4 g = *reinterpret_cast<const uint4*>(sdo + (u >> 3) * kChunk + rt * 128 + (((u & 7) ^ (rt & 7)) << 4));
         const uint32_t xs[4] = {o[c].x, o[c].y, o[c].z, o[c].w}, ys[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          part[e] = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), part[e]);
-          part[e] = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), part[e]);
+          sum[e] = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), sum[e]);
+          sum[e] = fmaf(__uint_as_float(xs[e] & 0xFFFF0000u), __uint_as_float(ys[e] & 0xFFFF0000u), sum[e]);
         }
       }
-      ok = got;
     }
-    float* exchange = reinterpret_cast<float*>(smem + C::kOffVec);
-    const float mine = (part[0] + part[1]) + (part[2] + part[3]);
-    exchange[half * kRows + w * 32 + lane] = mine;
-    named_barrier(1, 256);
-    const float delta = exchange[w * 32 + lane] + exchange[kRows + w * 32 + lane];
-    if (live && half == 0) P.delta[vec] = delta;
+    float* exchange = reinterpret_cast<float*>(smem + C::kOffVec) + w * 32 + lane;
+    exchange[part * kRows] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    named_barrier(1, 32 * kCompute);
+    const float delta = (exchange[0] + exchange[kRows]) + (exchange[2 * kRows] + exchange[3 * kRows]);
+    if (live && part == 0) P.delta[vec] = delta;
     const float sl = a.scale * kLog2e;
     for (int j = 0; j < n && ok; ++j) {
       ok = wait_all(&s_full[j & 1], j >> 1, abort_flag);
       if (!ok) break;
-      const uint32_t ts = tmem + lanes + (j & 1) * 128 + half * 64;
-      uint32_t s[2][32], p[2][32];
-      tmem_ld32(ts, s[0]);
-      tmem_ld32(ts + 32, s[1]);
+      const uint32_t ts = tmem + lanes + (j & 1) * 128 + part * 32;
+      uint32_t s[32], p[32];
+      tmem_ld32(ts, s);
       tmem_wait_ld();
-      // keys of this half block that the row sees
-      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows - half * 64;
-      const bool masked = __any_sync(0xffffffffu, vis < 64);
-      // The two warps of a scheduler take turns at the exponentials: one's other work overlaps
-      // the other's.
-      if (half == 1 || j > 0) ok = wait_all(&turn[4 * (1 - half) + w], half == 1 ? j : j - 1, abort_flag);
-      if (!ok) break;
+      // keys of this quarter of the block that the row sees
+      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows - part * 32;
+      const bool masked = __any_sync(0xffffffffu, vis < 32);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), sl, -lse)));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&turn[4 * half + w]);
+      for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e]), sl, -lse)));
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
-      tmem_ld32(tmem + lanes + kDp + half * 64, p[0]);
-      tmem_ld32(tmem + lanes + kDp + half * 64 + 32, p[1]);
+      tmem_ld32(tmem + lanes + kDp + part * 32, p);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dp_read);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * (__uint_as_float(p[c][e]) - delta));
+      for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * (__uint_as_float(p[e]) - delta));
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= vis) s[c][e] = 0;
+        for (int e = 0; e < 32; ++e)
+          if (e >= vis) s[e] = 0;
       }
-      uint32_t pk[32];
+      uint32_t pk[16];
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        pk[e] = round_bf16x2(__uint_as_float(s[e >> 4][2 * (e & 15)]), __uint_as_float(s[e >> 4][2 * (e & 15) + 1]));
-      tmem_st32(ts, pk);
+      for (int e = 0; e < 16; ++e) pk[e] = round_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+      tmem_st16(ts, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ds_full[j & 1]);
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
-    store_rows<HD / 2>(tmem + lanes + kDq + half * (HD / 2), sq, w, lane, half * (HD / 2), a.scale, n == 0,
-                       static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + half * (HD / 2),
-                       a.dq.ld, ok ? r.m - row0 - w * 32 : 0, a.head_dim);
+    // staged where Q was: its products are complete
+    if (part < HD / 32)
+      store_rows<32>(tmem + lanes + kDq + part * 32, sq, w, lane, part * 32, a.scale, n == 0,
+                     static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + part * 32, a.dq.ld,
+                     ok ? r.m - row0 - w * 32 : 0, a.head_dim);
     tc_fence_before();
   }
   if (!ok && lane == 0) {
@@ -383,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       mbar_init(&do_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_full, 8);
+    mbar_init(p_full, kCompute);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, kCompute);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -504,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       if (++t == tile0 + tiles) t = tile0, ++h;
     }
   } else if (warp >= 4) {
-    const int w = warp & 3, half = (warp - 4) >> 2;     // lane quarter, and half of a block's rows
+    const int w = warp & 3, part = (warp - 4) >> 2;     // lane quarter, and quarter of a block's rows
     const int key = key0 + w * 32 + lane;               // within the sequence
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const float sl = a.scale * kLog2e;
@@ -512,61 +495,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     for (int j = 0; j < n; ++j) {
       ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(s_full, j, abort_flag);
       if (!ok) break;
-      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + (j & 1) * C::kVecBytes) + half * 16;
+      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + (j & 1) * C::kVecBytes) + part * 8;
       const float4* dlt = lse + kRows / 4;
-      const uint32_t ts = tmem + lanes + half * 64, tp = ts + kDp;
-      uint32_t s[2][32];
-      tmem_ld32(ts, s[0]);
-      tmem_ld32(ts + 32, s[1]);
+      const uint32_t ts = tmem + lanes + part * 32, tp = ts + kDp;
+      uint32_t s[32], p[32], pk[16];
+      tmem_ld32(ts, s);
       tmem_wait_ld();
-      // the first row of this half block that sees the key (rows are columns here)
-      const int first = a.causal ? key - shift - t * kRows - half * 64 : 0;
+      // the first row of this quarter of the block that sees the key (rows are columns here)
+      const int first = a.causal ? key - shift - t * kRows - part * 32 : 0;
       if (++t == tile0 + tiles) t = tile0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 l = lse[(c * 32 + e) / 4];
-          s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), sl, -l.x)));
-          s[c][e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e + 1]), sl, -l.y)));
-          s[c][e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e + 2]), sl, -l.z)));
-          s[c][e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e + 3]), sl, -l.w)));
-        }
+      for (int e = 0; e < 32; e += 4) {
+        const float4 l = lse[e / 4];
+        s[e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e]), sl, -l.x)));
+        s[e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e + 1]), sl, -l.y)));
+        s[e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e + 2]), sl, -l.z)));
+        s[e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e + 3]), sl, -l.w)));
+      }
       if (__any_sync(0xffffffffu, first > 0)) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < first) s[c][e] = 0;
+        for (int e = 0; e < 32; ++e)
+          if (e < first) s[e] = 0;
       }
-      uint32_t pk[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        pk[e] = round_bf16x2(__uint_as_float(s[e >> 4][2 * (e & 15)]), __uint_as_float(s[e >> 4][2 * (e & 15) + 1]));
-      tmem_st32(ts, pk);
+      for (int e = 0; e < 16; ++e) pk[e] = round_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+      tmem_st16(ts, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
-      uint32_t p[2][32];
-      tmem_ld32(tp, p[0]);
-      tmem_ld32(tp + 32, p[1]);
+      tmem_ld32(tp, p);
       tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d = dlt[(c * 32 + e) / 4];
-          const float x0 = __uint_as_float(s[c][e]) * (__uint_as_float(p[c][e]) - d.x);
-          const float x1 = __uint_as_float(s[c][e + 1]) * (__uint_as_float(p[c][e + 1]) - d.y);
-          const float x2 = __uint_as_float(s[c][e + 2]) * (__uint_as_float(p[c][e + 2]) - d.z);
-          const float x3 = __uint_as_float(s[c][e + 3]) * (__uint_as_float(p[c][e + 3]) - d.w);
-          pk[(c * 32 + e) / 2] = round_bf16x2(x0, x1);
-          pk[(c * 32 + e) / 2 + 1] = round_bf16x2(x2, x3);
-        }
-      tmem_st32(tp, pk);
+      for (int e = 0; e < 32; e += 4) {
+        const float4 d = dlt[e / 4];
+        const float x0 = __uint_as_float(s[e]) * (__uint_as_float(p[e]) - d.x);
+        const float x1 = __uint_as_float(s[e + 1]) * (__uint_as_float(p[e + 1]) - d.y);
+        const float x2 = __uint_as_float(s[e + 2]) * (__uint_as_float(p[e + 2]) - d.z);
+        const float x3 = __uint_as_float(s[e + 3]) * (__uint_as_float(p[e + 3]) - d.w);
+        pk[e / 2] = round_bf16x2(x0, x1);
+        pk[e / 2 + 1] = round_bf16x2(x2, x3);
+      }
+      tmem_st16(tp, pk);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -576,12 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     // staged where V and K were: their products are complete
     const int64_t token = r.k0 + key0 + w * 32;
     const int rows = ok ? r.n - key0 - w * 32 : 0;
-    if (half == 0)
-      store_rows<HD>(tmem + lanes + kDv, sv, w, lane, 0, 1.f, n == 0,
-                     static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head, a.dv.ld, rows, a.head_dim);
+    const int col = (part & 1) * (HD / 2);
+    if (part < 2)
+      store_rows<HD / 2>(tmem + lanes + kDv + col, sv, w, lane, col, 1.f, n == 0,
+                         static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head + col, a.dv.ld, rows, a.head_dim);
     else
-      store_rows<HD>(tmem + lanes + kDk, sk, w, lane, 0, a.scale, n == 0,
-                     static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head, a.dk.ld, rows, a.head_dim);
+      store_rows<HD / 2>(tmem + lanes + kDk + col, sk, w, lane, col, a.scale, n == 0,
+                         static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head + col, a.dk.ld, rows, a.head_dim);
     tc_fence_before();
   }
   if (!ok && lane == 0) {
