@@ -108,10 +108,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   using C = BwdCfg<HD>;
   const muon_attention_t& a = P.a;
   const int heads = a.heads, head = static_cast<int>(blockIdx.x % heads);
-  // later rows see more keys: the long tiles of a causal sequence start first
-  const int slot = static_cast<int>(gridDim.x / heads - 1 - blockIdx.x / heads);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int row0;
-  const SeqRange r = seq_range(a, tile_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), kRows, slot, &row0));
+  const SeqRange r = find_tile(a, false, kRows, static_cast<int>(blockIdx.x / heads), static_cast<int>(gridDim.x / heads),
+                               lane, &row0);
   if (row0 >= r.m) return;
   const int shift = r.n - r.m;  // causal: row i sees keys j <= i + shift
   const int keys = a.causal ? min(r.n, min(row0 + kRows, r.m) + shift) : r.n;
@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   uint64_t* done = ds_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  uint8_t *sq = smem, *sdo = smem + C::kTile, *sk = smem + C::kOffRing3, *sv = smem + C::kOffRing2;
+  const int kvh = head / (heads / a.kv_heads);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -149,6 +150,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    // the first blocks are on their way before the other warps are set up
+    mbar_expect_tx(q_full, 2 * C::kTile);
+    for (int c = 0; c < HD / 64; ++c) {
+      tma_load_3d(sq + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0);
+      tma_load_3d(sdo + c * kChunk, &P.tdo, q_full, c * 64, head, r.q0 + row0);
+    }
+    if (n > 0) {
+      load_tile<HD>(sk, &P.tk, &k_full[0], kvh, r.k0);
+      load_tile<HD>(sv, &P.tv, &v_full[0], kvh, r.k0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -159,19 +171,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t kDp = 256, kDq = 384;  // columns of dP and dQ; S at 128 (j & 1)
-  uint8_t *sq = smem, *sdo = smem + C::kTile, *sk = smem + C::kOffRing3, *sv = smem + C::kOffRing2;
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
-      const int kvh = head / (heads / a.kv_heads);
-      mbar_expect_tx(q_full, 2 * C::kTile);
-      for (int c = 0; c < HD / 64; ++c) {
-        tma_load_3d(sq + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0);
-        tma_load_3d(sdo + c * kChunk, &P.tdo, q_full, c * 64, head, r.q0 + row0);
-      }
-      int kl = 0, vl = 0;
-      for (int j = 0; j < n; ++j) {
+      int kl = n > 0, vl = kl;
+      for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&k_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
         if (!ok) break;
         load_tile<HD>(sk + j % 3 * C::kTile, &P.tk, &k_full[j % 3], kvh, r.k0 + j * kRows);
@@ -327,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   using C = BwdCfg<HD>;
   const muon_attention_t& a = P.a;
   const int kvh = static_cast<int>(blockIdx.x % a.kv_heads), per = a.heads / a.kv_heads;
-  // earlier keys are seen by more rows, and come first
-  const int slot = static_cast<int>(blockIdx.x / a.kv_heads);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int key0;
-  const SeqRange r = seq_range(a, tile_seq(a.k_offsets, a.n_seq, static_cast<int>(a.k_tokens), kRows, slot, &key0));
+  const SeqRange r = find_tile(a, true, kRows, static_cast<int>(blockIdx.x / a.kv_heads),
+                               static_cast<int>(gridDim.x / a.kv_heads), lane, &key0);
   if (key0 >= r.n) return;
   const int shift = r.n - r.m;
   const int tile0 = a.causal ? max(0, key0 - shift) / kRows : 0;  // the first row tile that sees a key
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   uint64_t* done = ds_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  uint8_t *sk = smem, *sv = smem + C::kTile, *sq = smem + C::kOffRing3, *sdo = smem + C::kOffRing2;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -372,6 +377,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    // the first blocks are on their way before the other warps are set up
+    if (n > 0) {
+      mbar_expect_tx(kv_full, 2 * C::kTile);
+      for (int c = 0; c < HD / 64; ++c) {
+        tma_load_3d(sk + c * kChunk, &P.tk, kv_full, c * 64, kvh, r.k0 + key0);
+        tma_load_3d(sv + c * kChunk, &P.tv, kv_full, c * 64, kvh, r.k0 + key0);
+      }
+      load_tile<HD>(sq, &P.tq, &q_full[0], kvh * per, r.q0 + tile0 * kRows);
+      load_tile<HD>(sdo, &P.tdo, &do_full[0], kvh * per, r.q0 + tile0 * kRows);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -382,18 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   constexpr uint32_t kDp = 128, kDv = 256, kDk = 256 + HD;  // columns; S at 0
-  uint8_t *sk = smem, *sv = smem + C::kTile, *sq = smem + C::kOffRing3, *sdo = smem + C::kOffRing2;
   bool ok = true;
 
   if (warp == 0) {
     if (lane == 0 && n > 0) {
-      mbar_expect_tx(kv_full, 2 * C::kTile);
-      for (int c = 0; c < HD / 64; ++c) {
-        tma_load_3d(sk + c * kChunk, &P.tk, kv_full, c * 64, kvh, r.k0 + key0);
-        tma_load_3d(sv + c * kChunk, &P.tv, kv_full, c * 64, kvh, r.k0 + key0);
-      }
-      int ql = 0, dl = 0, h = kvh * per, t = tile0;
-      for (int j = 0; j < n; ++j) {
+      int ql = 1, dl = 1, h = kvh * per, t = tile0;
+      if (++t == tile0 + tiles) t = tile0, ++h;
+      for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&q_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
         if (!ok) break;
         load_tile<HD>(sq + j % 3 * C::kTile, &P.tq, &q_full[j % 3], h, r.q0 + t * kRows);

@@ -101,10 +101,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   const muon_attention_t& a = P.a;
   const int heads = a.heads;
   const int head = static_cast<int>(blockIdx.x % heads);
-  // later rows see more keys: the long tiles of a causal sequence start first
-  const int slot = static_cast<int>(gridDim.x / heads - 1 - blockIdx.x / heads);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int row0;
-  const SeqRange r = seq_range(a, tile_seq(a.q_offsets, a.n_seq, static_cast<int>(a.q_tokens), 2 * kRows, slot, &row0));
+  const SeqRange r = find_tile(a, false, 2 * kRows, static_cast<int>(blockIdx.x / heads),
+                               static_cast<int>(gridDim.x / heads), lane, &row0);
   if (row0 >= r.m) return;
   const int shift = r.n - r.m;  // causal: row i sees keys j <= i + shift
   auto blocks_of = [&](int i) {  // key blocks of tile i
@@ -130,12 +130,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert(8 * (2 * C::kStages + 23) + 8 <= 512, "barrier region");
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int kvh = head / (heads / a.kv_heads);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], (nb0 > 0 ? 1 : 0) + (nb1 > 0 ? 1 : 0));
+      mbar_init(&empty[s], nb0 > 0 && nb1 > 0 ? 2 : 1);  // an arrival from each working issuer
     }
     mbar_init(q_full, 1);
     for (int i = 0; i < 2; ++i) {
@@ -150,6 +150,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     }
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    // Q and the first K block are on their way before the other warps are set up
+    if (nmax > 0) {
+      mbar_expect_tx(q_full, 2 * C::kQBytes);
+      for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(smem + i * C::kQBytes + c * C::kQChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
+      mbar_expect_tx(&full[0], C::kKvBytes);
+      for (int c = 0; c < HD / 64; ++c)
+        tma_load_3d(smem + C::kOffKv + c * C::kKvChunk, &P.tk, &full[0], c * 64, kvh, r.k0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -169,14 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && nmax > 0) {
-      const int kvh = head / (heads / a.kv_heads);
-      mbar_expect_tx(q_full, 2 * C::kQBytes);
-      for (int i = 0; i < 2; ++i)
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(smem + i * C::kQBytes + c * C::kQChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
       bool ok = true;
-      int loads = 0, j[2] = {0, 0};  // the next K and V block
-      for (int t = 0; t < 2 * nmax; ++t) {
+      int loads = 1, j[2] = {1, 0};  // the next K and V block; K_0 is under way
+      for (int t = 1; t < 2 * nmax; ++t) {
         const int s = t % C::kStages;
         const bool is_v = j[1] < nmax && t == pos_v(j[1]);
         if (!mbar_wait(&empty[s], static_cast<uint32_t>((t / C::kStages) & 1) ^ 1u, abort_flag)) {
