@@ -63,7 +63,7 @@ static_assert(kTmemX + kStages * kXCols <= 512, "tensor memory");
 constexpr int kPairs = 74;                    // CTA pairs of a B200 (148 SMs)
 
 constexpr int kTileKb = 2;                    // what a tile costs beside its k-blocks, in k-blocks
-constexpr int kMaxBalanced = 1024;            // groups whose lengths every block adds up
+constexpr int kMaxBalanced = 128;             // groups whose lengths every block adds up
 
 // N: tile rows (out) of a CTA pair, half of them from each CTA's dY columns.
 template <int N>
@@ -206,33 +206,41 @@ __device__ __forceinline__ Job job_of(const WgradParams& P, uint32_t u) {
 __device__ __forceinline__ void balanced_range(const WgradParams& P, int pair, int pairs, int lane, uint32_t* u) {
   const int groups = P.a.groups;
   const int64_t per = static_cast<int64_t>(P.s.tiles_o) * P.s.tiles_i;
-  auto weight = [&](int g) {
+  int w[kMaxBalanced / 32];  // all loads first
+#pragma unroll
+  for (int c = 0; c < kMaxBalanced / 32; ++c) {
+    const int g = c * 32 + lane;
     int lo = 0, hi = 0;
     if (g < groups) group_range(P.a, g, &lo, &hi);
-    return g < groups ? static_cast<int64_t>((hi - lo + kTok - 1) / kTok + kTileKb) : int64_t(0);
-  };
+    w[c] = g < groups ? (hi - lo + kTok - 1) / kTok + kTileKb : 0;
+  }
   int64_t total = 0;
-  for (int g0 = 0; g0 < groups; g0 += 32) total += weight(g0 + lane);
+#pragma unroll
+  for (int c = 0; c < kMaxBalanced / 32; ++c) total += w[c];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= per;
+  const int64_t share[2] = {total * pair / pairs, total * (pair + 1) / pairs};
   int64_t before = 0, count[2] = {0, 0};
-  for (int g0 = 0; g0 < groups; g0 += 32) {
-    const int64_t w = weight(g0 + lane);
-    int64_t upto = w * per;
+#pragma unroll
+  for (int c = 0; c < kMaxBalanced / 32; ++c) {
+    if (c * 32 >= groups) break;
+    const int64_t mine = w[c] * per;
+    int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
-    const int64_t base = before + upto - w * per;
+    const int64_t base = before + upto - mine;
     before += __shfl_sync(0xffffffffu, upto, 31);
-    if (w == 0) continue;
+    if (w[c] == 0) continue;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       // tiles of the group whose middle base + i w + w / 2 lies before the share's end
-      const int64_t x = 2 * (total * (pair + e) / pairs - base) - w;
-      const int64_t n = x <= 0 ? 0 : (x + 2 * w - 1) / (2 * w);
+      const int64_t x = 2 * (share[e] - base) - w[c];
+      const int64_t up = x + 2 * w[c] - 1;
+      const int64_t n = x <= 0 ? 0 : up < (int64_t(1) << 32) ? static_cast<uint32_t>(up) / (2u * w[c]) : up / (2 * w[c]);
       count[e] += n < per ? n : per;
     }
   }
@@ -356,38 +364,36 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t par = 0;
-      int64_t loads = 0;
-      bool ok = true;
-      for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
-        const Job j = job_of<N>(P, u);
-        for (int kb = 0; kb < j.nkb; ++kb) {
-          if (!mbar_wait(&empty[s], par ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+    int s = 0;
+    uint32_t par = 0, loads = 0;
+    bool ok = true;
+    for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
+      const Job j = job_of<N>(P, u);
+      const int o = j.o0 + rank * (N / 2), i = j.i0 + rank * 128;
+      for (int kb = 0; kb < j.nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], par ^ 1u, abort_flag));
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* st = smem + s * C::kStageBytes;
-          const int t = j.t0 + kb * kTok, o = j.o0 + rank * (N / 2), i = j.i0 + rank * 128;
+          const int t = j.t0 + kb * kTok;
           mbar_expect_tx(&full[s], C::kStageBytes);
           tma_load_3d(st + C::kYBytes, &P.tq, &full[s], i, t, 0);
           tma_load_3d(st + C::kOffE, &P.te, &full[s], i / 512 * kEBytesRow, t, 0);
 #pragma unroll
           for (int c = 0; c < N / 128; ++c)
             tma_load_3d(st + c * (64 * kTok * 2), &P.ty, &full[s], o + 64 * c, t, 0);
-          ++loads;
-          if (++s == kStages) s = 0, par ^= 1u;
         }
+        ++loads;
+        if (++s == kStages) s = 0, par ^= 1u;
       }
-      if (!ok) {
-        set_error(a.status_dev, MUON_ERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      // never leave with bulk copies still landing in shared memory
-      for (int64_t r = loads > kStages ? loads - kStages : 0; r < loads; ++r)
-        mbar_wait(&full[r % kStages], static_cast<uint32_t>((r / kStages) & 1), nullptr);
     }
+    if (!ok && lane == 0) {
+      set_error(a.status_dev, MUON_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // never leave with bulk copies still landing in shared memory
+    for (uint32_t r = loads > kStages ? loads - kStages : 0; r < loads; ++r)
+      mbar_wait(&full[r % kStages], (r / kStages) & 1u, nullptr);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
