@@ -12,9 +12,9 @@
 // q 2^E has 7 significant bits and is exact in bf16, so every product dY q 2^E is exact and
 // sums are fp32 in tensor memory.
 //
-// Tile 256 (in) x 256 (out) per CTA pair (cta_group::2): each CTA restores its 128 columns of
-// X and loads its 128 columns of dY, so a restored element serves 256 output rows. Persistent,
-// one CTA per SM, warps:
+// Tile 256 (in) x N = 128, 256 or 384 (out) per CTA pair (cta_group::2): each CTA restores its
+// 128 columns of X and loads its N / 2 columns of dY, so a restored element serves N output
+// rows. Persistent, one CTA per SM, warps:
 //   0      TMA producer: per 64-token k-block 16 KB of dY, 8 KB of q and 1 KB of exponents
 //          into a ring of 8 stages
 //   1      TMEM allocator and (first CTA) MMA issuer
@@ -23,7 +23,6 @@
 //          cannot reach this one's sums
 //   14-21  epilogue: a lane is a column of dW's row, so the accumulator's registers are
 //          written in whole 128-byte rows at any alignment, without a transpose
-// Tensor memory: 256 columns of accumulator and 8 stages of X^T of 32 columns.
 // Split of the work: tiles are dealt to the 74 CTA pairs in whole rounds; the tiles left over
 // for the last round are split along the tokens into as many parts as keep all pairs busy,
 // whose fp32 partial sums a second kernel adds in order (no atomics).
@@ -52,34 +51,35 @@ constexpr int kTok = 64;                      // tokens per k-block
 constexpr int kQBytes = 128 * kTok;           // a CTA's stored X columns of one k-block
 constexpr int kEBytesRow = 16;                // exponents of 512 columns, the smallest TMA row
 constexpr int kEBytes = kEBytesRow * kTok;
-constexpr int kStages = 8;
 constexpr int kTeams = 3, kTeamWarps = 4;     // restore teams take k-blocks in turn
 constexpr int kRestoreWarps = kTeams * kTeamWarps, kEpiWarps = 8;
 constexpr int kFirstEpi = 2 + kRestoreWarps;
 constexpr int kThreads = 32 * (2 + kRestoreWarps + kEpiWarps);
-constexpr int kTmemX = 256;                   // first tensor-memory column of the X^T stages
 constexpr int kXCols = kTok / 2;              // columns of one stage
-static_assert(kTmemX + kStages * kXCols <= 512, "tensor memory");
 constexpr int kPairs = 74;                    // CTA pairs of a B200 (148 SMs)
 
-constexpr int kTileKb = 2;                    // what a tile costs beside its k-blocks, in k-blocks
 constexpr int kMaxBalanced = 128;             // groups whose lengths every block adds up
 
-// N: tile rows (out) of a CTA pair, half of them from each CTA's dY columns.
+// N: tile rows (out) of a CTA pair, half of them from each CTA's dY columns. Tensor memory holds
+// 256 / N accumulators (one of 256 or 384 columns) and, behind them, the stages of X^T.
 template <int N>
 struct WgradCfg {
-  static constexpr int kAcc = 256 / N;        // accumulators in tensor memory
+  static constexpr int kAcc = N >= 256 ? 1 : 256 / N;
+  static constexpr int kTmemX = kAcc * N;     // first column of the X^T stages
+  static constexpr int kStages = (512 - kTmemX) / kXCols;
   static constexpr int kYBytes = N / 2 * kTok * 2;
   static constexpr int kOffE = kYBytes + kQBytes;
   static constexpr int kStageBytes = kOffE + kEBytes;
   static constexpr int kOffBar = kStages * kStageBytes;
   static constexpr int kSmemBytes = kOffBar + 256 + 1024;
   static_assert(kSmemBytes <= 227 * 1024 && kStageBytes % 1024 == 0, "shared memory");
+  static_assert(kStages >= kTeams, "a team stays within one round of the ring");
 };
 
 // How the tiles are dealt: `whole` tiles by one unit each, the `left` ones by `splits` units.
 struct WgradSplit {
-  int32_t n;                 // tile rows, 256 or 128
+  int32_t n;                 // tile rows: 384, 256 or 128
+  int32_t tile_kb;           // what a tile costs beside its k-blocks, in k-blocks
   int32_t tiles_o, tiles_i;
   int32_t splits;
   int32_t balance;           // tiles dealt in contiguous runs of equal k-blocks
@@ -88,20 +88,28 @@ struct WgradSplit {
   size_t part_bytes;
 };
 
-// Picks the tile height and the split of the last round by a model of their time in cycles:
-// a round costs its k-blocks (620 cycles at 256 rows, where the products are the limit;
-// 400 at 128 rows, where restoring X is) and what its start and its epilogue add that
-// nothing hides (6000 and 3500: one accumulator of 256 columns against two of 128);
-// partial sums and the second launch cost about 7000. Tiles of 128 rows waste less of a small
-// or ragged `out`, and hide the epilogue of short groups.
+// What a tile of N rows costs a pair: cycles per k-block (measured on long groups: at 128 rows
+// the restoring of X is the limit, above the products are), and what its start and an epilogue
+// that nothing hides add.
+struct TileCost {
+  int n;
+  double per_kb, fixed;
+};
+constexpr TileCost kCosts[3] = {{384, 950., 5500.}, {256, 700., 4500.}, {128, 560., 2500.}};
+
+// Picks the tile height and the split of the last round by the cost of the longest pair's tiles;
+// partial sums and the second launch cost about 7000 cycles. High tiles restore X for more rows;
+// low ones waste less of a small or ragged `out`.
 WgradSplit split_of(const muon_weight_grad_t& a) {
   const int64_t kb = (a.tokens / a.groups + kTok - 1) / kTok;  // of a mean group
   WgradSplit best{};
   double best_cost = 0;
-  for (int n = 256; n >= 128; n /= 2) {
-    const double per_kb = n == 256 ? 620. : 400., fixed = n == 256 ? 6000. : 3500.;
+  for (const TileCost& t : kCosts) {
+    const int n = t.n;
+    const double per_kb = t.per_kb, fixed = t.fixed;
     WgradSplit s{};
     s.n = n;
+    s.tile_kb = static_cast<int32_t>(fixed / per_kb);
     s.tiles_o = static_cast<int32_t>((a.out + n - 1) / n);
     s.tiles_i = static_cast<int32_t>((a.in + kIn - 1) / kIn);
     s.part_bytes = static_cast<size_t>(n) * kIn * 4;
@@ -200,57 +208,51 @@ __device__ __forceinline__ Job job_of(const WgradParams& P, uint32_t u) {
 }
 
 // The tiles [u[0], u[1]) of CTA pair `pair` out of `pairs`, by one warp: tiles in order, each
-// weighing its k-blocks and kTileKb, and dealt to the pair in whose share of the total weight
+// weighing its k-blocks and tile_kb, and dealt to the pair in whose share of the total weight
 // its middle lies. A router's groups differ in length: dealt in turn, 64 experts of 0 to 1487
 // tokens left the busiest pair with 1.6 times the mean, dealt so with 1.2.
 __device__ __forceinline__ void balanced_range(const WgradParams& P, int pair, int pairs, int lane, uint32_t* u) {
   const int groups = P.a.groups;
-  const int64_t per = static_cast<int64_t>(P.s.tiles_o) * P.s.tiles_i;
+  const int per = P.s.tiles_o * P.s.tiles_i;  // below 2^24: a float holds it
   int w[kMaxBalanced / 32];  // all loads first
 #pragma unroll
   for (int c = 0; c < kMaxBalanced / 32; ++c) {
     const int g = c * 32 + lane;
     int lo = 0, hi = 0;
     if (g < groups) group_range(P.a, g, &lo, &hi);
-    w[c] = g < groups ? (hi - lo + kTok - 1) / kTok + kTileKb : 0;
+    w[c] = g < groups ? (hi - lo + kTok - 1) / kTok + P.s.tile_kb : 0;
   }
-  int64_t total = 0;
+  // in fp32: every pair computes the same numbers, and rounds monotonically, so that one's end
+  // is the next one's start
+  uint32_t mine = 0;
 #pragma unroll
-  for (int c = 0; c < kMaxBalanced / 32; ++c) total += w[c];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= per;
-  const int64_t share[2] = {total * pair / pairs, total * (pair + 1) / pairs};
-  int64_t before = 0, count[2] = {0, 0};
+  for (int c = 0; c < kMaxBalanced / 32; ++c) mine += w[c];
+  const float total = static_cast<float>(__reduce_add_sync(0xffffffffu, mine));
+  const float share[2] = {total * pair / pairs, total * (pair + 1) / pairs};
+  uint32_t before = 0, count[2] = {0, 0};
 #pragma unroll
   for (int c = 0; c < kMaxBalanced / 32; ++c) {
     if (c * 32 >= groups) break;
-    const int64_t mine = w[c] * per;
-    int64_t upto = mine;
+    uint32_t upto = w[c];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += x;
     }
-    const int64_t base = before + upto - mine;
+    const float base = static_cast<float>(before + upto - w[c]);
     before += __shfl_sync(0xffffffffu, upto, 31);
-    if (w[c] == 0) continue;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      // tiles of the group whose middle base + i w + w / 2 lies before the share's end
-      const int64_t x = 2 * (share[e] - base) - w[c];
-      const int64_t up = x + 2 * w[c] - 1;
-      const int64_t n = x <= 0 ? 0 : up < (int64_t(1) << 32) ? static_cast<uint32_t>(up) / (2u * w[c]) : up / (2 * w[c]);
-      count[e] += n < per ? n : per;
+      // tiles of the group whose middle base + (i + 1/2) w / per lies before the share's end
+      const float n = w[c] == 0 ? 0.f : ceilf((share[e] - base) * per / w[c] - 0.5f);
+      count[e] += static_cast<uint32_t>(fminf(fmaxf(n, 0.f), w[c] == 0 ? 0.f : static_cast<float>(per)));
     }
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) count[e] += __shfl_xor_sync(0xffffffffu, count[e], o);
+  for (int e = 0; e < 2; ++e) count[e] = __reduce_add_sync(0xffffffffu, count[e]);
   if (lane == 0) {
-    u[0] = static_cast<uint32_t>(count[0]);
-    u[1] = pair + 1 == pairs ? static_cast<uint32_t>(P.s.units) : static_cast<uint32_t>(count[1]);
+    u[0] = count[0];
+    u[1] = pair + 1 == pairs ? static_cast<uint32_t>(P.s.units) : count[1];
   }
 }
 
@@ -308,6 +310,13 @@ __device__ __forceinline__ void write_rows(T* p, int64_t ld, int n, bool accumul
     if (i < n) put(p, __uint_as_float(v[i]));
 }
 
+// The row of the tile that chunk c (64 columns of dY) of a CTA starts at: a product takes the
+// first half of its N rows from the first CTA and the second half from the other.
+template <int N>
+__device__ __forceinline__ int chunk_row(int rank, int c) {
+  return N > 256 && c == 2 ? 256 + rank * 64 : rank * (N < 256 ? N / 2 : 128) + 64 * c;
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constant__ WgradParams P) {
   using C = WgradCfg<N>;
@@ -315,15 +324,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // this CTA's loads have landed
-  uint64_t* ready = full + kStages;   // first CTA's: both CTAs' operands are in place
-  uint64_t* empty = ready + kStages;  // the MMAs have read the stage
-  uint64_t* tfull = empty + kStages;
+  uint64_t* ready = full + C::kStages;   // first CTA's: both CTAs' operands are in place
+  uint64_t* empty = ready + C::kStages;  // the MMAs have read the stage
+  uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* range = tmem_slot + 2;    // this pair's units
-  static_assert(8 * (3 * kStages + 5) + 16 <= 256, "barrier region");
+  static_assert(8 * (3 * C::kStages + 5) + 16 <= 256, "barrier region");
 
   const muon_weight_grad_t& a = P.a;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     tma_prefetch(&P.ty);
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&ready[s], 2 * kTeamWarps);
       mbar_init(&empty[s], 1);
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     bool ok = true;
     for (uint32_t u = unit0; u < unit1 && ok; u += stride) {
       const Job j = job_of<N>(P, u);
-      const int o = j.o0 + rank * (N / 2), i = j.i0 + rank * 128;
+      const int i = j.i0 + rank * 128;
       for (int kb = 0; kb < j.nkb; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], par ^ 1u, abort_flag));
         if (!ok) break;
@@ -381,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           tma_load_3d(st + C::kOffE, &P.te, &full[s], i / 512 * kEBytesRow, t, 0);
 #pragma unroll
           for (int c = 0; c < N / 128; ++c)
-            tma_load_3d(st + c * (64 * kTok * 2), &P.ty, &full[s], o + 64 * c, t, 0);
+            tma_load_3d(st + c * (64 * kTok * 2), &P.ty, &full[s], j.o0 + chunk_row<N>(rank, c), t, 0);
         }
         ++loads;
-        if (++s == kStages) s = 0, par ^= 1u;
+        if (++s == C::kStages) s = 0, par ^= 1u;
       }
     }
     if (!ok && lane == 0) {
@@ -392,12 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       *abort_flag = 1;
     }
     // never leave with bulk copies still landing in shared memory
-    for (uint32_t r = loads > kStages ? loads - kStages : 0; r < loads; ++r)
-      mbar_wait(&full[r % kStages], (r / kStages) & 1u, nullptr);
+    for (uint32_t r = loads > C::kStages ? loads - C::kStages : 0; r < loads; ++r)
+      mbar_wait(&full[r % C::kStages], (r / C::kStages) & 1u, nullptr);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, N, true);  // A from tensor memory, B MN-major
+      // A from tensor memory, B MN-major; 384 rows are two products, of 256 and 128
+      constexpr uint32_t idesc = idesc_bf16_f32(256, N < 256 ? N : 256, true), idesc2 = idesc_bf16_f32(256, 128, true);
       constexpr uint32_t mn = static_cast<uint32_t>((64 * kTok * 2) >> 4) << 16;
       const uint32_t base = smem_u32(smem) >> 4;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -420,10 +430,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           if (!ok) break;
           if (elect_one()) {
             const uint32_t bd = mn | (base + s * (C::kStageBytes >> 4));
-            const uint32_t at = tmem + kTmemX + s * kXCols;
+            const uint32_t at = tmem + C::kTmemX + s * kXCols;
 #pragma unroll
             for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens: 8 columns, 2 KB of a chunk
+            {
               umma_f16_pair_ts(d, at + 8u * kk, bd + 128u * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
+              if (N > 256)
+                umma_f16_pair_ts(d + 256, at + 8u * kk, bd + ((2 * 64 * kTok * 2) >> 4) + 128u * kk, idesc2,
+                                 (kb | kk) != 0 ? 1u : 0u);
+            }
             umma_commit_pair(smem_u32(&empty[s]));
             umma_commit_pair(peer_addr(&empty[s], 1));
             if (kb + 1 == j.nkb) {
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
               umma_commit_pair(peer_addr(&tfull[acc], 1));
             }
           }
-          if (++s == kStages) s = 0, par ^= 1u;
+          if (++s == C::kStages) s = 0, par ^= 1u;
         }
       }
       if (!ok && lane == 0) {
@@ -458,8 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       const int src = (grp & 7) * 4 + (lane & 3);
       for (int kb = static_cast<int>((team + kTeams - q0 % kTeams) % kTeams); kb < j.nkb; kb += kTeams) {
         const uint32_t q = q0 + kb;
-        const int s = static_cast<int>(q % kStages);
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], static_cast<uint32_t>((q / kStages) & 1), abort_flag))) {
+        const int s = static_cast<int>(q % C::kStages);
+        // A team does not see every k-block, and copies may land out of order: the parity of `full`
+        // alone could still be the one before the stage's previous copy. That copy has landed once
+        // the products that read it are complete. (They are at most one phase ahead: the team's
+        // own previous copy was issued after those of the round before.)
+        const uint32_t round = q / C::kStages;
+        const bool landed = (round == 0 || mbar_wait(&empty[s], (round - 1) & 1u, abort_flag)) &&
+                            mbar_wait(&full[s], round & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, landed)) {
           ok = false;
           if (lane == 0) {
             set_error(a.status_dev, MUON_ERR_TIMEOUT);
@@ -492,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
             }
           // the dY of tokens past the group: zeros too
           for (int t = live + w; t < kTok; t += kTeamWarps)
-            if (lane < N / 8) *reinterpret_cast<uint2*>(st + (lane >> 4) * (64 * kTok * 2) + t * 128 + (lane & 15) * 8) = make_uint2(0, 0);
+#pragma unroll
+            for (int c = 0; c < N / 128; ++c)
+              *reinterpret_cast<uint32_t*>(st + c * (64 * kTok * 2) + t * 128 + lane * 4) = 0;
           fence_proxy_async_smem();
         }
         uint32_t x[2][16];
@@ -507,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
             act8_restore4(v[2 * h + 1], sc[b][0], sc[b][1], &x[h][4 * b + 2], &x[h][4 * b + 3]);
           }
         }
-        const uint32_t at = tmem + kTmemX + s * kXCols + lanes;
+        const uint32_t at = tmem + C::kTmemX + s * kXCols + lanes;
         tmem_st_16x256b_x4(at, x[0]);
         tmem_st_16x256b_x4(at + (16u << 16), x[1]);
         tmem_wait_st();
@@ -752,6 +776,8 @@ extern "C" MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, 
                           a->ld_e)))
     return MUON_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = P.s.n == 256 ? launch_wgrad<256>(P, dev, sms, st) : launch_wgrad<128>(P, dev, sms, st);
+  const cudaError_t e = P.s.n == 384   ? launch_wgrad<384>(P, dev, sms, st)
+                        : P.s.n == 256 ? launch_wgrad<256>(P, dev, sms, st)
+                                       : launch_wgrad<128>(P, dev, sms, st);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
