@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
   cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  griddep_launch_dependents();  // the join, where there is one, waits for this grid's end
   const uint32_t unit0 = P.s.balance ? range[0] : blockIdx.x >> 1;
   const uint32_t unit1 = P.s.balance ? range[1] : static_cast<uint32_t>(P.s.units);
   const uint32_t stride = P.s.balance ? 1 : gridDim.x >> 1;
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
 // 4 columns of one row, kBatch partial sums in flight.
 template <int N>
 __global__ void __launch_bounds__(kIn) wgrad_join_kernel(const __grid_constant__ WgradParams P) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 10;
   const muon_weight_grad_t& a = P.a;
   const int64_t r = blockIdx.x / (N / 4);
   const int row = blockIdx.x % (N / 4) * 4 + threadIdx.x / 64, c0 = threadIdx.x % 64 * 4;
@@ -624,6 +625,7 @@ __global__ void __launch_bounds__(kIn) wgrad_join_kernel(const __grid_constant__
   const int64_t o = j.o0 + row;
   const int kb = (hi - lo + kTok - 1) / kTok, splits = P.s.splits, cols = static_cast<int>(a.in) - j.i0 - c0;
   if (o >= a.out || cols <= 0) return;
+  griddep_wait();  // the partial sums are complete
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* p = P.parts + r * splits * (N * kIn) + row * kIn + c0;
   for (int s0 = 0; s0 < splits; s0 += kBatch) {
@@ -631,8 +633,9 @@ __global__ void __launch_bounds__(kIn) wgrad_join_kernel(const __grid_constant__
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int s = s0 + b;
-      // a part without tokens has no partial sum
-      const bool have = s < splits && static_cast<int64_t>(kb) * s / splits != static_cast<int64_t>(kb) * (s + 1) / splits;
+      // a part without tokens has no partial sum (every part has some if there are k-blocks enough)
+      const uint32_t ukb = static_cast<uint32_t>(kb);
+      const bool have = s < splits && (kb >= splits || ukb * s / splits != ukb * (s + 1) / splits);
       v[b] = have ? __ldcs(reinterpret_cast<const float4*>(p + static_cast<int64_t>(s) * (N * kIn)))
                   : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -738,8 +741,12 @@ cudaError_t launch_wgrad(const WgradParams& P, int dev, int sms, cudaStream_t st
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, wgrad_kernel<N>, P);
   if (e != cudaSuccess || P.s.left == 0) return e;
-  wgrad_join_kernel<N><<<static_cast<unsigned>(P.s.left * (N / 4)), kIn, 0, st>>>(P);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(static_cast<unsigned>(P.s.left * (N / 4)), 1, 1);
+  cfg.blockDim = dim3(kIn, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, wgrad_join_kernel<N>, P);
 }
 
 }  // namespace
