@@ -29,8 +29,7 @@ namespace {
 // with short ones, whose launch costs the host a microsecond less.
 constexpr int kItemsPerLaunch = 128, kFewItems = 4;
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;
-constexpr int kUnitsPerBlock = kThreads * kUnits;
+constexpr int kUnits = 4;                // rows a thread handles
 constexpr int64_t kMaxCols = int64_t(1) << 26;
 
 template <int kItems>
@@ -41,14 +40,26 @@ struct Act8Launch {
 };
 static_assert(sizeof(Act8Launch<kItemsPerLaunch>) < 32000, "kernel parameter space");
 
-// Units of a row: whole groups of four, so that a group's lanes stay together.
-__host__ __device__ inline int64_t units_per_row(int64_t cols) { return (cols + 31) / 32 * 4; }
-
-struct Unit {
-  int64_t row;
-  int32_t col;     // first column
-  bool live;       // inside the matrix's rows
+// How a block covers a matrix: `span` units (whole groups of four, so that a group's lanes stay
+// together) of each row, one of `chunks` equal parts of it, in `rows` rows at a time, kUnits
+// times. A thread keeps its columns and steps down the rows, so that it divides once.
+struct Cover {
+  int32_t chunks, span, rows;
 };
+
+__host__ __device__ inline Cover cover_of(int64_t cols) {
+  const int32_t units = static_cast<int32_t>((cols + 31) / 32 * 4);
+  Cover c;
+  c.chunks = (units + kThreads - 1) / kThreads;
+  c.span = ((units + c.chunks - 1) / c.chunks + 3) / 4 * 4;
+  c.rows = kThreads / c.span;
+  return c;
+}
+
+inline int64_t blocks_of(const muon_act8_t& a) {
+  const Cover c = cover_of(a.cols);
+  return (a.rows + kUnits * c.rows - 1) / (kUnits * c.rows) * c.chunks;
+}
 
 template <int kItems>
 __device__ __forceinline__ int find_item(const Act8Launch<kItems>& L) {
@@ -60,74 +71,69 @@ __device__ __forceinline__ int find_item(const Act8Launch<kItems>& L) {
   return lo;
 }
 
-// Units of a block: from unit `rem` of row `row` on; `inv` divides by the units of a row.
-struct Span {
-  int64_t row;
-  uint32_t rem, upr, inv;
+// This thread's columns [col, col + 8) and its rows row, row + step, ..; live(u): in the matrix.
+struct Place {
+  int64_t row, rows;
+  int32_t col, step, cols;
+  __device__ __forceinline__ bool live(int u) const { return row + u * step < rows; }
+  __device__ __forceinline__ bool whole() const { return col + 8 <= cols; }
 };
 
-__device__ __forceinline__ Span block_span(const muon_act8_t& a, int64_t block) {
-  Span s;
-  s.upr = static_cast<uint32_t>(units_per_row(a.cols));
-  const int64_t base = block * kUnitsPerBlock;
-  s.row = base / s.upr;
-  s.rem = static_cast<uint32_t>(base - s.row * s.upr);
-  s.inv = 0xFFFFFFFFu / s.upr + 1;
-  return s;
-}
-
-__device__ __forceinline__ Unit unit_at(const muon_act8_t& a, const Span& s, int u) {
-  const uint32_t r = s.rem + u * kThreads + threadIdx.x, upr = s.upr;
-  // r / upr: r < 2 upr for long rows; for short ones r upr < 2^22 and the reciprocal is exact
-  const uint32_t dr = upr >= kUnitsPerBlock ? (r >= upr ? 1u : 0u) : __umulhi(r, s.inv);
-  Unit t;
-  t.row = s.row + dr;
-  t.col = static_cast<int32_t>(r - dr * upr) * 8;
-  t.live = t.row < a.rows;
-  return t;
+__device__ __forceinline__ Place place_of(const muon_act8_t& a, int block) {
+  const Cover c = cover_of(a.cols);
+  const int rb = block / c.chunks, chunk = block - rb * c.chunks;
+  const int rt = static_cast<int>(threadIdx.x) / c.span, ct = static_cast<int>(threadIdx.x) - rt * c.span;
+  Place p;
+  p.step = c.rows;
+  p.cols = static_cast<int32_t>(a.cols);
+  p.col = (chunk * c.span + ct) * 8;
+  p.row = static_cast<int64_t>(rb) * (kUnits * c.rows) + rt;
+  p.rows = rt < c.rows && p.col < p.cols ? a.rows : 0;
+  return p;
 }
 
 // The 8 values of a unit as they are in memory (BF16: 4 words, F32: 8); columns past the matrix
 // read as 0.
 template <bool kBf16>
-__device__ __forceinline__ void load_unit(const muon_act8_t& a, const Unit& t, bool vec, uint32_t (&w)[kBf16 ? 4 : 8]) {
+__device__ __forceinline__ void load_unit(const void* X, int64_t off, const Place& t, int u, bool vec,
+                                          uint32_t (&w)[kBf16 ? 4 : 8]) {
 #pragma unroll
   for (int i = 0; i < (kBf16 ? 4 : 8); ++i) w[i] = 0;
-  if (!t.live || t.col >= a.cols) return;
-  const int64_t off = t.row * a.ld_x + t.col;
+  if (!t.live(u)) return;
   if (kBf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(a.X) + off;
-    if (vec && t.col + 8 <= a.cols) {
+    const uint16_t* p = static_cast<const uint16_t*>(X) + off;
+    if (vec && t.whole()) {
       const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
       w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (t.col + i < a.cols) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+        if (t.col + i < t.cols) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
     }
   } else {
-    const uint32_t* p = static_cast<const uint32_t*>(a.X) + off;
-    if (vec && t.col + 8 <= a.cols) {
+    const uint32_t* p = static_cast<const uint32_t*>(X) + off;
+    if (vec && t.whole()) {
       const uint4 v0 = __ldcs(reinterpret_cast<const uint4*>(p)), v1 = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
       w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
       w[kBf16 ? 0 : 4] = v1.x; w[kBf16 ? 0 : 5] = v1.y; w[kBf16 ? 0 : 6] = v1.z; w[kBf16 ? 0 : 7] = v1.w;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (t.col + i < a.cols) w[kBf16 ? 0 : i] = p[i];
+        if (t.col + i < t.cols) w[kBf16 ? 0 : i] = p[i];
     }
   }
 }
 
 // Stores units u0 .. u0 + kCount - 1 of the thread: all loads first.
 template <bool kBf16, int kCount>
-__device__ __forceinline__ void store_units(const muon_act8_t& a, const Span& sp, bool vec, int u0) {
+__device__ __forceinline__ void store_units(const muon_act8_t& a, const Place& t, bool vec, int u0) {
   uint32_t w[kCount][kBf16 ? 4 : 8];
+  const int64_t row0 = t.row + u0 * t.step;
 #pragma unroll
-  for (int u = 0; u < kCount; ++u) load_unit<kBf16>(a, unit_at(a, sp, u0 + u), vec, w[u]);
+  for (int u = 0; u < kCount; ++u)
+    load_unit<kBf16>(a.X, (row0 + u * t.step) * a.ld_x + t.col, t, u0 + u, vec, w[u]);
 #pragma unroll
   for (int u = 0; u < kCount; ++u) {
-    const Unit t = unit_at(a, sp, u0 + u);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -141,29 +147,29 @@ __device__ __forceinline__ void store_units(const muon_act8_t& a, const Span& sp
     const uint32_t byte = be == 255 ? 255u : static_cast<uint32_t>(max(be - 6, 1));
     // 2^-E; a group with a NaN or an infinity stores zeros under byte 255
     const float inv = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
-    // Clamped before the rounding, which keeps whole numbers; adding 1.5 * 2^23 rounds half to
-    // even and leaves the integer in the low bits (a conversion instruction runs at a quarter
-    // of the rate).
+    // Adding 1.5 * 2^23 to the (exact) product rounds half to even and leaves the integer in the
+    // low bits (a conversion instruction runs at a quarter of the rate); then the clamp.
     uint32_t v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      v[i] = __float_as_uint(fminf(fmaxf(x[i] * inv, -127.f), 127.f) + 12582912.f);
+      v[i] = __float_as_uint(fminf(fmaxf(fmaf(x[i], inv, 12582912.f), 12582912.f - 127.f), 12582912.f + 127.f));
     uint32_t pk[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       pk[i] = __byte_perm(__byte_perm(v[4 * i], v[4 * i + 1], 0x0040), __byte_perm(v[4 * i + 2], v[4 * i + 3], 0x0040), 0x5410);
       if (byte == 255u) pk[i] = 0;
     }
-    if (!t.live || t.col >= a.cols) continue;
-    int8_t* q = a.q + t.row * a.ld_q + t.col;
-    if (t.col + 8 <= a.cols) {
+    if (!t.live(u0 + u)) continue;
+    const int64_t row = row0 + u * t.step;
+    int8_t* q = a.q + row * a.ld_q + t.col;
+    if (t.whole()) {
       *reinterpret_cast<uint2*>(q) = make_uint2(pk[0], pk[1]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (t.col + i < a.cols) q[i] = static_cast<int8_t>(pk[i >> 2] >> (8 * (i & 3)));
+        if (t.col + i < t.cols) q[i] = static_cast<int8_t>(pk[i >> 2] >> (8 * (i & 3)));
     }
-    if ((threadIdx.x & 3) == 0) a.exps[t.row * a.ld_e + (t.col >> 5)] = static_cast<uint8_t>(byte);
+    if ((threadIdx.x & 3) == 0) a.exps[row * a.ld_e + (t.col >> 5)] = static_cast<uint8_t>(byte);
   }
 }
 
@@ -176,13 +182,13 @@ template <int kItems>
 __global__ void __launch_bounds__(kThreads, 5) act8_store_kernel(const __grid_constant__ Act8Launch<kItems> L) {
   const int it = find_item(L);
   const muon_act8_t& a = L.a[it];
-  const Span sp = block_span(a, static_cast<int64_t>(blockIdx.x - L.block_base[it]));
+  const Place t = place_of(a, static_cast<int>(blockIdx.x) - L.block_base[it]);
   const bool vec = rows_aligned(a);
   if (a.dtype == MUON_BF16) {
-    store_units<true, kUnits>(a, sp, vec, 0);
+    store_units<true, kUnits>(a, t, vec, 0);
   } else {
-    store_units<false, kUnits / 2>(a, sp, vec, 0);
-    store_units<false, kUnits / 2>(a, sp, vec, kUnits / 2);
+    store_units<false, kUnits / 2>(a, t, vec, 0);
+    store_units<false, kUnits / 2>(a, t, vec, kUnits / 2);
   }
 }
 
@@ -190,38 +196,37 @@ template <int kItems>
 __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_constant__ Act8Launch<kItems> L) {
   const int it = find_item(L);
   const muon_act8_t& a = L.a[it];
-  const Span sp = block_span(a, static_cast<int64_t>(blockIdx.x - L.block_base[it]));
+  const Place t = place_of(a, static_cast<int>(blockIdx.x) - L.block_base[it]);
   const bool vec = rows_aligned(a);
   uint2 w[kUnits];
   uint32_t byte[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const Unit t = unit_at(a, sp, u);
     w[u] = make_uint2(0, 0);
     byte[u] = 1;
-    if (!t.live || t.col >= a.cols) continue;
-    const int8_t* q = a.q + t.row * a.ld_q + t.col;
-    if (t.col + 8 <= a.cols) {
+    if (!t.live(u)) continue;
+    const int64_t row = t.row + u * t.step;
+    const int8_t* q = a.q + row * a.ld_q + t.col;
+    if (t.whole()) {
       w[u] = __ldcs(reinterpret_cast<const uint2*>(q));
     } else {
       uint32_t pk[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (t.col + i < a.cols) pk[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(q[i])) << (8 * (i & 3));
+        if (t.col + i < t.cols) pk[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(q[i])) << (8 * (i & 3));
       w[u] = make_uint2(pk[0], pk[1]);
     }
-    byte[u] = a.exps[t.row * a.ld_e + (t.col >> 5)];
+    byte[u] = a.exps[row * a.ld_e + (t.col >> 5)];
   }
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    const Unit t = unit_at(a, sp, u);
-    if (!t.live || t.col >= a.cols) continue;
+    if (!t.live(u)) continue;
     const uint32_t sc = act8_scale2(byte[u]);
     uint32_t y[4];  // bf16 pairs
     act8_restore4(w[u].x, sc, sc, &y[0], &y[1]);
     act8_restore4(w[u].y, sc, sc, &y[2], &y[3]);
-    const int64_t off = t.row * a.ld_x + t.col;
-    const bool whole = vec && t.col + 8 <= a.cols;
+    const int64_t off = (t.row + u * t.step) * a.ld_x + t.col;
+    const bool whole = vec && t.whole();
     if (a.dtype == MUON_BF16) {
       uint16_t* p = static_cast<uint16_t*>(a.X) + off;
       if (whole) {
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_con
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (t.col + i < a.cols) p[i] = static_cast<uint16_t>(y[i >> 1] >> (16 * (i & 1)));
+          if (t.col + i < t.cols) p[i] = static_cast<uint16_t>(y[i >> 1] >> (16 * (i & 1)));
       }
     } else {
       float x[8];
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_con
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (t.col + i < a.cols) p[i] = x[i];
+          if (t.col + i < t.cols) p[i] = x[i];
       }
     }
   }
@@ -302,7 +307,7 @@ muon_status_t launch_act8(const muon_act8_t* items, int n, bool store, cudaStrea
   for (int i = 0; i < n; ++i) {
     L.a[i] = items[i];
     L.block_base[i] = static_cast<int32_t>(blocks);
-    blocks += (units_per_row(items[i].cols) * items[i].rows + kUnitsPerBlock - 1) / kUnitsPerBlock;
+    blocks += blocks_of(items[i]);
   }
   L.block_base[n] = static_cast<int32_t>(blocks);
   if (blocks == 0) return MUON_OK;
@@ -318,9 +323,7 @@ muon_status_t run_act8(const muon_act8_t* items, int n, bool store, void* stream
   const muon_status_t d = current_device(&dev, &sms);
   if (d != MUON_OK) return d;
   for (int i = 0; i < n; ++i)  // nothing runs unless every launch fits its grid
-    if (units_per_row(items[i].cols) * items[i].rows / kUnitsPerBlock >
-        (int64_t(1) << 30) / kItemsPerLaunch)
-      return MUON_ERR_SHAPE;
+    if (blocks_of(items[i]) > (int64_t(1) << 30) / kItemsPerLaunch) return MUON_ERR_SHAPE;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (n <= kFewItems) return launch_act8<kFewItems>(items, n, store, st);
   for (int i0 = 0; i0 < n; i0 += kItemsPerLaunch) {
