@@ -124,44 +124,63 @@ __device__ __forceinline__ void load_unit(const void* X, int64_t off, const Plac
   }
 }
 
-// Stores units u0 .. u0 + kCount - 1 of the thread: all loads first.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// Two signed 16-bit numbers clamped to [-127, 127].
+__device__ __forceinline__ uint32_t clamp127_s16x2(uint32_t x) {
+  uint32_t r;
+  asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x007F007Fu));
+  asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0xFF81FF81u));
+  return r;
+}
+
+// Stores rows u0 .. u0 + kCount - 1 of the thread: all loads first.
 template <bool kBf16, int kCount>
 __device__ __forceinline__ void store_units(const muon_act8_t& a, const Place& t, bool vec, int u0) {
   uint32_t w[kCount][kBf16 ? 4 : 8];
-  const int64_t row0 = t.row + u0 * t.step;
+  const int64_t row0 = t.row + u0 * t.step, off0 = row0 * a.ld_x + t.col, step_x = t.step * a.ld_x;
 #pragma unroll
-  for (int u = 0; u < kCount; ++u)
-    load_unit<kBf16>(a.X, (row0 + u * t.step) * a.ld_x + t.col, t, u0 + u, vec, w[u]);
+  for (int u = 0; u < kCount; ++u) load_unit<kBf16>(a.X, off0 + u * step_x, t, u0 + u, vec, w[u]);
+  int8_t* q = a.q + row0 * a.ld_q + t.col;
+  uint8_t* ex = a.exps + row0 * a.ld_e + (t.col >> 5);
+  const int64_t step_q = t.step * a.ld_q, step_e = t.step * a.ld_e;
 #pragma unroll
-  for (int u = 0; u < kCount; ++u) {
+  for (int u = 0; u < kCount; ++u, q += step_q, ex += step_e) {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       x[i] = __uint_as_float(!kBf16 ? w[u][kBf16 ? 0 : i] : (i & 1) ? w[u][i >> 1] & 0xFFFF0000u : w[u][i >> 1] << 16);
     uint32_t top = 0;  // magnitudes compare as integers, NaN above infinity
+    if (kBf16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 4; ++i) top = max_u16x2(top, w[u][i] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFF0000u, top << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, w[u][kBf16 ? 0 : i] & 0x7FFFFFFFu);
+    }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int be = static_cast<int>(top >> 23);
     const uint32_t byte = be == 255 ? 255u : static_cast<uint32_t>(max(be - 6, 1));
     // 2^-E; a group with a NaN or an infinity stores zeros under byte 255
     const float inv = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
-    // Adding 1.5 * 2^23 to the (exact) product rounds half to even and leaves the integer in the
-    // low bits (a conversion instruction runs at a quarter of the rate); then the clamp.
-    uint32_t v[8];
+    // Adding 1.5 * 2^23 to the (exact) product rounds half to even and leaves the integer, at most
+    // 128, in the low bits (a conversion instruction runs at a quarter of the rate); the clamp
+    // then takes two of them at a time.
+    uint32_t v[8], pk[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = __float_as_uint(fminf(fmaxf(fmaf(x[i], inv, 12582912.f), 12582912.f - 127.f), 12582912.f + 127.f));
-    uint32_t pk[2];
+    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(fmaf(x[i], inv, 12582912.f));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      pk[i] = __byte_perm(__byte_perm(v[4 * i], v[4 * i + 1], 0x0040), __byte_perm(v[4 * i + 2], v[4 * i + 3], 0x0040), 0x5410);
+      pk[i] = __byte_perm(clamp127_s16x2(__byte_perm(v[4 * i], v[4 * i + 1], 0x5410)),
+                          clamp127_s16x2(__byte_perm(v[4 * i + 2], v[4 * i + 3], 0x5410)), 0x6420);
       if (byte == 255u) pk[i] = 0;
     }
     if (!t.live(u0 + u)) continue;
-    const int64_t row = row0 + u * t.step;
-    int8_t* q = a.q + row * a.ld_q + t.col;
     if (t.whole()) {
       *reinterpret_cast<uint2*>(q) = make_uint2(pk[0], pk[1]);
     } else {
@@ -169,7 +188,7 @@ __device__ __forceinline__ void store_units(const muon_act8_t& a, const Place& t
       for (int i = 0; i < 8; ++i)
         if (t.col + i < t.cols) q[i] = static_cast<int8_t>(pk[i >> 2] >> (8 * (i & 3)));
     }
-    if ((threadIdx.x & 3) == 0) a.exps[row * a.ld_e + (t.col >> 5)] = static_cast<uint8_t>(byte);
+    if ((threadIdx.x & 3) == 0) *ex = static_cast<uint8_t>(byte);
   }
 }
 
@@ -200,13 +219,14 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_con
   const bool vec = rows_aligned(a);
   uint2 w[kUnits];
   uint32_t byte[kUnits];
+  const int8_t* q = a.q + t.row * a.ld_q + t.col;
+  const uint8_t* ex = a.exps + t.row * a.ld_e + (t.col >> 5);
+  const int64_t step_q = t.step * a.ld_q, step_e = t.step * a.ld_e;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < kUnits; ++u, q += step_q, ex += step_e) {
     w[u] = make_uint2(0, 0);
     byte[u] = 1;
     if (!t.live(u)) continue;
-    const int64_t row = t.row + u * t.step;
-    const int8_t* q = a.q + row * a.ld_q + t.col;
     if (t.whole()) {
       w[u] = __ldcs(reinterpret_cast<const uint2*>(q));
     } else {
@@ -216,16 +236,17 @@ __global__ void __launch_bounds__(kThreads) act8_restore_kernel(const __grid_con
         if (t.col + i < t.cols) pk[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(q[i])) << (8 * (i & 3));
       w[u] = make_uint2(pk[0], pk[1]);
     }
-    byte[u] = a.exps[row * a.ld_e + (t.col >> 5)];
+    byte[u] = *ex;
   }
+  int64_t off = t.row * a.ld_x + t.col;
+  const int64_t step_x = t.step * a.ld_x;
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < kUnits; ++u, off += step_x) {
     if (!t.live(u)) continue;
     const uint32_t sc = act8_scale2(byte[u]);
     uint32_t y[4];  // bf16 pairs
     act8_restore4(w[u].x, sc, sc, &y[0], &y[1]);
     act8_restore4(w[u].y, sc, sc, &y[2], &y[3]);
-    const int64_t off = (t.row + u * t.step) * a.ld_x + t.col;
     const bool whole = vec && t.whole();
     if (a.dtype == MUON_BF16) {
       uint16_t* p = static_cast<uint16_t*>(a.X) + off;
