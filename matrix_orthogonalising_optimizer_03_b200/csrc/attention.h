@@ -104,7 +104,9 @@ __device__ __forceinline__ SeqRange find_tile(const muon_attention_t& a, bool by
     const int mid = (lo + hi + 1) >> 1;
     if (clamp_offset(off, mid, tokens) / rows + mid <= t) lo = mid; else hi = mid - 1;
   }
-  *row0 = (t - (clamp_offset(off, lo, tokens) / rows + lo)) * rows;
+  // slots below the first sequence's (its offset may be past 0) have no tile
+  const int tile = t - (clamp_offset(off, lo, tokens) / rows + lo);
+  *row0 = tile < 0 ? 0x7FFFFFFF : tile * rows;
   return seq_range(a, lo);
 }
 

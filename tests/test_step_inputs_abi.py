@@ -61,7 +61,7 @@ def wgrad(**kw):
     (dict(exps=FAKE + 2 * GB + 4), 1), (dict(dW=FAKE + 3 * GB + 1), 1), (dict(offsets=FAKE + 4 * GB + 2), 1),
     (dict(status_dev=FAKE + 2), 1), (dict(dW=FAKE + 64), 4), (dict(dW=FAKE + GB + 64), 4),
     (dict(dW=FAKE + 2 * GB + 64), 4), (dict(dW=FAKE + 4 * GB), 4), (dict(status_dev=FAKE + 3 * GB + 400), 4),
-    (dict(tokens=1 << 31), 2), (dict(out=1 << 20, in_=1 << 20, ld_w=1 << 20, ld_dy=1 << 20, ld_q=1 << 20,
+    (dict(tokens=1 << 31), 2), (dict(tokens=(1 << 31) - 63), 2), (dict(out=1 << 20, in_=1 << 20, ld_w=1 << 20, ld_dy=1 << 20, ld_q=1 << 20,
                                      ld_e=1 << 20, groups=1), 2)])
 def test_weight_grad_refusals(lib, kw, status):
     assert lib.muon_weight_grad(ctypes.byref(wgrad(**kw)), None, 0, None) == status

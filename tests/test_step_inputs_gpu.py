@@ -49,7 +49,7 @@ def ints(values):
 # ---------------------------------------------------------------- checkpoints
 @pytest.mark.parametrize("rows,cols,ld,dtype", [
     (1, 1, 1, F32), (1, 1, 1, BF16), (3, 31, 31, BF16), (5, 32, 32, F32), (7, 33, 40, BF16),
-    (64, 255, 255, F32), (129, 1021, 1024, BF16), (33, 2048, 2053, F32), (300, 320, 320, BF16)])
+    (2, 9001, 9001, BF16), (3, 20000, 20008, F32), (1000, 8, 8, BF16), (64, 255, 255, F32), (129, 1021, 1024, BF16), (33, 2048, 2053, F32), (300, 320, 320, BF16)])
 def test_store_and_restore_follow_the_definition(B, rows, cols, ld, dtype):
     g = gen_of(rows * 1000 + cols)
     x = torch.zeros(rows, ld, device="cuda", dtype=dtype)[:, :cols]
@@ -238,6 +238,50 @@ def test_weight_grad_offsets_are_clamped(B):
         ref.check(dw[e], want[0], 100 * ref.U_F32 * mag[0], f"group {e}")
 
 
+@pytest.mark.parametrize("out,inn,groups,top", [
+    (320, 512, 64, 700),       # a layer's experts: runs of tiles of equal work
+    (40, 24, 200, 90),         # more groups than are weighed
+    (384, 256, 90, 520), (128, 520, 128, 70), (700, 260, 33, 400), (64, 64, 129, 1)])
+def test_weight_grad_of_many_ragged_groups_is_exact(B, out, inn, groups, top):
+    """Whole numbers again, so every tile height and every way to deal the tiles gives the same
+    bits; a quarter of the groups is empty, the first and the last among them."""
+    g = gen_of(groups)
+    counts = torch.randint(0, top + 1, (groups,), generator=g, device="cuda").tolist()
+    counts = [0 if i % 4 == 0 or i == groups - 1 else c for i, c in enumerate(counts)]
+    t = max(1, sum(counts))
+    ck = B.new_act8(t, inn)
+    ck.q[:, :inn].copy_(torch.randint(-4, 5, (t, inn), generator=g, device="cuda"))
+    ck.exps.fill_(127)
+    dy = dy_of(g, t, out)
+    dy.copy_(torch.randint(-3, 4, (t, out), generator=g, device="cuda"))
+    off = offsets_of(counts)
+    want, _ = ref.weight_grad(dy, ck.q[:, :inn], off)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dw = torch.full((groups, out, inn), 9.0, device="cuda")
+    plan = B.WeightGradPlan(dy, ck, dw, offsets=ints(off), status=status)
+    for _ in range(40):                        # again and again: copies land in another order each time
+        plan.apply()
+    assert torch.equal(dw.double(), want) and int(status) == 0
+    B.weight_grad(dy, ck, dw, offsets=ints(off), accumulate=True)
+    assert torch.equal(dw.double(), 2 * want)
+
+
+def test_weight_grad_dense_of_each_tile_height_is_exact(B):
+    """One tile row of 384, 256 and 128, over many tiles along `in`, many times over."""
+    g = gen_of(31)
+    for out, inn, tokens in ((384, 15360, 512), (256, 12288, 700), (100, 9000, 130), (1024, 1024, 16384)):
+        ck = B.new_act8(tokens, inn)
+        ck.q[:, :inn].copy_(torch.randint(-2, 3, (tokens, inn), generator=g, device="cuda"))
+        ck.exps.fill_(126)
+        dy = dy_of(g, tokens, out)
+        dy.copy_(torch.randint(-2, 3, (tokens, out), generator=g, device="cuda"))
+        dw = torch.zeros(out, inn, device="cuda")
+        plan = B.WeightGradPlan(dy, ck, dw)
+        for _ in range(20):
+            plan.apply()
+        assert torch.equal(dw, dy.float().t() @ (ck.q[:, :inn].float() * 0.5))     # exact in fp32 too
+
+
 # ---------------------------------------------------------------- attention
 def inputs(seed, q_len, k_len, h, g, d, pad=0, sharp=1.0):
     """q, k, v, dout as views of wider buffers."""
@@ -322,6 +366,58 @@ def test_attention_of_packed_qkv_and_head_major_tensors(B):
     hm = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v, do)]
     res = both(B, *hm, lens, lens, True)
     assert torch.equal(res[0], o) and torch.equal(res[3], dqkv[:, 0])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n_seq,first", [(32, 0), (33, 0), (70, 700)])
+def test_attention_of_many_sequences(B, n_seq, first, causal):
+    """Up to 32 sequences a block finds its tile by level, beyond by bisection; the first sequence
+    may start anywhere, and rows outside every sequence stay."""
+    gen = torch.Generator().manual_seed(n_seq)
+    lens = torch.randint(0, 90, (n_seq,), generator=gen).tolist()
+    lens[3], lens[7], lens[-1] = 300, 0, 129
+    k_lens = [0 if i % 11 == 5 else n + i % 3 for i, n in enumerate(lens)]
+    q, k, v, do = inputs(n_seq, lens, k_lens, 2, 1, 64)
+    pad = torch.zeros(first, 2, 64, device="cuda", dtype=BF16)
+    q, do = torch.cat([pad, q]), torch.cat([pad, do])
+    k, v = torch.cat([pad[:, :1], k]), torch.cat([pad[:, :1], v])
+    qo, ko = ints(offsets_of(lens, first)), ints(offsets_of(k_lens, first))
+    o = torch.full_like(q, 4.0)
+    lse = torch.full((2, q.shape[0]), 4.0, device="cuda")
+    grads = [torch.full_like(t, 4.0) for t in (q, k, v)]
+    B.attention_forward(q, k, v, o, lse, qo, ko, causal=causal)
+    B.attention_backward(do, q, k, v, o, lse, *grads, qo, ko, causal=causal)
+    want, tol = ref.attention(q[first:], k[first:], v[first:], lens, k_lens, causal, 0.125, do[first:], o[first:],
+                              lse[:, first:])
+    ref.check(o[first:], want["o"], tol["o"], "o")
+    ref.check(lse[:, first:], want["lse"], tol["lse"], "lse")
+    for n, t in zip(("dq", "dk", "dv"), grads):
+        ref.check(t[first:], want[n], tol[n], n)
+    assert all(bool((t[:first] == 4).all()) for t in [o, *grads]) and bool((lse[:, :first] == 4).all())
+
+
+def test_attention_on_two_streams_at_once(B):
+    """Two plans on two streams, again and again, each with its own workspace: the bits of a call
+    alone."""
+    plans, outs = [], []
+    for i, d in enumerate((64, 128)):
+        q, k, v, do = inputs(40 + i, [900, 300], [900, 300], 4, 2, d)
+        off = ints([0, 900, 1200])
+        o, lse = torch.zeros_like(q), torch.zeros(4, 1200, device="cuda")
+        grads = tuple(torch.zeros_like(t) for t in (q, k, v))
+        plans.append(B.AttentionPlan(q, k, v, o, lse, off, off, grads=(do, *grads)))
+        plans[-1].forward()
+        plans[-1].backward()
+        outs.append((o, lse, *grads))
+    torch.cuda.synchronize()
+    alone = [[t.clone() for t in ts] for ts in outs]
+    streams = [torch.cuda.Stream() for _ in plans]
+    for _ in range(10):
+        for p, s in zip(plans, streams):
+            p.forward(stream=s)
+            p.backward(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x, y in zip(alone, outs) for a, b in zip(x, y))
 
 
 def test_attention_one_sequence_without_offsets(B):
