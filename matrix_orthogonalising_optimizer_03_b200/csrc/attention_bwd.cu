@@ -44,7 +44,12 @@ struct BwdCfg {
   static constexpr int kOffRing2 = kOffRing3 + kRing3 * kTile;
   static constexpr int kOffVec = kOffRing2 + kRing2 * kTile;  // lse and delta of a block of rows
   static constexpr int kVecBytes = 2 * kRows * 4;
-  static constexpr int kOffBar = kOffVec + 2 * kVecBytes;
+  // Head dimension 64 leaves tensor memory for a second S in the kernel of dK and dV, so that the
+  // next block's scores are computed during this block's softmax; it then needs lse and delta of
+  // three blocks.
+  static constexpr bool kTwoS = HD == 64;
+  static constexpr int kVecs = kTwoS ? 3 : 2;
+  static constexpr int kOffBar = kOffVec + kVecs * kVecBytes;
   static constexpr int kSmemBytes = kOffBar + 512;
 };
 
@@ -127,7 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   uint64_t* dp_full = s_full + 2;
   uint64_t* dp_read = dp_full + 1;
   uint64_t* ds_full = dp_read + 1;  // per block parity
-  uint64_t* done = ds_full + 2;
+  uint64_t* turn = ds_full + 2;     // per half of the parts and lane quarter: exponentials done
+  uint64_t* done = turn + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t *sq = smem, *sdo = smem + C::kTile, *sk = smem + C::kOffRing3, *sv = smem + C::kOffRing2;
@@ -145,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       mbar_init(&s_full[s], 1);
       mbar_init(&ds_full[s], kCompute);
     }
+    for (int e = 0; e < 8; ++e) mbar_init(&turn[e], 2);
     mbar_init(dp_full, 1);
     mbar_init(dp_read, kCompute);
     mbar_init(done, 1);
@@ -280,8 +287,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       // keys of this quarter of the block that the row sees
       const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows - part * 32;
       const bool masked = __any_sync(0xffffffffu, vis < 32);
+      // Of the four warps of a scheduler two take turns with the other two at the exponentials:
+      // one pair's other work overlaps the other's.
+      const int grp = part >> 1;
+      if (grp == 1 || j > 0) ok = wait_all(&turn[4 * (1 - grp) + w], grp == 1 ? j : j - 1, abort_flag);
+      if (!ok) break;
 #pragma unroll
       for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e]), sl, -lse)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&turn[4 * grp + w]);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tmem + lanes + kDp + part * 32, p);
@@ -349,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   uint64_t* do_full = q_empty + 3;   // ring of dout blocks
   uint64_t* do_ready = do_full + 2;
   uint64_t* do_empty = do_ready + 2;
-  uint64_t* s_full = do_empty + 2;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* dp_full = p_full + 1;
+  uint64_t* s_full = do_empty + 2;   // per block parity (two S), as p_full
+  uint64_t* p_full = s_full + 2;
+  uint64_t* dp_full = p_full + 2;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* done = ds_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -370,8 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       mbar_init(&do_ready[s], 1);
       mbar_init(&do_empty[s], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kCompute);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], kCompute);
+    }
     mbar_init(dp_full, 1);
     mbar_init(ds_full, kCompute);
     mbar_init(done, 1);
@@ -397,7 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  constexpr uint32_t kDp = 128, kDv = 256, kDk = 256 + HD;  // columns; S at 0
+  constexpr uint32_t kDp = 128, kDv = 256, kDk = 256 + HD;  // columns; S at 0, and at 384 (two S)
+  // the S of block j, and barriers that may complete for the next block before this one's wait
+  auto s_col = [](int j) { return C::kTwoS && (j & 1) ? 384u : 0u; };
+  auto s_par = [](int j) { return C::kTwoS ? j & 1 : 0; };
+  auto s_phase = [](int j) { return C::kTwoS ? j >> 1 : j; };
   bool ok = true;
 
   if (warp == 0) {
@@ -421,15 +441,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       for (int j = dl > 2 ? dl - 2 : 0; j < dl; ++j) mbar_wait(&do_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), nullptr);
     }
   } else if (warp == 1) {
-    // One issuer keeps the order dV_j, S_{j+1}, dK_j, dP_{j+1}: S_{j+1} is what the softmax waits
-    // for next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1}
+    // One issuer keeps the order dV_j, S_{j+1} (two S: S_{j+2}), dK_j, dP_{j+1}: S_{j+1} is what the
+    // softmax waits for next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1}
     // came 600 cycles later.
     if (n > 0) {
-      auto score = [&](int j) {  // S^T_j; P^T_{j-1} over it went into a product issued before
+      auto score = [&](int j) {  // S^T_j; the P^T before it in these columns went into an earlier product
         if (!wait_all(&q_ready[j % 3], j / 3, abort_flag)) return false;
         if (elect_one()) {
-          product_ss<HD>(tmem, smem_u32(sk), smem_u32(sq) + j % 3 * C::kTile);
-          umma_commit(s_full);
+          product_ss<HD>(tmem + s_col(j), smem_u32(sk), smem_u32(sq) + j % 3 * C::kTile);
+          umma_commit(&s_full[s_par(j)]);
         }
         return true;
       };
@@ -441,15 +461,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
         }
         return true;
       };
-      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0);
+      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0) && (!C::kTwoS || n < 2 || score(1));
       for (int j = 0; j < n && ok; ++j) {
-        ok = wait_all(p_full, j, abort_flag);
+        ok = wait_all(&p_full[s_par(j)], s_phase(j), abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDv, tmem, smem_u32(sdo) + (j & 1) * C::kTile, j > 0);
+          product_ts<HD>(tmem + kDv, tmem + s_col(j), smem_u32(sdo) + (j & 1) * C::kTile, j > 0);
           umma_commit(&do_empty[j & 1]);
         }
-        if (j + 1 < n) ok = score(j + 1);
+        constexpr int ahead = C::kTwoS ? 2 : 1;
+        if (j + ahead < n) ok = score(j + ahead);
         ok = ok && wait_all(ds_full, j, abort_flag);
         if (!ok) break;
         if (elect_one()) {
@@ -477,11 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
         l[e] = x == -INFINITY ? INFINITY : x * kLog2e;
         d[e] = i < live ? P.delta[at + i] : 0.f;
       }
-      // two of these vectors: block j - 2 is done with its own once its last product is complete
+      // With two of these vectors, block j - 2 is done with its own once its last product is
+      // complete; with three, the copy of Q_j came after that of block j - 3.
       ok = wait_all(&q_full[j % 3], j / 3, abort_flag) &&
-           (j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
+           (C::kVecs == 3 || j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
       if (!ok) break;
-      float* v = reinterpret_cast<float*>(smem + C::kOffVec + (j & 1) * C::kVecBytes);
+      float* v = reinterpret_cast<float*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e * 32 + lane] = l[e];
@@ -504,11 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     const float sl = a.scale * kLog2e;
     int t = tile0;
     for (int j = 0; j < n; ++j) {
-      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(s_full, j, abort_flag);
+      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(&s_full[s_par(j)], s_phase(j), abort_flag);
       if (!ok) break;
-      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + (j & 1) * C::kVecBytes) + part * 8;
+      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes) + part * 8;
       const float4* dlt = lse + kRows / 4;
-      const uint32_t ts = tmem + lanes + part * 32, tp = ts + kDp;
+      const uint32_t ts = tmem + lanes + s_col(j) + part * 32, tp = tmem + lanes + kDp + part * 32;
       uint32_t s[32], p[32], pk[16];
       tmem_ld32(ts, s);
       tmem_wait_ld();
@@ -534,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(&p_full[s_par(j)]);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tp, p);
