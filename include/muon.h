@@ -351,7 +351,8 @@ MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, void* works
  *   s_max[h] = max(s_max[h], largest S_ij of head h over all sequences)
  * A row that sees no key has o = 0 and lse = -inf. s_max is raised, never lowered, so it
  * collects the maximum over micro-batches: set it to -inf before the first (NaN logits do
- * not raise it). Rows outside every sequence are neither read nor written.
+ * not raise it). Rows outside every sequence are not written, and what they hold does not
+ * matter.
  * The backward pass recomputes P = exp(S - lse) and needs the forward pass's o and lse:
  *   delta_i = o_i . dout_i,  dV = P^T dout,  dS = P (dout V^T - delta)
  *   dQ = scale dS K,  dK = scale dS^T Q   (dK and dV summed over the heads of a key head)

@@ -177,16 +177,6 @@ def _torch():
     return _torch_module
 
 
-def _find_raw_stream():
-    try:
-        return getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-    except ImportError:
-        return None
-
-
-_raw_stream = _find_raw_stream()
-
-
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.float32:
@@ -244,10 +234,11 @@ def _stream_ptr(stream) -> Optional[int]:
     """The cudaStream_t of a torch stream, by default of the current device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    cuda = _torch().cuda
-    if _raw_stream is not None:  # without building a Stream object
-        return _raw_stream(cuda.current_device())
-    return cuda.current_stream().cuda_stream
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _on_stream(stream):

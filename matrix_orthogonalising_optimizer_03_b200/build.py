@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libmuon.so")
 
 SOURCES = ["muon_api.cpp", "elementwise.cu", "ns_simt.cu", "ns_tc.cu", "noalloc.cu", "diagnostics.cu", "qkclip.cu",
            "act8.cu", "wgrad.cu", "attention.cu", "attention_fwd.cu", "attention_bwd.cu"]
-HEADERS = ["muon_internal.h", "elementwise.h", "ptx.cuh", "ns_tc.h", "validate.h", "attention.h", "act8.cuh"]
+HEADERS = ["muon_internal.h", "elementwise.h", "ptx.cuh", "ns_tc.h", "validate.h", "attention.h", "act8.cuh",
+           "umma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",

@@ -10,9 +10,10 @@
 // matrix instruction restores it without a second rounding.
 //
 // Memory bound: store reads x and writes 1 + 1/32 bytes per element, restore the reverse.
-// A thread owns units of 8 consecutive columns (one or two 16-byte loads, one 8-byte store),
-// four neighbouring lanes a group (two shuffles for amax); kUnits units a thread keep as
-// many loads in flight.
+// A thread owns 8 consecutive columns (one or two 16-byte loads, one 8-byte store) of kUnits
+// rows, all loaded first; four neighbouring lanes hold a group (two shuffles for amax).
+// 16384 x 5632 in bf16: store 65 us (4.3 TB/s, still the instructions: about 10 per element),
+// restore 48 us (5.8 TB/s).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -4,7 +4,7 @@
 #include <cuda_runtime.h>
 
 #include "muon.h"
-#include "ptx.cuh"
+#include "umma.cuh"
 
 namespace muon {
 

@@ -8,12 +8,15 @@
 // and dV, over all query heads of the key head. S and dout V^T are computed in both: seven
 // products instead of five, against fp32 atomics on dQ, whose order changes its sums.
 // In both, 16 warps own a 128 x 128 block in tensor memory, a thread 32 elements of one lane's
-// row (8 warps of 64 elements could not hide the waits and transfers of a block). P and dS are rounded to bf16 (relative 2^-9, errors of either sign) and written back
-// over the scores they came from, where the next product takes them as its tensor-memory
+// row. P and dS are rounded to bf16 (at most 2^-8 relative, errors of either sign) and written
+// back over the scores they came from, where the next product takes them as its tensor-memory
 // operand; the transposes that dV and dK need cost nothing, because the second kernel computes
 // S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
-// Bound by the tensor core: an M = 128 product whose operands both come from shared memory
-// runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles.
+// Per block of head dimension 128 the products take 1536 cycles (dQ) and 2048 (dK, dV) at the
+// full rate; measured 2100 and 3000, the tensor core active 64 and 68 % of the time. An M = 128
+// product whose operands both come from shared memory runs at 0.84 of the rate for N = 128, as
+// it reads 8 KB per 64 cycles; the rest is the chain product - exponential - product of a block.
+// Short sequences are bound by a block's start and end, about 8000 cycles.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -25,7 +28,7 @@
 
 #include "attention.h"
 #include "muon.h"
-#include "ptx.cuh"
+#include "umma.cuh"
 
 namespace muon {
 namespace {
@@ -87,7 +90,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int live, int lane) {
 template <int HD>
 __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
-  const uint32_t ad = (1u << 16) | (a_addr >> 4), bd = (1u << 16) | (b_addr >> 4);
+  const uint32_t ad = desc_lo(a_addr, 16), bd = desc_lo(b_addr, 16);
 #pragma unroll
   for (int k = 0; k < HD / 16; ++k) {
     const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
@@ -100,7 +103,7 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t
 template <int HD>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
-  const uint32_t bd = (static_cast<uint32_t>(kChunk >> 4) << 16) | (b_addr >> 4);
+  const uint32_t bd = desc_lo(b_addr, kChunk);
 #pragma unroll
   for (int k = 0; k < kRows / 16; ++k)
     umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
@@ -339,17 +342,81 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------ dK and dV
+// Sums shared by a cluster: dV and dK of a key tile in fp32, 128 rows x HD each, over the block's
+// shared memory from its start (its products are complete). 16-byte units are swizzled by the row.
+template <int HD>
+__device__ __forceinline__ uint32_t sum_offset(int tensor, int row, int unit) {
+  return static_cast<uint32_t>(((tensor * kRows + row) * (HD / 4) + (unit ^ (row & 7))) * 16);
+}
+
+// A thread's share of its row: half of the columns of dV (parts 0, 1) or dK (2, 3).
+template <int HD>
+__device__ __forceinline__ void leave_sums(uint8_t* smem, uint32_t taddr, int part, int row, bool zero) {
+  const int col = (part & 1) * (HD / 2);
+#pragma unroll
+  for (int c = 0; c < HD / 2; c += 32) {
+    uint32_t v[32];
+    if (!zero) {
+      tmem_ld32(taddr + col + c, v);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<uint4*>(smem + sum_offset<HD>(part >> 1, row, (col + c + e) / 4)) =
+          make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+  }
+}
+
+__device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Adds rows rank * 128 / split .. of both tensors over the cluster's blocks, in their order, and
+// writes them: thread t of 32 kCompute takes 8 columns at a time. Of the tile's rows `rows` exist.
+template <int HD>
+__device__ __forceinline__ void join_sums(const uint8_t* smem, const muon_attention_t& a, int split, int rank, int t, int kvh,
+                                          int64_t token0, int rows) {
+  const int mine = kRows / split, total = 2 * mine * (HD / 8);
+  for (int i = t; i < total; i += 32 * kCompute) {
+    const int u = i % (HD / 8), row = rank * mine + i / (HD / 8) % mine, tensor = i / (HD / 8) / mine;
+    if (row >= rows || u * 8 >= a.head_dim) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int c = 0; c < split; ++c) {
+      const uint32_t base = peer_addr(smem, static_cast<uint32_t>(c));
+      const float4 p = load_cluster_f4(base + sum_offset<HD>(tensor, row, 2 * u));
+      const float4 q = load_cluster_f4(base + sum_offset<HD>(tensor, row, 2 * u + 1));
+      x.x += p.x; x.y += p.y; x.z += p.z; x.w += p.w;
+      y.x += q.x; y.y += q.y; y.z += q.z; y.w += q.w;
+    }
+    const float f = tensor == 0 ? 1.f : a.scale;
+    const muon_heads_t& out = tensor == 0 ? a.dv : a.dk;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out.ptr) + (token0 + row) * out.ld + kvh * out.head + u * 8) =
+        make_uint4(round_bf16x2(x.x * f, x.y * f), round_bf16x2(x.z * f, x.w * f), round_bf16x2(y.x * f, y.y * f),
+                   round_bf16x2(y.z * f, y.w * f));
+  }
+}
+
 // S^T_j = K Q_j^T, dP^T_j = V dout_j^T, dV += P^T_j dout_j, dK += dS^T_j Q_j.
-// Block j runs over the row tiles that see the keys, head after head.
+// Block j runs over the row tiles that see the keys, head after head. With several query heads to
+// a key head and few tiles, a cluster shares the heads (dkv_split): each block leaves its sums in
+// its shared memory, and each then adds a share of the rows over all blocks, in their order.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
   using C = BwdCfg<HD>;
   const muon_attention_t& a = P.a;
-  const int kvh = static_cast<int>(blockIdx.x % a.kv_heads), per = a.heads / a.kv_heads;
+  const int split = static_cast<int>(cluster_num_ctas()), rank = static_cast<int>(cluster_cta_rank());
+  const int block = static_cast<int>(blockIdx.x) / split;
+  const int kvh = block % a.kv_heads, per = a.heads / a.kv_heads / split;
+  const int head0 = (kvh * split + rank) * per;  // this block's query heads: head0 .. head0 + per - 1
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int key0;
-  const SeqRange r = find_tile(a, true, kRows, static_cast<int>(blockIdx.x / a.kv_heads),
-                               static_cast<int>(gridDim.x / a.kv_heads), lane, &key0);
+  const SeqRange r = find_tile(a, true, kRows, block / a.kv_heads, static_cast<int>(gridDim.x) / split / a.kv_heads, lane, &key0);
   if (key0 >= r.n) return;
   const int shift = r.n - r.m;
   const int tile0 = a.causal ? max(0, key0 - shift) / kRows : 0;  // the first row tile that sees a key
@@ -401,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
         tma_load_3d(sk + c * kChunk, &P.tk, kv_full, c * 64, kvh, r.k0 + key0);
         tma_load_3d(sv + c * kChunk, &P.tv, kv_full, c * 64, kvh, r.k0 + key0);
       }
-      load_tile<HD>(sq, &P.tq, &q_full[0], kvh * per, r.q0 + tile0 * kRows);
-      load_tile<HD>(sdo, &P.tdo, &do_full[0], kvh * per, r.q0 + tile0 * kRows);
+      load_tile<HD>(sq, &P.tq, &q_full[0], head0, r.q0 + tile0 * kRows);
+      load_tile<HD>(sdo, &P.tdo, &do_full[0], head0, r.q0 + tile0 * kRows);
     }
   }
   if (warp == 1) {
@@ -422,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
 
   if (warp == 0) {
     if (lane == 0 && n > 0) {
-      int ql = 1, dl = 1, h = kvh * per, t = tile0;
+      int ql = 1, dl = 1, h = head0, t = tile0;
       if (++t == tile0 + tiles) t = tile0, ++h;
       for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&q_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
@@ -486,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     // Stages what the copies do not bring: lse (times log2 e) and delta of the block's rows, and
     // zeros over the rows past the sequence. Such rows, and rows that see no key, get lse = inf:
     // P = 0.
-    int h = kvh * per, t = tile0;
+    int h = head0, t = tile0;
     for (int j = 0; j < n; ++j) {
       const int live = r.m - t * kRows;
       const int64_t at = static_cast<int64_t>(h) * a.q_tokens + r.q0 + t * kRows;
@@ -578,16 +645,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
-    // staged where V and K were: their products are complete
-    const int64_t token = r.k0 + key0 + w * 32;
-    const int rows = ok ? r.n - key0 - w * 32 : 0;
-    const int col = (part & 1) * (HD / 2);
-    if (part < 2)
-      store_rows<HD / 2>(tmem + lanes + kDv + col, sv, w, lane, col, 1.f, n == 0,
-                         static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head + col, a.dv.ld, rows, a.head_dim);
-    else
-      store_rows<HD / 2>(tmem + lanes + kDk + col, sk, w, lane, col, a.scale, n == 0,
-                         static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head + col, a.dk.ld, rows, a.head_dim);
+    if (split > 1) {
+      leave_sums<HD>(smem, tmem + lanes + (part < 2 ? kDv : kDk), part, w * 32 + lane, n == 0);
+    } else {
+      // staged where V and K were: their products are complete
+      const int64_t token = r.k0 + key0 + w * 32;
+      const int rows = ok ? r.n - key0 - w * 32 : 0;
+      const int col = (part & 1) * (HD / 2);
+      if (part < 2)
+        store_rows<HD / 2>(tmem + lanes + kDv + col, sv, w, lane, col, 1.f, n == 0,
+                           static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head + col, a.dv.ld, rows, a.head_dim);
+      else
+        store_rows<HD / 2>(tmem + lanes + kDk + col, sk, w, lane, col, a.scale, n == 0,
+                           static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head + col, a.dk.ld, rows, a.head_dim);
+    }
     tc_fence_before();
   }
   if (!ok && lane == 0) {
@@ -595,10 +666,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     *abort_flag = 1;
   }
   __syncthreads();
+  if (split > 1) {
+    cluster_sync_all();
+    if (warp >= 4)
+      join_sums<HD>(smem, a, split, rank, static_cast<int>(threadIdx.x) - 128, kvh, r.k0 + key0, r.n - key0);
+    cluster_sync_all();  // nobody leaves while its sums are read
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Blocks that share a key tile's query heads: as many (a power of two that divides them, at most
+// 4: a block takes a whole SM, and larger clusters leave SMs of a GPC over) as it takes to give
+// every SM three blocks. Few key heads would otherwise leave SMs idle, and the long tiles of a
+// causal sequence make them wait; more blocks only repeat the loads of K and V and the joins.
+// The whole backward pass at 8192 tokens, causal, split against not: 4 query heads on 1 key head
+// 210 against 500 us, 16 on 4 753 against 769 us.
+int dkv_split(const muon_attention_t& a, int64_t grid) {
+  int split = 1;
+  while (split < 4 && (a.heads / a.kv_heads) % (2 * split) == 0 && grid * split < 3 * 148) split *= 2;
+  return split;
 }
 
 template <int HD>
@@ -620,8 +709,21 @@ cudaError_t launch(const BwdParams& P, int dev, int64_t grid_q, int64_t grid_k, 
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (P.a.k_tokens > 0) attention_dkv_kernel<HD><<<static_cast<unsigned>(grid_k), kThreads, smem, st>>>(P);
-  return cudaGetLastError();
+  if (P.a.k_tokens == 0) return cudaSuccess;
+  const int split = dkv_split(P.a, grid_k);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid_k * split), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attention_dkv_kernel<HD>, P);
 }
 
 }  // namespace

@@ -3,18 +3,21 @@
 //
 // One pass over the keys with a running maximum and sum per row. A CTA owns 256 query rows of
 // one head as two tiles of 128, whose softmax and products alternate on the tensor core:
-//   S_i = Q_i K^T (128 x 128, fp32 in tensor memory), P = exp2(S scale log2 e - m) as bf16 over
-//   the same columns, O_i += P V with P as the tensor-memory operand
-// Warps: 0 TMA producer (Q once, then K and V blocks of 128 keys through a ring), 1 and 2 MMA
-// issuers, one per tile (one issuer for both spent all its time issuing and waiting), 4-7 and 8-11 the softmax of tile 0 and 1, one thread per row. While
-// one tile's softmax runs, the other tile's products do.
+//   S_i = Q_i K^T (fp32 in tensor memory), P = exp2(S scale log2 e - m) as bf16 in tensor memory,
+//   O_i += P V with P as the tensor-memory operand
+// Warps: 0 TMA producer (Q once, then K and V blocks through a ring), 1 and 2 MMA issuers, one per
+// tile (a single issuer spent all its time issuing and waiting), 4-7 and 8-11 the softmax of
+// tile 0 and 1, one thread per row. The next block's S is computed while this block's softmax
+// runs; how tensor memory allows that differs by head dimension (FwdCfg).
 // m is the row's running maximum, moved only when a block exceeds it by more than 2^8 in the
 // exponent: until then P stays below 2^8 and nothing overflows (fp32 sums, bf16 P), and the
 // accumulator, which a thread would have to read and write back, is left alone. P is rounded
-// to bf16 for the product (relative 2^-9 on average errors of either sign); the row's sum
-// adds the unrounded values.
-// Bound by the exponentials: 16 per cycle and SM, 2048 cycles for a block of both tiles, as
-// many as the products of head dimension 128 take (1024 for 64).
+// to bf16 for the product (at most 2^-8 relative, errors of either sign); the row's sum adds the
+// unrounded values.
+// Bounds: head dimension 64 by the exponentials, 16 per cycle and SM (2048 cycles for 128 keys of
+// both tiles, 2900 measured: a warp's FMAs, sums and conversions do not all hide behind them);
+// head dimension 128 by the products (2048 cycles at the full rate; S with both operands in
+// shared memory and 64 columns runs at half of it, 3700 measured).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -27,7 +30,7 @@
 #include "attention.h"
 #include "muon.h"
 #include "ns_tc.h"
-#include "ptx.cuh"
+#include "umma.cuh"
 
 namespace muon {
 
@@ -210,10 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     const int i = warp - 1, n = i == 0 ? nb0 : nb1;
     if (n > 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kKeys, false), idesc_o = idesc_bf16_f32(128, HD, true);
-      // low words of the operand descriptors: address and leading offset, both / 16
-      constexpr uint32_t kmaj = 1u << 16, mn = static_cast<uint32_t>(C::kKvChunk >> 4) << 16;
-      const uint32_t base = smem_u32(smem) >> 4;
-      const uint32_t qd = kmaj | (base + i * (C::kQBytes >> 4));
+      const uint32_t base = smem_u32(smem), qd = desc_lo(base + i * C::kQBytes, 16);
       const uint32_t to = tmem + C::kO + i * HD;
       auto slot_of = [&](int t) { return t % C::kStages; };
       auto wait_bar = [&](uint64_t* bar, int phase) {
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         if (!wait_bar(&full[slot_of(t)], t / C::kStages)) return false;
         if (C::kOwnP && j > 0 && !wait_bar(&s_read[i], j - 1)) return false;
         if (elect_one()) {
-          const uint32_t kd = kmaj | (base + ((C::kOffKv + slot_of(t) * C::kKvBytes) >> 4));
+          const uint32_t kd = desc_lo(base + C::kOffKv + slot_of(t) * C::kKvBytes, 16);
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
             const uint32_t in = (k & 3) * 2, c = k >> 2;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const uint32_t vd = mn | (base + ((C::kOffKv + s * C::kKvBytes) >> 4));
+        const uint32_t vd = desc_lo(base + C::kOffKv + s * C::kKvBytes, C::kKvChunk);
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
           if (!(C::kOwnP ? wait_bar(&p_full[2 * i + h], j) : wait_bar(&p_full[2 * i + (j & 1)], j >> 1))) return false;

@@ -15,17 +15,21 @@
 // Tile 256 (in) x N = 128, 256 or 384 (out) per CTA pair (cta_group::2): each CTA restores its
 // 128 columns of X and loads its N / 2 columns of dY, so a restored element serves N output
 // rows. Persistent, one CTA per SM, warps:
-//   0      TMA producer: per 64-token k-block 16 KB of dY, 8 KB of q and 1 KB of exponents
-//          into a ring of 8 stages
+//   0      TMA producer: per 64-token k-block 8 to 24 KB of dY, 8 KB of q and 1 KB of exponents,
+//          into a ring of 8 stages (N = 384: 4)
 //   1      TMEM allocator and (first CTA) MMA issuer
 //   2-13   restore, three teams that take the k-blocks in turn; the last k-block of a group also
 //          clears the rows past its end in both operands, so that a neighbouring group's NaN
 //          cannot reach this one's sums
 //   14-21  epilogue: a lane is a column of dW's row, so the accumulator's registers are
 //          written in whole 128-byte rows at any alignment, without a transpose
-// Split of the work: tiles are dealt to the 74 CTA pairs in whole rounds; the tiles left over
-// for the last round are split along the tokens into as many parts as keep all pairs busy,
-// whose fp32 partial sums a second kernel adds in order (no atomics).
+// Split of the work: groups of several matrices are dealt in runs of tiles of equal work; other
+// tiles go to the 74 CTA pairs in whole rounds, and those left over for the last round are split
+// along the tokens into as many parts as keep all pairs busy, whose fp32 partial sums a second
+// kernel adds in order (no atomics).
+// Bound by the products and their operands for long groups (128 us for 5632 x 2048 from 8192
+// tokens, 1475 TFLOP/s, at the full clock; 158 us under the power cap), by restoring X at 128
+// rows, and by start and epilogue for short groups.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -37,7 +41,7 @@
 #include "act8.cuh"
 #include "muon.h"
 #include "ns_tc.h"
-#include "ptx.cuh"
+#include "umma.cuh"
 #include "validate.h"
 
 namespace muon {
@@ -409,8 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
     if (rank == 0) {
       // A from tensor memory, B MN-major; 384 rows are two products, of 256 and 128
       constexpr uint32_t idesc = idesc_bf16_f32(256, N < 256 ? N : 256, true), idesc2 = idesc_bf16_f32(256, 128, true);
-      constexpr uint32_t mn = static_cast<uint32_t>((64 * kTok * 2) >> 4) << 16;
-      const uint32_t base = smem_u32(smem) >> 4;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
         tc_fence_after();
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
           ok = wait(&ready[s], par);
           if (!ok) break;
           if (elect_one()) {
-            const uint32_t bd = mn | (base + s * (C::kStageBytes >> 4));
+            const uint32_t bd = desc_lo(smem_u32(smem) + s * C::kStageBytes, 64 * kTok * 2);
             const uint32_t at = tmem + C::kTmemX + s * kXCols;
 #pragma unroll
             for (int kk = 0; kk < kTok / 16; ++kk)  // 16 tokens: 8 columns, 2 KB of a chunk
