@@ -53,31 +53,32 @@ bool encode_heads_map(CUtensorMap* out, const muon_heads_t& t, int64_t tokens, i
 
 namespace {
 
-constexpr int kRows = 128;          // query rows of a tile
-constexpr int kThreads = 384;
+constexpr int kRows = 128;          // query rows of a block
+constexpr int kThreads = 256;
 constexpr float kLazy = 8.f;        // the running maximum moves when exceeded by this (log2)
 
 template <int HD>
 struct FwdCfg {
-  // Tensor memory: the two accumulators leave 256 columns (head dimension 128) or 384 (64).
-  //   128: S in blocks of 64 keys, two buffers a tile, P over the buffer it came from
-  //   64:  S in blocks of 128 keys, one buffer a tile, and P in columns of its own
+  // Half of the tensor memory, 256 columns, beside the accumulator's HD:
+  //   128: S in blocks of 64 keys, two buffers, P over the buffer it came from
+  //   64:  S in blocks of 128 keys, one buffer, and P in columns of its own
   // Either way the next block's S is computed while this block's softmax runs.
   static constexpr bool kOwnP = HD == 64;
   static constexpr int kKeys = kOwnP ? 128 : 64;      // keys of a block
   static constexpr int kHalves = kKeys / 64;          // P is handed over by 64 keys
   static constexpr int kQBytes = kRows * HD * 2;
-  static constexpr int kQChunk = kRows * 128;         // bytes of 64 columns of a Q tile
+  static constexpr int kQChunk = kRows * 128;         // bytes of 64 columns of Q
   static constexpr int kKvBytes = kKeys * HD * 2;
   static constexpr int kKvChunk = kKeys * 128;
-  static constexpr int kStages = 8;                   // K and V blocks in flight
-  static constexpr int kOffKv = 2 * kQBytes;
+  static constexpr int kStages = 5;                   // K and V blocks in flight
+  static constexpr int kOffKv = kQBytes;
   static constexpr int kOffBar = kOffKv + kStages * kKvBytes;
-  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
-  static constexpr int kO = 256;                      // first accumulator column
-  static constexpr int kP = kO + 2 * HD;              // P of its own: 64 columns a tile
-  __host__ __device__ static constexpr uint32_t s_col(int i, int j) { return i * 128 + (kOwnP ? 0 : (j & 1) * 64); }
-  __host__ __device__ static constexpr uint32_t p_col(int i, int j) { return kOwnP ? kP + i * 64 : s_col(i, j); }
+  static constexpr int kSmemBytes = kOffBar + 256;
+  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two blocks share an SM");
+  static constexpr uint32_t kO = 128;                 // first accumulator column
+  static constexpr uint32_t kP = kO + HD;             // P of its own: 64 columns
+  __host__ __device__ static constexpr uint32_t s_col(int j) { return kOwnP ? 0 : (j & 1) * 64; }
+  __host__ __device__ static constexpr uint32_t p_col(int j) { return kOwnP ? kP : s_col(j); }
 };
 
 struct FwdParams {
@@ -99,74 +100,62 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid_constant__ FwdParams P) {
+__global__ void __launch_bounds__(kThreads, 2) attention_fwd_kernel(const __grid_constant__ FwdParams P) {
   using C = FwdCfg<HD>;
   const muon_attention_t& a = P.a;
   const int heads = a.heads;
   const int head = static_cast<int>(blockIdx.x % heads);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   int row0;
-  const SeqRange r = find_tile(a, false, 2 * kRows, static_cast<int>(blockIdx.x / heads),
+  const SeqRange r = find_tile(a, false, kRows, static_cast<int>(blockIdx.x / heads),
                                static_cast<int>(gridDim.x / heads), lane, &row0);
   if (row0 >= r.m) return;
   const int shift = r.n - r.m;  // causal: row i sees keys j <= i + shift
-  auto blocks_of = [&](int i) {  // key blocks of tile i
-    const int first = row0 + i * kRows, last = min(first + kRows, r.m) - 1;
-    const int keys = first >= r.m ? 0 : a.causal ? min(r.n, last + shift + 1) : r.n;
-    return keys > 0 ? (keys + C::kKeys - 1) / C::kKeys : 0;
-  };
-  const int nb0 = blocks_of(0), nb1 = blocks_of(1), nmax = max(nb0, nb1);
+  const int keys = a.causal ? min(r.n, min(row0 + kRows, r.m) + shift) : r.n;
+  const int n = keys > 0 ? (keys + C::kKeys - 1) / C::kKeys : 0;  // key blocks
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // ring of K and V blocks
   uint64_t* empty = full + C::kStages;
   uint64_t* q_full = empty + C::kStages;
   // A barrier that may complete for block j + 1 before block j has been waited for exists once
   // per block parity.
-  uint64_t* s_full = q_full + 1;   // per tile and block parity: S is complete
-  uint64_t* s_read = s_full + 4;   // per tile: S is in registers (own P)
-  uint64_t* p_full = s_read + 2;   // per tile, and half (own P) or block parity: 64 keys of P
-  uint64_t* o_full = p_full + 4;   // per tile and block parity: the product with V is complete
-  uint64_t* turn = o_full + 4;     // per tile and warp: its exponentials of the block are done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
+  uint64_t* s_full = q_full + 1;   // per block parity: S is complete
+  uint64_t* s_read = s_full + 2;   // S is in registers (own P)
+  uint64_t* p_full = s_read + 1;   // per half (own P) or block parity: 64 keys of P are in place
+  uint64_t* o_full = p_full + 2;   // per block parity: the product with V is complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (2 * C::kStages + 23) + 8 <= 512, "barrier region");
+  static_assert(8 * (2 * C::kStages + 8) + 8 <= 256, "barrier region");
   const int kvh = head / (heads / a.kv_heads);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], nb0 > 0 && nb1 > 0 ? 2 : 1);  // an arrival from each working issuer
+      mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[2 * i], 1);
-      mbar_init(&s_full[2 * i + 1], 1);
-      mbar_init(&s_read[i], 4);
-      mbar_init(&p_full[2 * i], 4);
-      mbar_init(&p_full[2 * i + 1], 4);
-      mbar_init(&o_full[2 * i], 1);
-      mbar_init(&o_full[2 * i + 1], 1);
-      for (int w = 0; w < 4; ++w) mbar_init(&turn[4 * i + w], 1);
+    mbar_init(s_read, 4);
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&s_full[e], 1);
+      mbar_init(&p_full[e], 4);
+      mbar_init(&o_full[e], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
     // Q and the first K block are on their way before the other warps are set up
-    if (nmax > 0) {
-      mbar_expect_tx(q_full, 2 * C::kQBytes);
-      for (int i = 0; i < 2; ++i)
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(smem + i * C::kQBytes + c * C::kQChunk, &P.tq, q_full, c * 64, head, r.q0 + row0 + i * kRows);
+    if (n > 0) {
+      mbar_expect_tx(q_full, C::kQBytes);
+      for (int c = 0; c < HD / 64; ++c)
+        tma_load_3d(smem + c * C::kQChunk, &P.tq, q_full, c * 64, head, r.q0 + row0);
       mbar_expect_tx(&full[0], C::kKvBytes);
       for (int c = 0; c < HD / 64; ++c)
         tma_load_3d(smem + C::kOffKv + c * C::kKvChunk, &P.tk, &full[0], c * 64, kvh, r.k0);
     }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -176,18 +165,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
 
   // Ring positions of the K and V blocks, in the order of use: K_{j+1} before V_j.
   auto pos_k = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-  auto pos_v = [&](int j) { return j + 1 < nmax ? 2 * j + 2 : 2 * nmax - 1; };
+  auto pos_v = [&](int j) { return j + 1 < n ? 2 * j + 2 : 2 * n - 1; };
 
-  // Registers: 384 x 168 at launch; 128 x 56 + 256 x 224 is the same total.
+  // Registers: 256 x 128 at launch; 128 x 56 + 128 x 200 is the same total.
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && nmax > 0) {
+    if (lane == 0 && n > 0) {
       bool ok = true;
       int loads = 1, j[2] = {1, 0};  // the next K and V block; K_0 is under way
-      for (int t = 1; t < 2 * nmax; ++t) {
+      for (int t = 1; t < 2 * n; ++t) {
         const int s = t % C::kStages;
-        const bool is_v = j[1] < nmax && t == pos_v(j[1]);
+        const bool is_v = j[1] < n && t == pos_v(j[1]);
         if (!mbar_wait(&empty[s], static_cast<uint32_t>((t / C::kStages) & 1) ^ 1u, abort_flag)) {
           ok = false;
           break;
@@ -208,13 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       for (int t = loads > C::kStages ? loads - C::kStages : 0; t < loads; ++t)
         mbar_wait(&full[t % C::kStages], static_cast<uint32_t>((t / C::kStages) & 1), nullptr);
     }
-  } else if (warp < 3) {
-    // ------------------------------------------------------------ MMA issuers, one per tile
-    const int i = warp - 1, n = i == 0 ? nb0 : nb1;
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
     if (n > 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kKeys, false), idesc_o = idesc_bf16_f32(128, HD, true);
-      const uint32_t base = smem_u32(smem), qd = desc_lo(base + i * C::kQBytes, 16);
-      const uint32_t to = tmem + C::kO + i * HD;
+      const uint32_t base = smem_u32(smem), qd = desc_lo(base, 16);
+      const uint32_t to = tmem + C::kO;
       auto slot_of = [&](int t) { return t % C::kStages; };
       auto wait_bar = [&](uint64_t* bar, int phase) {
         const bool got = __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag));
@@ -226,16 +214,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       auto qk = [&](int j) {
         const int t = pos_k(j);
         if (!wait_bar(&full[slot_of(t)], t / C::kStages)) return false;
-        if (C::kOwnP && j > 0 && !wait_bar(&s_read[i], j - 1)) return false;
+        if (C::kOwnP && j > 0 && !wait_bar(s_read, j - 1)) return false;
         if (elect_one()) {
           const uint32_t kd = desc_lo(base + C::kOffKv + slot_of(t) * C::kKvBytes, 16);
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
             const uint32_t in = (k & 3) * 2, c = k >> 2;
-            umma_f16_lo(tmem + C::s_col(i, j), qd + c * (C::kQChunk >> 4) + in, kd + c * (C::kKvChunk >> 4) + in,
+            umma_f16_lo(tmem + C::s_col(j), qd + c * (C::kQChunk >> 4) + in, kd + c * (C::kKvChunk >> 4) + in,
                         kDescHi, idesc_s, k != 0);
           }
-          umma_commit(&s_full[2 * i + (j & 1)]);
+          umma_commit(&s_full[j & 1]);
           umma_commit(&empty[slot_of(t)]);
         }
         return true;
@@ -244,8 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         const int t = pos_v(j), s = slot_of(t), live = r.n - j * C::kKeys;
         if (!wait_bar(&full[s], t / C::kStages)) return false;
         if (live < C::kKeys) {
-          // Keys past the sequence have probability 0, and their V must not be NaN. Both
-          // issuers write these zeros; whichever is later writes over zeros.
+          // keys past the sequence have probability 0, and their V must not be NaN
           uint8_t* v = smem + C::kOffKv + s * C::kKvBytes;
           for (int e = live * 8 + lane; e < C::kKeys * 8; e += 32)
 #pragma unroll
@@ -257,32 +244,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         const uint32_t vd = desc_lo(base + C::kOffKv + s * C::kKvBytes, C::kKvChunk);
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
-          if (!(C::kOwnP ? wait_bar(&p_full[2 * i + h], j) : wait_bar(&p_full[2 * i + (j & 1)], j >> 1))) return false;
+          if (!(C::kOwnP ? wait_bar(&p_full[h], j) : wait_bar(&p_full[j & 1], j >> 1))) return false;
           if (elect_one()) {
 #pragma unroll
             for (int k = 4 * h; k < 4 * h + 4; ++k)
-              umma_f16_ts_lo(to, tmem + C::p_col(i, j) + k * 8, vd + 128u * k, kDescHi, idesc_o, (j | k) != 0);
+              umma_f16_ts_lo(to, tmem + C::p_col(j) + k * 8, vd + 128u * k, kDescHi, idesc_o, (j | k) != 0);
             if (h == C::kHalves - 1) {
-              umma_commit(&o_full[2 * i + (j & 1)]);
+              umma_commit(&o_full[j & 1]);
               umma_commit(&empty[s]);
             }
           }
         }
         return true;
       };
-      // what the tile does not use itself, it still has to free
-      auto skip = [&](int t) {
-        if (!wait_bar(&full[slot_of(t)], t / C::kStages)) return false;
-        if (elect_one()) mbar_arrive(&empty[slot_of(t)]);
-        return true;
-      };
       bool ok = wait_bar(q_full, 0) && qk(0);
-      for (int j = 0; j < nmax && ok; ++j) {
-        if (j + 1 < nmax) ok = j + 1 < n ? qk(j + 1) : skip(pos_k(j + 1));
-        ok = ok && (j < n ? pv(j) : skip(pos_v(j)));
-      }
+      for (int j = 0; j < n && ok; ++j) ok = (j + 1 >= n || qk(j + 1)) && pv(j);
       // never leave with products still running
-      ok = ok && wait_bar(&o_full[2 * i + ((n - 1) & 1)], (n - 1) >> 1);
+      ok = ok && wait_bar(&o_full[(n - 1) & 1], (n - 1) >> 1);
       if (!ok && lane == 0) {
         set_error(a.status_dev, MUON_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -290,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax, one thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int i = (warp - 4) / 4, w = warp & 3, nbi = i == 0 ? nb0 : nb1;
-    const int row = row0 + i * kRows + w * 32 + lane;  // within the sequence
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int w = warp & 3;
+    const int row = row0 + w * 32 + lane;  // within the sequence
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-    const uint32_t to = tmem + lanes + C::kO + i * HD;
+    const uint32_t to = tmem + lanes + C::kO;
     constexpr int kParts = C::kKeys / 32;
     const float sl = a.scale * 1.4426950408889634f;
     float top = -INFINITY;            // largest logit so far, unscaled
@@ -302,24 +280,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     float sum = 0.f;
     bool ok = true;
     auto wait_o = [&](int j) {  // the product of block j is complete
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&o_full[2 * i + (j & 1)], static_cast<uint32_t>((j >> 1) & 1), abort_flag));
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&o_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), abort_flag));
       tc_fence_after();
       return got;
     };
-    for (int j = 0; j < nbi; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[2 * i + (j & 1)], static_cast<uint32_t>((j >> 1) & 1), abort_flag))) {
+    for (int j = 0; j < n; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), abort_flag))) {
         ok = false;
         break;
       }
       tc_fence_after();
       uint32_t s[kParts][32];
 #pragma unroll
-      for (int c = 0; c < kParts; ++c) tmem_ld32(tmem + lanes + C::s_col(i, j) + c * 32, s[c]);
+      for (int c = 0; c < kParts; ++c) tmem_ld32(tmem + lanes + C::s_col(j) + c * 32, s[c]);
       tmem_wait_ld();
       if (C::kOwnP) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_read[i]);
+        if (lane == 0) mbar_arrive(s_read);
       }
       // keys of this block that the row sees
       const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * C::kKeys;
@@ -367,12 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           }
         }
       }
-      // Two warps, one of each tile, share a scheduler and its exponential unit: they take
-      // turns, so that one's maximum and transfers overlap the other's exponentials.
-      if (C::kOwnP && (i == 0 ? j > 0 && j <= nb1 : j < nb0)) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&turn[4 * (1 - i) + w], static_cast<uint32_t>((i == 0 ? j - 1 : j) & 1), abort_flag));
-        if (!ok) break;
-      }
       float add[4] = {sum, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int h = 0; h < C::kHalves; ++h) {
@@ -386,15 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
           add[2 * (e & 1) + 1] += p1;
           pk[e] = round_bf16x2(p0, p1);
         }
-        if (C::kOwnP && h == C::kHalves - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&turn[4 * i + w]);
-        }
-        tmem_st32(tmem + lanes + C::p_col(i, j) + h * 32, pk);
+        tmem_st32(tmem + lanes + C::p_col(j) + h * 32, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * i + (C::kOwnP ? h : j & 1)]);
+        if (lane == 0) mbar_arrive(&p_full[C::kOwnP ? h : j & 1]);
       }
       sum = (add[0] + add[1]) + (add[2] + add[3]);
     }
@@ -402,20 +370,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
       set_error(a.status_dev, MUON_ERR_TIMEOUT);
       *abort_flag = 1;
     }
-    if (nbi > 0 && ok) {
-      ok = wait_o(nbi - 1);
-      if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
-    }
-    if (nbi == 0 && nmax > 0) {  // no copy may land over the staged zeros
-      ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, abort_flag));
+    if (n > 0 && ok) {
+      ok = wait_o(n - 1);
       if (!ok && lane == 0) set_error(a.status_dev, MUON_ERR_TIMEOUT);
     }
     const bool live = row < r.m, seen = top > -INFINITY || sum != 0.f;
     const float inv = seen ? 1.f / sum : 0.f;  // 0: the row is written as zeros
     // staged where Q was: its products are complete
-    store_rows<HD>(to, smem + i * C::kQBytes, w, lane, 0, inv, nbi == 0,
-                   static_cast<uint16_t*>(a.o.ptr) + static_cast<int64_t>(r.q0 + row0 + i * kRows + w * 32) * a.o.ld + head * a.o.head,
-                   a.o.ld, ok ? r.m - row0 - i * kRows - w * 32 : 0, a.head_dim);
+    store_rows<HD>(to, smem, w, lane, 0, inv, n == 0,
+                   static_cast<uint16_t*>(a.o.ptr) + static_cast<int64_t>(r.q0 + row0 + w * 32) * a.o.ld + head * a.o.head,
+                   a.o.ld, ok ? r.m - row0 - w * 32 : 0, a.head_dim);
     if (live && ok)
       a.lse[static_cast<int64_t>(head) * a.q_tokens + r.q0 + row] =
           seen ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -431,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -441,8 +405,11 @@ cudaError_t launch(const FwdParams& P, int dev, int64_t grid, cudaStream_t st) {
   static std::atomic<uint64_t> attr_devices{0};
   const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
   if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(attention_fwd_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               FwdCfg<HD>::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(attention_fwd_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         FwdCfg<HD>::kSmemBytes);
+    if (e == cudaSuccess)  // all of the SM's memory, so that two blocks fit
+      e = cudaFuncSetAttribute(attention_fwd_kernel<HD>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_devices.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -461,7 +428,7 @@ cudaError_t launch_attention_forward(const muon_attention_t& a, int dev, cudaStr
       !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, keys) ||
       !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, keys))
     return cudaErrorInvalidValue;
-  const int64_t grid = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, 2 * kRows) * a.heads;
+  const int64_t grid = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, kRows) * a.heads;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
   return a.head_dim <= 64 ? launch<64>(P, dev, grid, st) : launch<128>(P, dev, grid, st);
 }
