@@ -1,23 +1,26 @@
 // Forward pass of softmax attention over packed sequences, with the log-sum-exp of every row
 // and the largest logit of every head (muon_attention_forward).
 //
-// One pass over the keys with a running maximum and sum per row. A CTA owns 256 query rows of
-// one head as two tiles of 128, whose softmax and products alternate on the tensor core:
-//   S_i = Q_i K^T (fp32 in tensor memory), P = exp2(S scale log2 e - m) as bf16 in tensor memory,
-//   O_i += P V with P as the tensor-memory operand
-// Warps: 0 TMA producer (Q once, then K and V blocks through a ring), 1 and 2 MMA issuers, one per
-// tile (a single issuer spent all its time issuing and waiting), 4-7 and 8-11 the softmax of
-// tile 0 and 1, one thread per row. The next block's S is computed while this block's softmax
+// One pass over the keys with a running maximum and sum per row. A block owns 128 query rows of
+// one head:
+//   S = Q K^T (fp32 in tensor memory), P = exp2(S scale log2 e - m) as bf16 in tensor memory,
+//   O += P V with P as the tensor-memory operand
+// Warps: 0 TMA producer (Q once, then K and V blocks through a ring), 1 MMA issuer, 4-7 the
+// softmax, one thread per row. Two blocks share an SM (256 columns of tensor memory and half of
+// the shared memory each): one's softmax, start and end overlap the other's products. (Two tiles
+// in one block of 256 rows, taking turns, needed 10 to 20 % longer for head dimension 128 and
+// short sequences, 5 % less for 64.) The next key block's S is computed while this one's softmax
 // runs; how tensor memory allows that differs by head dimension (FwdCfg).
 // m is the row's running maximum, moved only when a block exceeds it by more than 2^8 in the
 // exponent: until then P stays below 2^8 and nothing overflows (fp32 sums, bf16 P), and the
 // accumulator, which a thread would have to read and write back, is left alone. P is rounded
 // to bf16 for the product (at most 2^-8 relative, errors of either sign); the row's sum adds the
 // unrounded values.
-// Bounds: head dimension 64 by the exponentials, 16 per cycle and SM (2048 cycles for 128 keys of
-// both tiles, 2900 measured: a warp's FMAs, sums and conversions do not all hide behind them);
-// head dimension 128 by the products (2048 cycles at the full rate; S with both operands in
-// shared memory and 64 columns runs at half of it, 3700 measured).
+// Bounds, per 128 keys of both blocks: head dimension 128 by the products, 2048 cycles at the full
+// rate (S, with both operands in shared memory and 64 columns, runs at half of it; 3400 measured,
+// 1089 TFLOP/s at 8191 tokens, 12 heads); head dimension 64 by the exponentials, 16 per cycle and
+// SM, 2048 cycles (3100 measured: the sums, maxima and transfers of two softmax warps to a
+// scheduler do not all hide behind them; moving exponentials to the FMA pipe made it slower).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
