@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_fwd_kernel(const __grid
         for (int c = 0; c < kParts; ++c)
           m[2 * (c & 1) + (e / 2 & 1)] = max3(m[2 * (c & 1) + (e / 2 & 1)], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
       top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-      const float want = top == -INFINITY ? 0.f : top * sl;
+      // (a row whose logits so far are all -inf: below any that follow, yet finite)
+      const float want = top == -INFINITY ? -3e38f : top * sl;
       if (j == 0) {
         ref = want;
       } else {

@@ -476,6 +476,25 @@ def test_attention_s_max_is_raised_only(B):
     ref.check(neg, want["s_max"], torch.tensor(tol["s_max"]), "negative s_max")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_keys_masked_by_infinite_entries(B, d):
+    """Keys whose entries make every logit -inf (with queries of one sign) count for nothing, also
+    where they fill the first blocks and what follows has low logits; a row that sees no other key
+    has o = 0 and lse = -inf."""
+    q, k, v, _ = inputs(14, [300], [300], 2, 1, d)
+    q.copy_(q.abs())
+    k.copy_(-40 * k.abs())
+    k[:200] = -math.inf
+    s_max = torch.full((2,), -math.inf, device="cuda")
+    o, lse = B.attention_forward(q, k, v, s_max=s_max)
+    assert bool((o[:200] == 0).all()) and bool((lse[:, :200] == -math.inf).all())
+    want, tol = ref.attention(q[200:], k[200:], v[200:], [100], [100], True, d ** -0.5)
+    assert float(want["s_max"].max()) < -100
+    ref.check(o[200:], want["o"], tol["o"], "o")
+    ref.check(lse[:, 200:], want["lse"], tol["lse"], "lse")
+    ref.check(s_max, want["s_max"], torch.as_tensor(tol["s_max"]), "s_max")
+
+
 def test_attention_gradients_against_differences(B):
     """A directional difference of sum(o * dout) in float64 against the kernel's gradients."""
     lens = [70, 33]
