@@ -685,9 +685,9 @@ muon_status_t validate_weight_grad(const muon_weight_grad_t* p) {
   const muon_weight_grad_t& a = *p;
   if (a.w_dtype != MUON_F32 && a.w_dtype != MUON_BF16) return MUON_ERR_DTYPE;
   const int64_t lim = int64_t(1) << 31;
-  // (a token count stays countable in k-blocks with 32 bits)
-  if (a.tokens < 0 || a.out < 1 || a.in < 1 || a.groups < 1 || a.tokens > lim - 64 || a.out >= lim ||
-      a.in >= lim || a.groups > 65535 || a.out * a.in >= lim)
+  // (tokens up to the end of a k-block, rows and columns up to the end of a tile stay below 2^31)
+  if (a.tokens < 0 || a.out < 1 || a.in < 1 || a.groups < 1 || a.tokens > lim - kTok || a.out > lim - 512 ||
+      a.in > lim - 512 || a.groups > 65535 || a.out * a.in >= lim)
     return MUON_ERR_SHAPE;
   if (a.ld_dy < a.out || a.ld_q < a.in || a.ld_e < (a.in + 31) / 32 || a.ld_w < a.in ||
       a.ld_dy >= lim || a.ld_q >= lim || a.ld_e >= lim || a.ld_w >= lim ||
