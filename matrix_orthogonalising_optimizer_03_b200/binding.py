@@ -584,7 +584,7 @@ def weight_grad(dy, ck: Act8, dw, offsets=None, accumulate: bool = False, worksp
     """One weight gradient (see `WeightGradPlan`). Returns the workspace used (or None)."""
     with _on_stream(stream):
         plan = WeightGradPlan(dy, ck, dw, offsets, accumulate, workspace, status)
-        plan.apply()
+        plan.apply(stream)
     return plan.workspace
 
 
@@ -685,7 +685,7 @@ def attention_forward(q, k, v, o=None, lse=None, q_offsets=None, k_offsets=None,
         if lse is None:
             lse = torch.full((q.size(1), q.size(0)), float("-inf"), dtype=torch.float32, device=q.device)
         AttentionPlan(q, k, v, o, lse, q_offsets, k_offsets, causal, scale, s_max,
-                      status=status).forward()
+                      status=status).forward(stream)
     return o, lse
 
 
@@ -699,7 +699,7 @@ def attention_backward(dout, q, k, v, o, lse, dq=None, dk=None, dv=None, q_offse
         dq, dk, dv = (torch.zeros_like(t, memory_format=torch.contiguous_format) if g is None else g
                       for g, t in ((dq, q), (dk, k), (dv, v)))
         AttentionPlan(q, k, v, o, lse, q_offsets, k_offsets, causal, scale, grads=(dout, dq, dk, dv),
-                      workspace=workspace, status=status).backward()
+                      workspace=workspace, status=status).backward(stream)
     return dq, dk, dv
 
 

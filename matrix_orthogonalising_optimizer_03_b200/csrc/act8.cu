@@ -16,7 +16,10 @@
 // restore 48 us (5.8 TB/s).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "act8.cuh"
 #include "muon.h"
@@ -301,22 +304,33 @@ muon_status_t validate_act8(const muon_act8_t* items, int n, bool store) {
         reinterpret_cast<uintptr_t>(a.q) % 16 || reinterpret_cast<uintptr_t>(a.exps) % 16)
       return MUON_ERR_INVALID_ARG;
   }
+  // Nothing written (store: q and exps, restore: X) overlaps anything else: in the order of their
+  // starts, nothing begins before the end of what is written before it, and nothing written
+  // before the end of anything.
+  struct Range {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  Range few[3 * kFewItems];
+  std::unique_ptr<Range[]> many(n > kFewItems ? new (std::nothrow) Range[3 * static_cast<size_t>(n)] : nullptr);
+  Range* const r = n > kFewItems ? many.get() : few;
+  if (r == nullptr) return MUON_ERR_CUDA;  // out of host memory
+  size_t count = 0;
   for (int i = 0; i < n; ++i) {
     const muon_act8_t& a = items[i];
-    for (int j = 0; j < n; ++j) {
-      const muon_act8_t& b = items[j];
-      const void* bp[3] = {b.X, b.q, b.exps};
-      const size_t bs[3] = {span_x(b), span_q(b), span_e(b)};
-      for (int k = 0; k < 3; ++k) {
-        // store writes q and exps, restore writes X; a buffer does not overlap itself
-        if (store) {
-          if (!(i == j && k == 1) && ranges_overlap(a.q, span_q(a), bp[k], bs[k])) return MUON_ERR_ALIAS;
-          if (!(i == j && k == 2) && ranges_overlap(a.exps, span_e(a), bp[k], bs[k])) return MUON_ERR_ALIAS;
-        } else if (!(i == j && k == 0) && ranges_overlap(a.X, span_x(a), bp[k], bs[k])) {
-          return MUON_ERR_ALIAS;
-        }
-      }
-    }
+    if (a.rows == 0) continue;
+    const auto x = reinterpret_cast<uintptr_t>(a.X), q = reinterpret_cast<uintptr_t>(a.q),
+               e = reinterpret_cast<uintptr_t>(a.exps);
+    r[count++] = {x, x + span_x(a), !store};
+    r[count++] = {q, q + span_q(a), store};
+    r[count++] = {e, e + span_e(a), store};
+  }
+  std::sort(r, r + count, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t end = 0, end_written = 0;
+  for (size_t i = 0; i < count; ++i) {
+    if (r[i].lo < (r[i].written ? end : end_written)) return MUON_ERR_ALIAS;
+    end = std::max(end, r[i].hi);
+    if (r[i].written) end_written = std::max(end_written, r[i].hi);
   }
   return MUON_OK;
 }

@@ -45,6 +45,24 @@ def test_act8_aliases_between_items(lib):
     assert lib.muon_act8_restore(shared, 2, None) == 4
 
 
+def test_act8_read_buffers_may_be_shared(lib):
+    """Shared activations of a store and shared checkpoints of a restore pass; whatever is written
+    may not lie inside anything else, wherever it stands in a long list."""
+    far = FAKE + 100 * GB
+
+    def items(n, **last):
+        return (B.MuonAct8 * n)(*(act8(X=FAKE, q=far + 2 * i * GB, exps=far + (2 * i + 1) * GB) for i in range(n - 1)),
+                                act8(**last))
+    for n in (3, 40):
+        good = items(n)
+        assert lib.muon_act8_store(good, n, None) not in (1, 2, 3, 4)
+        assert lib.muon_act8_restore(good, n, None) == 4            # one X written n times
+        inside = items(n, q=far + 64)                                # inside the first item's q
+        assert lib.muon_act8_store(inside, n, None) == 4
+        inside = items(n, X=far - 16, ld_x=1 << 20)                  # an X around other buffers
+        assert lib.muon_act8_store(inside, n, None) == 4
+
+
 def wgrad(**kw):
     a = dict(dY=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, dW=FAKE + 3 * GB, offsets=FAKE + 4 * GB, status_dev=None,
              tokens=100, out=50, in_=70, ld_dy=56, ld_q=80, ld_e=16, ld_w=70, stride_w=3500, groups=3, w_dtype=1,
@@ -61,7 +79,9 @@ def wgrad(**kw):
     (dict(exps=FAKE + 2 * GB + 4), 1), (dict(dW=FAKE + 3 * GB + 1), 1), (dict(offsets=FAKE + 4 * GB + 2), 1),
     (dict(status_dev=FAKE + 2), 1), (dict(dW=FAKE + 64), 4), (dict(dW=FAKE + GB + 64), 4),
     (dict(dW=FAKE + 2 * GB + 64), 4), (dict(dW=FAKE + 4 * GB), 4), (dict(status_dev=FAKE + 3 * GB + 400), 4),
-    (dict(tokens=1 << 31), 2), (dict(tokens=(1 << 31) - 63), 2), (dict(out=1 << 20, in_=1 << 20, ld_w=1 << 20, ld_dy=1 << 20, ld_q=1 << 20,
+    (dict(tokens=1 << 31), 2), (dict(tokens=(1 << 31) - 63), 2),
+    (dict(out=1, in_=(1 << 31) - 500, ld_w=(1 << 31) - 1, ld_q=(1 << 31) - 16, ld_e=1 << 27, groups=1), 2),
+    (dict(in_=1, out=(1 << 31) - 500, ld_dy=(1 << 31) - 8, groups=1), 2), (dict(out=1 << 20, in_=1 << 20, ld_w=1 << 20, ld_dy=1 << 20, ld_q=1 << 20,
                                      ld_e=1 << 20, groups=1), 2)])
 def test_weight_grad_refusals(lib, kw, status):
     assert lib.muon_weight_grad(ctypes.byref(wgrad(**kw)), None, 0, None) == status
