@@ -7,16 +7,20 @@
 // calls give equal bits: one per 128 query rows for dQ (and delta), one per 128 keys for dK
 // and dV, over all query heads of the key head. S and dout V^T are computed in both: seven
 // products instead of five, against fp32 atomics on dQ, whose order changes its sums.
-// In both, 16 warps own a 128 x 128 block in tensor memory, a thread 32 elements of one lane's
-// row. P and dS are rounded to bf16 (at most 2^-8 relative, errors of either sign) and written
-// back over the scores they came from, where the next product takes them as its tensor-memory
-// operand; the transposes that dV and dK need cost nothing, because the second kernel computes
-// S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
-// Per block of head dimension 128 the products take 1536 cycles (dQ) and 2048 (dK, dV) at the
-// full rate; measured 2100 and 3000, the tensor core active 64 and 68 % of the time. An M = 128
-// product whose operands both come from shared memory runs at 0.84 of the rate for N = 128, as
-// it reads 8 KB per 64 cycles; the rest is the chain product - exponential - product of a block.
-// Short sequences are bound by a block's start and end, about 8000 cycles.
+// A thread owns 32 elements of one lane's row. P and dS are rounded to bf16 (at most 2^-8 relative,
+// errors of either sign) and written back over the scores they came from, where the next product
+// takes them as its tensor-memory operand; the transposes that dV and dK need cost nothing, because
+// the second kernel computes S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
+// Head dimension 128: 128 x 128 scores at a time, 16 warps, one block on an SM. Per 128 x 128
+// scores the products take 1536 cycles (dQ) and 2048 (dK, dV) at the full rate; measured 2100 and
+// 3000, the tensor core active 64 and 68 % of the time. An M = 128 product whose operands both come
+// from shared memory runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles; the
+// rest is the chain product - exponential - product of a block.
+// Head dimension 64: 128 x 64 scores at a time, 8 warps, two blocks on an SM, whose chains, starts
+// and ends (about 8000 cycles of a block) overlap. With 128 x 128 scores and one block, sequences
+// of 1 to 2311 tokens, 12 heads, took 139 us instead of 109. The exponentials alone, taken in both
+// kernels, are 1024 cycles per 128 x 128 scores of each, the products 1280 and 1536 (S and dP at
+// half of the rate with 64 columns).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -33,27 +37,33 @@
 namespace muon {
 namespace {
 
-constexpr int kRows = 128;            // rows and keys of a block
-constexpr int kChunk = kRows * 128;   // bytes of 64 columns of a tile
-constexpr int kCompute = 16;          // warps that compute, four to a scheduler
-constexpr int kThreads = 32 * (4 + kCompute);  // and 4 that move and issue
+constexpr int kRows = 128;            // rows of a dQ tile, keys of a tile of dK and dV
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int HD>
 struct BwdCfg {
+  // Keys (dQ) or rows (dK, dV) of a block: with 64 of them, head dimension 64 needs half of the
+  // tensor memory and of the shared memory, and two thread blocks share an SM.
+  static constexpr int kCols = HD;
+  static constexpr int kParts = kCols / 32;                // 32 columns a thread
+  static constexpr int kCompute = 4 * kParts;              // warps that compute
+  static constexpr int kThreads = 32 * (4 + kCompute);     // and 4 that move and issue
+  // Thread blocks on an SM. Two of 384 threads have 80 registers a thread at launch, of which the
+  // four warps that move and issue leave some to the others: 128 x 64 + 256 x 88 is the same total.
+  static constexpr int kPerSm = HD == 64 ? 2 : 1;
+  static constexpr uint32_t kTmem = 512 / kPerSm;
   static constexpr int kTile = kRows * HD * 2;
+  static constexpr int kBlock = kCols * HD * 2;
   static constexpr int kRing3 = 3, kRing2 = 2;  // the operand of two chains, and of one
   static constexpr int kOffRing3 = 2 * kTile;
-  static constexpr int kOffRing2 = kOffRing3 + kRing3 * kTile;
-  static constexpr int kOffVec = kOffRing2 + kRing2 * kTile;  // lse and delta of a block of rows
-  static constexpr int kVecBytes = 2 * kRows * 4;
-  // Head dimension 64 leaves tensor memory for a second S in the kernel of dK and dV, so that the
-  // next block's scores are computed during this block's softmax; it then needs lse and delta of
-  // three blocks.
-  static constexpr bool kTwoS = HD == 64;
-  static constexpr int kVecs = kTwoS ? 3 : 2;
-  static constexpr int kOffBar = kOffVec + kVecs * kVecBytes;
+  static constexpr int kOffRing2 = kOffRing3 + kRing3 * kBlock;
+  static constexpr int kOffVec = kOffRing2 + kRing2 * kBlock;  // lse and delta of a block of rows
+  static constexpr int kVecBytes = 2 * kCols * 4;
+  static constexpr int kOffBar = kOffVec + 2 * kVecBytes;
   static constexpr int kSmemBytes = kOffBar + 512;
+  static_assert(kParts * kRows * 4 <= 2 * kVecBytes, "exchange of the parts of delta");
+  static_assert(2 * kRows * HD * 4 <= kOffVec, "sums shared by a cluster");
+  static_assert(kPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 struct BwdParams {
@@ -68,51 +78,64 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, int phase, volatile int*
   return got;
 }
 
-template <int HD>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
-  mbar_expect_tx(bar, BwdCfg<HD>::kTile);
+// Loads kR rows of one head by boxes of kCols rows.
+template <int HD, int kR>
+__device__ __forceinline__ void load_boxes(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
+  constexpr int kCols = BwdCfg<HD>::kCols;
 #pragma unroll
-  for (int c = 0; c < HD / 64; ++c) tma_load_3d(dst + c * kChunk, map, bar, c * 64, head, token);
+  for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+    for (int b = 0; b < kR; b += kCols) tma_load_3d(dst + (c * kR + b) * 128, map, bar, c * 64, head, token + b);
 }
 
-// Zeros the rows from `live` on of a tile in shared memory (one warp): another sequence's rows
+template <int HD>
+__device__ __forceinline__ void load_block(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
+  mbar_expect_tx(bar, BwdCfg<HD>::kBlock);
+  load_boxes<HD, BwdCfg<HD>::kCols>(dst, map, bar, head, token);
+}
+
+// Zeros the rows from `live` on of a block in shared memory (one warp): another sequence's rows
 // that a product would sum over, with factors of zero but perhaps NaN themselves.
 template <int HD>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int live, int lane) {
-  for (int e = live * 8 + lane; e < kRows * 8; e += 32)
+__device__ __forceinline__ void clear_rows(uint8_t* block, int live, int lane) {
+  constexpr int kCols = BwdCfg<HD>::kCols;
+  for (int e = live * 8 + lane; e < kCols * 8; e += 32)
 #pragma unroll
-    for (int c = 0; c < HD / 64; ++c) *reinterpret_cast<uint4*>(tile + c * kChunk + e * 16) = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < HD / 64; ++c)
+      *reinterpret_cast<uint4*>(block + c * (kCols * 128) + e * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
 }
 
-// D (+)= A B^T over the head dimension: both operands K-major tiles in shared memory.
+// D = A B^T over the head dimension: a tile and a block in shared memory, both K-major.
 template <int HD>
 __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false);
+  constexpr int kCols = BwdCfg<HD>::kCols;
+  constexpr uint32_t idesc = idesc_bf16_f32(128, kCols, false);
   const uint32_t ad = desc_lo(a_addr, 16), bd = desc_lo(b_addr, 16);
 #pragma unroll
   for (int k = 0; k < HD / 16; ++k) {
-    const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
-    umma_f16_lo(d, ad + off, bd + off, kDescHi, idesc, k != 0);
+    const uint32_t c = k >> 2, in = (k & 3) * 2;
+    umma_f16_lo(d, ad + c * (kRows * 8) + in, bd + c * (kCols * 8) + in, kDescHi, idesc, k != 0);
   }
 }
 
-// D (+)= A B over the 128 rows or keys of a block: A bf16 in tensor memory (each 32 of them in
-// the first 16 of the 32 columns they came from), B an MN-major tile in shared memory.
+// D (+)= A B over the rows or keys of a block: A bf16 in tensor memory (each 32 of them in the
+// first 16 of the 32 columns they came from), B an MN-major block in shared memory.
 template <int HD>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate) {
+  constexpr int kCols = BwdCfg<HD>::kCols;
   constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
-  const uint32_t bd = desc_lo(b_addr, kChunk);
+  const uint32_t bd = desc_lo(b_addr, kCols * 128);
 #pragma unroll
-  for (int k = 0; k < kRows / 16; ++k)
+  for (int k = 0; k < kCols / 16; ++k)
     umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
 }
 
 // ------------------------------------------------------------------ dQ and delta
 // Chain A: S_j = Q K_j^T (two buffers), dQ += dS_j K_j.  Chain B: dP_j = dout V_j^T.
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_constant__ BwdParams P) {
+__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) attention_dq_kernel(const __grid_constant__ BwdParams P) {
   using C = BwdCfg<HD>;
   const muon_attention_t& a = P.a;
   const int heads = a.heads, head = static_cast<int>(blockIdx.x % heads);
@@ -123,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   if (row0 >= r.m) return;
   const int shift = r.n - r.m;  // causal: row i sees keys j <= i + shift
   const int keys = a.causal ? min(r.n, min(row0 + kRows, r.m) + shift) : r.n;
-  const int n = keys > 0 ? (keys + kRows - 1) / kRows : 0;  // key blocks
+  const int n = keys > 0 ? (keys + C::kCols - 1) / C::kCols : 0;  // key blocks
 
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -152,36 +175,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&ds_full[s], kCompute);
+      mbar_init(&ds_full[s], C::kCompute);
     }
     for (int e = 0; e < 8; ++e) mbar_init(&turn[e], 2);
     mbar_init(dp_full, 1);
-    mbar_init(dp_read, kCompute);
+    mbar_init(dp_read, C::kCompute);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
     // the first blocks are on their way before the other warps are set up
     mbar_expect_tx(q_full, 2 * C::kTile);
-    for (int c = 0; c < HD / 64; ++c) {
-      tma_load_3d(sq + c * kChunk, &P.tq, q_full, c * 64, head, r.q0 + row0);
-      tma_load_3d(sdo + c * kChunk, &P.tdo, q_full, c * 64, head, r.q0 + row0);
-    }
+    load_boxes<HD, kRows>(sq, &P.tq, q_full, head, r.q0 + row0);
+    load_boxes<HD, kRows>(sdo, &P.tdo, q_full, head, r.q0 + row0);
     if (n > 0) {
-      load_tile<HD>(sk, &P.tk, &k_full[0], kvh, r.k0);
-      load_tile<HD>(sv, &P.tv, &v_full[0], kvh, r.k0);
+      load_block<HD>(sk, &P.tk, &k_full[0], kvh, r.k0);
+      load_block<HD>(sv, &P.tv, &v_full[0], kvh, r.k0);
     }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  constexpr uint32_t kDp = 256, kDq = 384;  // columns of dP and dQ; S at 128 (j & 1)
+  constexpr uint32_t kDp = 2 * C::kCols, kDq = 3 * C::kCols;  // columns of dP and dQ; S at kCols (j & 1)
   bool ok = true;
+  if (C::kPerSm == 2 && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");  // see kPerSm
 
   if (warp == 0) {
     if (lane == 0) {
@@ -189,11 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&k_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_tile<HD>(sk + j % 3 * C::kTile, &P.tk, &k_full[j % 3], kvh, r.k0 + j * kRows);
+        load_block<HD>(sk + j % 3 * C::kBlock, &P.tk, &k_full[j % 3], kvh, r.k0 + j * C::kCols);
         ++kl;
         ok = mbar_wait(&v_empty[j & 1], static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_tile<HD>(sv + (j & 1) * C::kTile, &P.tv, &v_full[j & 1], kvh, r.k0 + j * kRows);
+        load_block<HD>(sv + (j & 1) * C::kBlock, &P.tv, &v_full[j & 1], kvh, r.k0 + j * C::kCols);
         ++vl;
       }
       // never leave with bulk copies still landing in shared memory
@@ -205,10 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
     if (n > 0) {
       auto score = [&](int j) {  // S_j; the buffer's dS_{j-2} went into a product issued before
         if (!wait_all(&k_full[j % 3], j / 3, abort_flag)) return false;
-        const int live = r.n - j * kRows;
-        if (live < kRows) clear_rows<HD>(sk + j % 3 * C::kTile, live, lane);
+        const int live = r.n - j * C::kCols;
+        if (live < C::kCols) clear_rows<HD>(sk + j % 3 * C::kBlock, live, lane);
         if (elect_one()) {
-          product_ss<HD>(tmem + (j & 1) * 128, smem_u32(sq), smem_u32(sk) + j % 3 * C::kTile);
+          product_ss<HD>(tmem + (j & 1) * C::kCols, smem_u32(sq), smem_u32(sk) + j % 3 * C::kBlock);
           umma_commit(&s_full[j & 1]);
         }
         return true;
@@ -218,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
         ok = wait_all(&ds_full[j & 1], j >> 1, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDq, tmem + (j & 1) * 128, smem_u32(sk) + j % 3 * C::kTile, j > 0);
+          product_ts<HD>(tmem + kDq, tmem + (j & 1) * C::kCols, smem_u32(sk) + j % 3 * C::kBlock, j > 0);
           umma_commit(&k_empty[j % 3]);
           if (j + 1 == n) umma_commit(done);
         }
@@ -232,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       for (int j = 0; j < n && ok; ++j) {
         ok = wait_all(&v_full[j & 1], j >> 1, abort_flag) && (j == 0 || wait_all(dp_read, j - 1, abort_flag));
         if (ok && elect_one()) {
-          product_ss<HD>(tmem + kDp, smem_u32(sdo), smem_u32(sv) + (j & 1) * C::kTile);
+          product_ss<HD>(tmem + kDp, smem_u32(sdo), smem_u32(sv) + (j & 1) * C::kBlock);
           umma_commit(dp_full);
           umma_commit(&v_empty[j & 1]);
         }
@@ -240,17 +262,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
       ok = ok && wait_all(dp_full, n - 1, abort_flag);
     }
   } else if (warp >= 4) {
-    const int w = warp & 3, part = (warp - 4) >> 2;     // lane quarter, and quarter of a block's keys
+    if (C::kPerSm == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    const int w = warp & 3, part = (warp - 4) >> 2;     // lane quarter, and 32 of a block's keys
     const int row = row0 + w * 32 + lane;               // within the sequence
     const bool live = row < r.m;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const int64_t token = r.q0 + row, vec = static_cast<int64_t>(head) * a.q_tokens + token;
-    // delta = o . dout: the four threads of a row sum a quarter of the columns each, dout from
-    // its tile in shared memory
+    // delta = o . dout: the threads of a row sum 32 of the columns each, dout from its tile in
+    // shared memory
     float lse = INFINITY;  // of rows without keys, or none: P = 0
     float sum[4] = {};
     {
-      constexpr int kUnits = HD / 32;
+      constexpr int kUnits = 4;
       uint4 o[kUnits];
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.ptr) + token * a.o.ld + head * a.o.head);
 #pragma unroll
@@ -265,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
 #pragma unroll
       for (int c = 0; c < kUnits; ++c) {
         const int u = part * kUnits + c;
-        const uint4 g = *reinterpret_cast<const uint4*>(sdo + (u >> 3) * kChunk + rt * 128 + (((u & 7) ^ (rt & 7)) << 4));
+        const uint4 g = *reinterpret_cast<const uint4*>(sdo + (u >> 3) * (kRows * 128) + rt * 128 + (((u & 7) ^ (rt & 7)) << 4));
         const uint32_t xs[4] = {o[c].x, o[c].y, o[c].z, o[c].w}, ys[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -276,29 +299,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
     }
     float* exchange = reinterpret_cast<float*>(smem + C::kOffVec) + w * 32 + lane;
     exchange[part * kRows] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    named_barrier(1, 32 * kCompute);
-    const float delta = (exchange[0] + exchange[kRows]) + (exchange[2 * kRows] + exchange[3 * kRows]);
+    named_barrier(1, 32 * C::kCompute);
+    float delta = exchange[0] + exchange[kRows];
+    if (C::kParts > 2) delta += exchange[2 * kRows] + exchange[3 * kRows];
     if (live && part == 0) P.delta[vec] = delta;
     const float sl = a.scale * kLog2e;
     for (int j = 0; j < n && ok; ++j) {
       ok = wait_all(&s_full[j & 1], j >> 1, abort_flag);
       if (!ok) break;
-      const uint32_t ts = tmem + lanes + (j & 1) * 128 + part * 32;
+      const uint32_t ts = tmem + lanes + (j & 1) * C::kCols + part * 32;
       uint32_t s[32], p[32];
       tmem_ld32(ts, s);
       tmem_wait_ld();
-      // keys of this quarter of the block that the row sees
-      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * kRows - part * 32;
+      // keys of this part of the block that the row sees
+      const int vis = min(r.n, a.causal ? row + shift + 1 : r.n) - j * C::kCols - part * 32;
       const bool masked = __any_sync(0xffffffffu, vis < 32);
-      // Of the four warps of a scheduler two take turns with the other two at the exponentials:
-      // one pair's other work overlaps the other's.
+      // With one block on the SM, two of the four warps of a scheduler take turns with the other two
+      // at the exponentials: one pair's other work overlaps the other's. (Two blocks overlap by
+      // themselves: 408 us with turns, 398 without, 8192 tokens, 12 heads of 64, causal.)
       const int grp = part >> 1;
-      if (grp == 1 || j > 0) ok = wait_all(&turn[4 * (1 - grp) + w], grp == 1 ? j : j - 1, abort_flag);
+      if (C::kPerSm == 1 && (grp == 1 || j > 0)) ok = wait_all(&turn[4 * (1 - grp) + w], grp == 1 ? j : j - 1, abort_flag);
       if (!ok) break;
 #pragma unroll
       for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e]), sl, -lse)));
       __syncwarp();
-      if (lane == 0) mbar_arrive(&turn[4 * grp + w]);
+      if (C::kPerSm == 1 && lane == 0) mbar_arrive(&turn[4 * grp + w]);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tmem + lanes + kDp + part * 32, p);
@@ -324,10 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
     // staged where Q was: its products are complete
-    if (part < HD / 32)
-      store_rows<32>(tmem + lanes + kDq + part * 32, sq, w, lane, part * 32, a.scale, n == 0,
-                     static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + part * 32, a.dq.ld,
-                     ok ? r.m - row0 - w * 32 : 0, a.head_dim);
+    store_rows<32>(tmem + lanes + kDq + part * 32, sq, w, lane, part * 32, a.scale, n == 0,
+                   static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + part * 32, a.dq.ld,
+                   ok ? r.m - row0 - w * 32 : 0, a.head_dim);
     tc_fence_before();
   }
   if (!ok && lane == 0) {
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dq_kernel(const __grid_
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -349,12 +373,11 @@ __device__ __forceinline__ uint32_t sum_offset(int tensor, int row, int unit) {
   return static_cast<uint32_t>(((tensor * kRows + row) * (HD / 4) + (unit ^ (row & 7))) * 16);
 }
 
-// A thread's share of its row: half of the columns of dV (parts 0, 1) or dK (2, 3).
+// A thread's share of its row: 64 columns of dV or dK, from `col` on.
 template <int HD>
-__device__ __forceinline__ void leave_sums(uint8_t* smem, uint32_t taddr, int part, int row, bool zero) {
-  const int col = (part & 1) * (HD / 2);
+__device__ __forceinline__ void leave_sums(uint8_t* smem, uint32_t taddr, int tensor, int col, int row, bool zero) {
 #pragma unroll
-  for (int c = 0; c < HD / 2; c += 32) {
+  for (int c = 0; c < 64; c += 32) {
     uint32_t v[32];
     if (!zero) {
       tmem_ld32(taddr + col + c, v);
@@ -365,7 +388,7 @@ __device__ __forceinline__ void leave_sums(uint8_t* smem, uint32_t taddr, int pa
     }
 #pragma unroll
     for (int e = 0; e < 32; e += 4)
-      *reinterpret_cast<uint4*>(smem + sum_offset<HD>(part >> 1, row, (col + c + e) / 4)) =
+      *reinterpret_cast<uint4*>(smem + sum_offset<HD>(tensor, row, (col + c + e) / 4)) =
           make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
   }
 }
@@ -383,7 +406,7 @@ template <int HD>
 __device__ __forceinline__ void join_sums(const uint8_t* smem, const muon_attention_t& a, int split, int rank, int t, int kvh,
                                           int64_t token0, int rows) {
   const int mine = kRows / split, total = 2 * mine * (HD / 8);
-  for (int i = t; i < total; i += 32 * kCompute) {
+  for (int i = t; i < total; i += 32 * BwdCfg<HD>::kCompute) {
     const int u = i % (HD / 8), row = rank * mine + i / (HD / 8) % mine, tensor = i / (HD / 8) / mine;
     if (row >= rows || u * 8 >= a.head_dim) continue;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -407,7 +430,7 @@ __device__ __forceinline__ void join_sums(const uint8_t* smem, const muon_attent
 // a key head and few tiles, a cluster shares the heads (dkv_split): each block leaves its sums in
 // its shared memory, and each then adds a share of the rows over all blocks, in their order.
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
+__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
   using C = BwdCfg<HD>;
   const muon_attention_t& a = P.a;
   const int split = static_cast<int>(cluster_num_ctas()), rank = static_cast<int>(cluster_cta_rank());
@@ -419,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   const SeqRange r = find_tile(a, true, kRows, block / a.kv_heads, static_cast<int>(gridDim.x) / split / a.kv_heads, lane, &key0);
   if (key0 >= r.n) return;
   const int shift = r.n - r.m;
-  const int tile0 = a.causal ? max(0, key0 - shift) / kRows : 0;  // the first row tile that sees a key
-  const int tiles = max(0, (r.m + kRows - 1) / kRows - tile0), n = tiles * per;
+  const int tile0 = a.causal ? max(0, key0 - shift) / C::kCols : 0;  // the first block of rows that sees a key
+  const int tiles = max(0, (r.m + C::kCols - 1) / C::kCols - tile0), n = tiles * per;
 
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -430,9 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   uint64_t* do_full = q_empty + 3;   // ring of dout blocks
   uint64_t* do_ready = do_full + 2;
   uint64_t* do_empty = do_ready + 2;
-  uint64_t* s_full = do_empty + 2;   // per block parity (two S), as p_full
-  uint64_t* p_full = s_full + 2;
-  uint64_t* dp_full = p_full + 2;
+  uint64_t* s_full = do_empty + 2;
+  uint64_t* p_full = s_full + 1;
+  uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* done = ds_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -451,12 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       mbar_init(&do_ready[s], 1);
       mbar_init(&do_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], kCompute);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(p_full, C::kCompute);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, kCompute);
+    mbar_init(ds_full, C::kCompute);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -464,28 +485,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     // the first blocks are on their way before the other warps are set up
     if (n > 0) {
       mbar_expect_tx(kv_full, 2 * C::kTile);
-      for (int c = 0; c < HD / 64; ++c) {
-        tma_load_3d(sk + c * kChunk, &P.tk, kv_full, c * 64, kvh, r.k0 + key0);
-        tma_load_3d(sv + c * kChunk, &P.tv, kv_full, c * 64, kvh, r.k0 + key0);
-      }
-      load_tile<HD>(sq, &P.tq, &q_full[0], head0, r.q0 + tile0 * kRows);
-      load_tile<HD>(sdo, &P.tdo, &do_full[0], head0, r.q0 + tile0 * kRows);
+      load_boxes<HD, kRows>(sk, &P.tk, kv_full, kvh, r.k0 + key0);
+      load_boxes<HD, kRows>(sv, &P.tv, kv_full, kvh, r.k0 + key0);
+      load_block<HD>(sq, &P.tq, &q_full[0], head0, r.q0 + tile0 * C::kCols);
+      load_block<HD>(sdo, &P.tdo, &do_full[0], head0, r.q0 + tile0 * C::kCols);
     }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  constexpr uint32_t kDp = 128, kDv = 256, kDk = 256 + HD;  // columns; S at 0, and at 384 (two S)
-  // the S of block j, and barriers that may complete for the next block before this one's wait
-  auto s_col = [](int j) { return C::kTwoS && (j & 1) ? 384u : 0u; };
-  auto s_par = [](int j) { return C::kTwoS ? j & 1 : 0; };
-  auto s_phase = [](int j) { return C::kTwoS ? j >> 1 : j; };
+  constexpr uint32_t kDp = C::kCols, kDv = 2 * C::kCols, kDk = kDv + HD;  // columns; S at 0
   bool ok = true;
+  if (C::kPerSm == 2 && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");  // see kPerSm
 
   if (warp == 0) {
     if (lane == 0 && n > 0) {
@@ -494,11 +510,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&q_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_tile<HD>(sq + j % 3 * C::kTile, &P.tq, &q_full[j % 3], h, r.q0 + t * kRows);
+        load_block<HD>(sq + j % 3 * C::kBlock, &P.tq, &q_full[j % 3], h, r.q0 + t * C::kCols);
         ++ql;
         ok = mbar_wait(&do_empty[j & 1], static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_tile<HD>(sdo + (j & 1) * C::kTile, &P.tdo, &do_full[j & 1], h, r.q0 + t * kRows);
+        load_block<HD>(sdo + (j & 1) * C::kBlock, &P.tdo, &do_full[j & 1], h, r.q0 + t * C::kCols);
         ++dl;
         if (++t == tile0 + tiles) t = tile0, ++h;
       }
@@ -508,40 +524,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       for (int j = dl > 2 ? dl - 2 : 0; j < dl; ++j) mbar_wait(&do_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), nullptr);
     }
   } else if (warp == 1) {
-    // One issuer keeps the order dV_j, S_{j+1} (two S: S_{j+2}), dK_j, dP_{j+1}: S_{j+1} is what the
-    // softmax waits for next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1}
-    // came 600 cycles later.
+    // One issuer keeps the order dV_j, S_{j+1}, dK_j, dP_{j+1}: S_{j+1} is what the softmax waits for
+    // next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1} came 600
+    // cycles later.
     if (n > 0) {
       auto score = [&](int j) {  // S^T_j; the P^T before it in these columns went into an earlier product
         if (!wait_all(&q_ready[j % 3], j / 3, abort_flag)) return false;
         if (elect_one()) {
-          product_ss<HD>(tmem + s_col(j), smem_u32(sk), smem_u32(sq) + j % 3 * C::kTile);
-          umma_commit(&s_full[s_par(j)]);
+          product_ss<HD>(tmem, smem_u32(sk), smem_u32(sq) + j % 3 * C::kBlock);
+          umma_commit(s_full);
         }
         return true;
       };
       auto dprob = [&](int j) {  // dP^T_j; dS^T_{j-1} over it went into a product issued before
         if (!wait_all(&do_ready[j & 1], j >> 1, abort_flag)) return false;
         if (elect_one()) {
-          product_ss<HD>(tmem + kDp, smem_u32(sv), smem_u32(sdo) + (j & 1) * C::kTile);
+          product_ss<HD>(tmem + kDp, smem_u32(sv), smem_u32(sdo) + (j & 1) * C::kBlock);
           umma_commit(dp_full);
         }
         return true;
       };
-      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0) && (!C::kTwoS || n < 2 || score(1));
+      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0);
       for (int j = 0; j < n && ok; ++j) {
-        ok = wait_all(&p_full[s_par(j)], s_phase(j), abort_flag);
+        ok = wait_all(p_full, j, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDv, tmem + s_col(j), smem_u32(sdo) + (j & 1) * C::kTile, j > 0);
+          product_ts<HD>(tmem + kDv, tmem, smem_u32(sdo) + (j & 1) * C::kBlock, j > 0);
           umma_commit(&do_empty[j & 1]);
         }
-        constexpr int ahead = C::kTwoS ? 2 : 1;
-        if (j + ahead < n) ok = score(j + ahead);
+        if (j + 1 < n) ok = score(j + 1);
         ok = ok && wait_all(ds_full, j, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kTile, j > 0);
+          product_ts<HD>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kBlock, j > 0);
           umma_commit(&q_empty[j % 3]);
           if (j + 1 == n) umma_commit(done);
         }
@@ -555,54 +570,54 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
     // P = 0.
     int h = head0, t = tile0;
     for (int j = 0; j < n; ++j) {
-      const int live = r.m - t * kRows;
-      const int64_t at = static_cast<int64_t>(h) * a.q_tokens + r.q0 + t * kRows;
-      float l[4], d[4];
+      const int live = r.m - t * C::kCols;
+      const int64_t at = static_cast<int64_t>(h) * a.q_tokens + r.q0 + t * C::kCols;
+      float l[C::kParts], d[C::kParts];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < C::kParts; ++e) {
         const int i = e * 32 + lane;
         const float x = i < live ? __ldg(a.lse + at + i) : -INFINITY;
         l[e] = x == -INFINITY ? INFINITY : x * kLog2e;
         d[e] = i < live ? P.delta[at + i] : 0.f;
       }
-      // With two of these vectors, block j - 2 is done with its own once its last product is
-      // complete; with three, the copy of Q_j came after that of block j - 3.
+      // block j - 2 is done with its vectors once its last product is complete
       ok = wait_all(&q_full[j % 3], j / 3, abort_flag) &&
-           (C::kVecs == 3 || j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
+           (j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
       if (!ok) break;
-      float* v = reinterpret_cast<float*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes);
+      float* v = reinterpret_cast<float*>(smem + C::kOffVec + (j & 1) * C::kVecBytes);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < C::kParts; ++e) {
         v[e * 32 + lane] = l[e];
-        v[kRows + e * 32 + lane] = d[e];
+        v[C::kCols + e * 32 + lane] = d[e];
       }
-      if (live < kRows) clear_rows<HD>(sq + j % 3 * C::kTile, live, lane);
+      if (live < C::kCols) clear_rows<HD>(sq + j % 3 * C::kBlock, live, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_ready[j % 3]);
       ok = wait_all(&do_full[j & 1], j >> 1, abort_flag);
       if (!ok) break;
-      if (live < kRows) clear_rows<HD>(sdo + (j & 1) * C::kTile, live, lane);
+      if (live < C::kCols) clear_rows<HD>(sdo + (j & 1) * C::kBlock, live, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&do_ready[j & 1]);
       if (++t == tile0 + tiles) t = tile0, ++h;
     }
   } else if (warp >= 4) {
-    const int w = warp & 3, part = (warp - 4) >> 2;     // lane quarter, and quarter of a block's rows
+    if (C::kPerSm == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    const int w = warp & 3, part = (warp - 4) >> 2;     // lane quarter, and 32 of a block's rows
     const int key = key0 + w * 32 + lane;               // within the sequence
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const float sl = a.scale * kLog2e;
     int t = tile0;
     for (int j = 0; j < n; ++j) {
-      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(&s_full[s_par(j)], s_phase(j), abort_flag);
+      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(s_full, j, abort_flag);
       if (!ok) break;
-      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes) + part * 8;
-      const float4* dlt = lse + kRows / 4;
-      const uint32_t ts = tmem + lanes + s_col(j) + part * 32, tp = tmem + lanes + kDp + part * 32;
+      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + (j & 1) * C::kVecBytes) + part * 8;
+      const float4* dlt = lse + C::kCols / 4;
+      const uint32_t ts = tmem + lanes + part * 32, tp = tmem + lanes + kDp + part * 32;
       uint32_t s[32], p[32], pk[16];
       tmem_ld32(ts, s);
       tmem_wait_ld();
-      // the first row of this quarter of the block that sees the key (rows are columns here)
-      const int first = a.causal ? key - shift - t * kRows - part * 32 : 0;
+      // the first row of this part of the block that sees the key (rows are columns here)
+      const int first = a.causal ? key - shift - t * C::kCols - part * 32 : 0;
       if (++t == tile0 + tiles) t = tile0;
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
@@ -623,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s_par(j)]);
+      if (lane == 0) mbar_arrive(p_full);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tp, p);
@@ -645,19 +660,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
       if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
+    // half of the parts write dV, half dK, 64 columns each
+    const int tensor = part / (C::kParts / 2), col = part % (C::kParts / 2) * 64;
+    const uint32_t acc = tmem + lanes + (tensor == 0 ? kDv : kDk);
     if (split > 1) {
-      leave_sums<HD>(smem, tmem + lanes + (part < 2 ? kDv : kDk), part, w * 32 + lane, n == 0);
+      leave_sums<HD>(smem, acc, tensor, col, w * 32 + lane, n == 0);
     } else {
       // staged where V and K were: their products are complete
-      const int64_t token = r.k0 + key0 + w * 32;
-      const int rows = ok ? r.n - key0 - w * 32 : 0;
-      const int col = (part & 1) * (HD / 2);
-      if (part < 2)
-        store_rows<HD / 2>(tmem + lanes + kDv + col, sv, w, lane, col, 1.f, n == 0,
-                           static_cast<uint16_t*>(a.dv.ptr) + token * a.dv.ld + kvh * a.dv.head + col, a.dv.ld, rows, a.head_dim);
-      else
-        store_rows<HD / 2>(tmem + lanes + kDk + col, sk, w, lane, col, a.scale, n == 0,
-                           static_cast<uint16_t*>(a.dk.ptr) + token * a.dk.ld + kvh * a.dk.head + col, a.dk.ld, rows, a.head_dim);
+      const muon_heads_t& out = tensor == 0 ? a.dv : a.dk;
+      store_rows<64>(acc + col, tensor == 0 ? sv : sk, w, lane, col, tensor == 0 ? 1.f : a.scale, n == 0,
+                     static_cast<uint16_t*>(out.ptr) + (r.k0 + key0 + w * 32) * out.ld + kvh * out.head + col, out.ld,
+                     ok ? r.n - key0 - w * 32 : 0, a.head_dim);
     }
     tc_fence_before();
   }
@@ -674,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_dkv_kernel(const __grid
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kTmem);
   }
 }
 
@@ -692,7 +705,7 @@ int dkv_split(const muon_attention_t& a, int64_t grid) {
 
 template <int HD>
 cudaError_t launch(const BwdParams& P, int dev, int64_t grid_q, int64_t grid_k, cudaStream_t st) {
-  constexpr int smem = BwdCfg<HD>::kSmemBytes;
+  constexpr int smem = BwdCfg<HD>::kSmemBytes, kThreads = BwdCfg<HD>::kThreads;
   static_assert(smem <= 227 * 1024, "shared memory");
   // the shared-memory opt-in is a per-device attribute: set it once on each device
   static std::atomic<uint64_t> attr_devices{0};
@@ -701,6 +714,13 @@ cudaError_t launch(const BwdParams& P, int dev, int64_t grid_q, int64_t grid_k, 
     cudaError_t e = cudaFuncSetAttribute(attention_dq_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(attention_dkv_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // all of the SM's memory, so that two blocks fit
+    if (e == cudaSuccess && BwdCfg<HD>::kPerSm > 1)
+      e = cudaFuncSetAttribute(attention_dq_kernel<HD>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && BwdCfg<HD>::kPerSm > 1)
+      e = cudaFuncSetAttribute(attention_dkv_kernel<HD>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_devices.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -733,10 +753,11 @@ cudaError_t launch_attention_backward(const muon_attention_t& a, float* delta, i
   std::memset(&P, 0, sizeof(P));
   P.a = a;
   P.delta = delta;
-  if (!encode_heads_map(&P.tq, a.q, a.q_tokens, a.heads, a.head_dim, kRows) ||
-      !encode_heads_map(&P.tdo, a.dout, a.q_tokens, a.heads, a.head_dim, kRows) ||
-      !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, kRows) ||
-      !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, kRows))
+  const int box = a.head_dim <= 64 ? BwdCfg<64>::kCols : BwdCfg<128>::kCols;
+  if (!encode_heads_map(&P.tq, a.q, a.q_tokens, a.heads, a.head_dim, box) ||
+      !encode_heads_map(&P.tdo, a.dout, a.q_tokens, a.heads, a.head_dim, box) ||
+      !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, box) ||
+      !encode_heads_map(&P.tv, a.v, a.k_tokens, a.kv_heads, a.head_dim, box))
     return cudaErrorInvalidValue;
   const int64_t grid_q = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, kRows) * a.heads;
   const int64_t grid_k = tile_slots(a.k_offsets, a.n_seq, a.k_tokens, kRows) * a.kv_heads;
