@@ -16,8 +16,8 @@
 // 3000, the tensor core active 64 and 68 % of the time. An M = 128 product whose operands both come
 // from shared memory runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles; the
 // rest is the chain product - exponential - product of a block.
-// Head dimension 64: 128 x 64 scores at a time, 8 warps, two blocks on an SM, whose chains, starts
-// and ends (about 8000 cycles of a block) overlap. With 128 x 128 scores and one block, sequences
+// Head dimension 64, large grids: 128 x 64 scores at a time, 8 warps, two blocks on an SM, whose
+// chains, starts and ends (about 8000 cycles of a block) overlap. With 128 x 128 scores and one block, sequences
 // of 1 to 2311 tokens, 12 heads, took 139 us instead of 109. The exponentials alone, taken in both
 // kernels, are 1024 cycles per 128 x 128 scores of each, the products 1280 and 1536 (S and dP at
 // half of the rate with 64 columns).
@@ -40,17 +40,17 @@ namespace {
 constexpr int kRows = 128;            // rows of a dQ tile, keys of a tile of dK and dV
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int HD>
+// W: keys (dQ) or rows (dK, dV) of a block. With 64 of them, head dimension 64 needs half of the
+// tensor memory and of the shared memory, and two thread blocks share an SM.
+template <int HD, int W>
 struct BwdCfg {
-  // Keys (dQ) or rows (dK, dV) of a block: with 64 of them, head dimension 64 needs half of the
-  // tensor memory and of the shared memory, and two thread blocks share an SM.
-  static constexpr int kCols = HD;
+  static constexpr int kCols = W;
   static constexpr int kParts = kCols / 32;                // 32 columns a thread
   static constexpr int kCompute = 4 * kParts;              // warps that compute
   static constexpr int kThreads = 32 * (4 + kCompute);     // and 4 that move and issue
   // Thread blocks on an SM. Two of 384 threads have 80 registers a thread at launch, of which the
   // four warps that move and issue leave some to the others: 128 x 64 + 256 x 88 is the same total.
-  static constexpr int kPerSm = HD == 64 ? 2 : 1;
+  static constexpr int kPerSm = W == 64 ? 2 : 1;
   static constexpr uint32_t kTmem = 512 / kPerSm;
   static constexpr int kTile = kRows * HD * 2;
   static constexpr int kBlock = kCols * HD * 2;
@@ -59,7 +59,12 @@ struct BwdCfg {
   static constexpr int kOffRing2 = kOffRing3 + kRing3 * kBlock;
   static constexpr int kOffVec = kOffRing2 + kRing2 * kBlock;  // lse and delta of a block of rows
   static constexpr int kVecBytes = 2 * kCols * 4;
-  static constexpr int kOffBar = kOffVec + 2 * kVecBytes;
+  // Blocks of 128 rows of head dimension 64 leave tensor memory for a second S in the kernel of dK
+  // and dV, so that the next block's scores are computed during this block's softmax; it then
+  // needs lse and delta of three blocks.
+  static constexpr bool kTwoS = HD == 64 && W == 128;
+  static constexpr int kVecs = kTwoS ? 3 : 2;
+  static constexpr int kOffBar = kOffVec + kVecs * kVecBytes;
   static constexpr int kSmemBytes = kOffBar + 512;
   static_assert(kParts * kRows * 4 <= 2 * kVecBytes, "exchange of the parts of delta");
   static_assert(2 * kRows * HD * 4 <= kOffVec, "sums shared by a cluster");
@@ -78,65 +83,61 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, int phase, volatile int*
   return got;
 }
 
-// Loads kR rows of one head by boxes of kCols rows.
+// Loads kR rows of one head by boxes of HD rows.
 template <int HD, int kR>
 __device__ __forceinline__ void load_boxes(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
-  constexpr int kCols = BwdCfg<HD>::kCols;
 #pragma unroll
   for (int c = 0; c < HD / 64; ++c)
 #pragma unroll
-    for (int b = 0; b < kR; b += kCols) tma_load_3d(dst + (c * kR + b) * 128, map, bar, c * 64, head, token + b);
+    for (int b = 0; b < kR; b += HD) tma_load_3d(dst + (c * kR + b) * 128, map, bar, c * 64, head, token + b);
 }
 
-template <int HD>
+template <int HD, int W>
 __device__ __forceinline__ void load_block(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int token) {
-  mbar_expect_tx(bar, BwdCfg<HD>::kBlock);
-  load_boxes<HD, BwdCfg<HD>::kCols>(dst, map, bar, head, token);
+  mbar_expect_tx(bar, BwdCfg<HD, W>::kBlock);
+  load_boxes<HD, W>(dst, map, bar, head, token);
 }
 
 // Zeros the rows from `live` on of a block in shared memory (one warp): another sequence's rows
 // that a product would sum over, with factors of zero but perhaps NaN themselves.
-template <int HD>
+template <int HD, int W>
 __device__ __forceinline__ void clear_rows(uint8_t* block, int live, int lane) {
-  constexpr int kCols = BwdCfg<HD>::kCols;
-  for (int e = live * 8 + lane; e < kCols * 8; e += 32)
+    for (int e = live * 8 + lane; e < W * 8; e += 32)
 #pragma unroll
     for (int c = 0; c < HD / 64; ++c)
-      *reinterpret_cast<uint4*>(block + c * (kCols * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(block + c * (W * 128) + e * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
 }
 
 // D = A B^T over the head dimension: a tile and a block in shared memory, both K-major.
-template <int HD>
+template <int HD, int W>
 __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
-  constexpr int kCols = BwdCfg<HD>::kCols;
-  constexpr uint32_t idesc = idesc_bf16_f32(128, kCols, false);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, W, false);
   const uint32_t ad = desc_lo(a_addr, 16), bd = desc_lo(b_addr, 16);
 #pragma unroll
   for (int k = 0; k < HD / 16; ++k) {
     const uint32_t c = k >> 2, in = (k & 3) * 2;
-    umma_f16_lo(d, ad + c * (kRows * 8) + in, bd + c * (kCols * 8) + in, kDescHi, idesc, k != 0);
+    umma_f16_lo(d, ad + c * (kRows * 8) + in, bd + c * (W * 8) + in, kDescHi, idesc, k != 0);
   }
 }
 
 // D (+)= A B over the rows or keys of a block: A bf16 in tensor memory (each 32 of them in the
 // first 16 of the 32 columns they came from), B an MN-major block in shared memory.
-template <int HD>
+template <int HD, int W>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate) {
-  constexpr int kCols = BwdCfg<HD>::kCols;
-  constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
-  const uint32_t bd = desc_lo(b_addr, kCols * 128);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
+  const uint32_t bd = desc_lo(b_addr, W * 128);
 #pragma unroll
-  for (int k = 0; k < kCols / 16; ++k)
+  for (int k = 0; k < W / 16; ++k)
     umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
 }
 
 // ------------------------------------------------------------------ dQ and delta
 // Chain A: S_j = Q K_j^T (two buffers), dQ += dS_j K_j.  Chain B: dP_j = dout V_j^T.
-template <int HD>
-__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) attention_dq_kernel(const __grid_constant__ BwdParams P) {
-  using C = BwdCfg<HD>;
+template <int HD, int W>
+__global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm) attention_dq_kernel(const __grid_constant__ BwdParams P) {
+  using C = BwdCfg<HD, W>;
   const muon_attention_t& a = P.a;
   const int heads = a.heads, head = static_cast<int>(blockIdx.x % heads);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -189,8 +190,8 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
     load_boxes<HD, kRows>(sq, &P.tq, q_full, head, r.q0 + row0);
     load_boxes<HD, kRows>(sdo, &P.tdo, q_full, head, r.q0 + row0);
     if (n > 0) {
-      load_block<HD>(sk, &P.tk, &k_full[0], kvh, r.k0);
-      load_block<HD>(sv, &P.tv, &v_full[0], kvh, r.k0);
+      load_block<HD, W>(sk, &P.tk, &k_full[0], kvh, r.k0);
+      load_block<HD, W>(sv, &P.tv, &v_full[0], kvh, r.k0);
     }
   }
   if (warp == 1) {
@@ -211,11 +212,11 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&k_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_block<HD>(sk + j % 3 * C::kBlock, &P.tk, &k_full[j % 3], kvh, r.k0 + j * C::kCols);
+        load_block<HD, W>(sk + j % 3 * C::kBlock, &P.tk, &k_full[j % 3], kvh, r.k0 + j * C::kCols);
         ++kl;
         ok = mbar_wait(&v_empty[j & 1], static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_block<HD>(sv + (j & 1) * C::kBlock, &P.tv, &v_full[j & 1], kvh, r.k0 + j * C::kCols);
+        load_block<HD, W>(sv + (j & 1) * C::kBlock, &P.tv, &v_full[j & 1], kvh, r.k0 + j * C::kCols);
         ++vl;
       }
       // never leave with bulk copies still landing in shared memory
@@ -228,9 +229,9 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       auto score = [&](int j) {  // S_j; the buffer's dS_{j-2} went into a product issued before
         if (!wait_all(&k_full[j % 3], j / 3, abort_flag)) return false;
         const int live = r.n - j * C::kCols;
-        if (live < C::kCols) clear_rows<HD>(sk + j % 3 * C::kBlock, live, lane);
+        if (live < C::kCols) clear_rows<HD, W>(sk + j % 3 * C::kBlock, live, lane);
         if (elect_one()) {
-          product_ss<HD>(tmem + (j & 1) * C::kCols, smem_u32(sq), smem_u32(sk) + j % 3 * C::kBlock);
+          product_ss<HD, W>(tmem + (j & 1) * C::kCols, smem_u32(sq), smem_u32(sk) + j % 3 * C::kBlock);
           umma_commit(&s_full[j & 1]);
         }
         return true;
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
         ok = wait_all(&ds_full[j & 1], j >> 1, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDq, tmem + (j & 1) * C::kCols, smem_u32(sk) + j % 3 * C::kBlock, j > 0);
+          product_ts<HD, W>(tmem + kDq, tmem + (j & 1) * C::kCols, smem_u32(sk) + j % 3 * C::kBlock, j > 0);
           umma_commit(&k_empty[j % 3]);
           if (j + 1 == n) umma_commit(done);
         }
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       for (int j = 0; j < n && ok; ++j) {
         ok = wait_all(&v_full[j & 1], j >> 1, abort_flag) && (j == 0 || wait_all(dp_read, j - 1, abort_flag));
         if (ok && elect_one()) {
-          product_ss<HD>(tmem + kDp, smem_u32(sdo), smem_u32(sv) + (j & 1) * C::kBlock);
+          product_ss<HD, W>(tmem + kDp, smem_u32(sdo), smem_u32(sv) + (j & 1) * C::kBlock);
           umma_commit(dp_full);
           umma_commit(&v_empty[j & 1]);
         }
@@ -268,12 +269,12 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
     const bool live = row < r.m;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     const int64_t token = r.q0 + row, vec = static_cast<int64_t>(head) * a.q_tokens + token;
-    // delta = o . dout: the threads of a row sum 32 of the columns each, dout from its tile in
+    // delta = o . dout: the threads of a row sum a share of the columns each, dout from its tile in
     // shared memory
     float lse = INFINITY;  // of rows without keys, or none: P = 0
     float sum[4] = {};
     {
-      constexpr int kUnits = 4;
+      constexpr int kUnits = HD / 8 / C::kParts;
       uint4 o[kUnits];
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.ptr) + token * a.o.ld + head * a.o.head);
 #pragma unroll
@@ -349,9 +350,10 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
     // staged where Q was: its products are complete
-    store_rows<32>(tmem + lanes + kDq + part * 32, sq, w, lane, part * 32, a.scale, n == 0,
-                   static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + part * 32, a.dq.ld,
-                   ok ? r.m - row0 - w * 32 : 0, a.head_dim);
+    if (part < HD / 32)
+      store_rows<32>(tmem + lanes + kDq + part * 32, sq, w, lane, part * 32, a.scale, n == 0,
+                     static_cast<uint16_t*>(a.dq.ptr) + (r.q0 + row0 + w * 32) * a.dq.ld + head * a.dq.head + part * 32, a.dq.ld,
+                     ok ? r.m - row0 - w * 32 : 0, a.head_dim);
     tc_fence_before();
   }
   if (!ok && lane == 0) {
@@ -373,11 +375,11 @@ __device__ __forceinline__ uint32_t sum_offset(int tensor, int row, int unit) {
   return static_cast<uint32_t>(((tensor * kRows + row) * (HD / 4) + (unit ^ (row & 7))) * 16);
 }
 
-// A thread's share of its row: 64 columns of dV or dK, from `col` on.
-template <int HD>
+// A thread's share of its row: kShare columns of dV or dK, from `col` on.
+template <int HD, int kShare>
 __device__ __forceinline__ void leave_sums(uint8_t* smem, uint32_t taddr, int tensor, int col, int row, bool zero) {
 #pragma unroll
-  for (int c = 0; c < 64; c += 32) {
+  for (int c = 0; c < kShare; c += 32) {
     uint32_t v[32];
     if (!zero) {
       tmem_ld32(taddr + col + c, v);
@@ -402,11 +404,11 @@ __device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
 
 // Adds rows rank * 128 / split .. of both tensors over the cluster's blocks, in their order, and
 // writes them: thread t of 32 kCompute takes 8 columns at a time. Of the tile's rows `rows` exist.
-template <int HD>
+template <int HD, int W>
 __device__ __forceinline__ void join_sums(const uint8_t* smem, const muon_attention_t& a, int split, int rank, int t, int kvh,
                                           int64_t token0, int rows) {
   const int mine = kRows / split, total = 2 * mine * (HD / 8);
-  for (int i = t; i < total; i += 32 * BwdCfg<HD>::kCompute) {
+  for (int i = t; i < total; i += 32 * BwdCfg<HD, W>::kCompute) {
     const int u = i % (HD / 8), row = rank * mine + i / (HD / 8) % mine, tensor = i / (HD / 8) / mine;
     if (row >= rows || u * 8 >= a.head_dim) continue;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -429,9 +431,9 @@ __device__ __forceinline__ void join_sums(const uint8_t* smem, const muon_attent
 // Block j runs over the row tiles that see the keys, head after head. With several query heads to
 // a key head and few tiles, a cluster shares the heads (dkv_split): each block leaves its sums in
 // its shared memory, and each then adds a share of the rows over all blocks, in their order.
-template <int HD>
-__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
-  using C = BwdCfg<HD>;
+template <int HD, int W>
+__global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm) attention_dkv_kernel(const __grid_constant__ BwdParams P) {
+  using C = BwdCfg<HD, W>;
   const muon_attention_t& a = P.a;
   const int split = static_cast<int>(cluster_num_ctas()), rank = static_cast<int>(cluster_cta_rank());
   const int block = static_cast<int>(blockIdx.x) / split;
@@ -453,9 +455,9 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
   uint64_t* do_full = q_empty + 3;   // ring of dout blocks
   uint64_t* do_ready = do_full + 2;
   uint64_t* do_empty = do_ready + 2;
-  uint64_t* s_full = do_empty + 2;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* dp_full = p_full + 1;
+  uint64_t* s_full = do_empty + 2;   // per block parity (two S), as p_full
+  uint64_t* p_full = s_full + 2;
+  uint64_t* dp_full = p_full + 2;
   uint64_t* ds_full = dp_full + 1;
   uint64_t* done = ds_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -474,8 +476,10 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       mbar_init(&do_ready[s], 1);
       mbar_init(&do_empty[s], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(p_full, C::kCompute);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], C::kCompute);
+    }
     mbar_init(dp_full, 1);
     mbar_init(ds_full, C::kCompute);
     mbar_init(done, 1);
@@ -487,8 +491,8 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       mbar_expect_tx(kv_full, 2 * C::kTile);
       load_boxes<HD, kRows>(sk, &P.tk, kv_full, kvh, r.k0 + key0);
       load_boxes<HD, kRows>(sv, &P.tv, kv_full, kvh, r.k0 + key0);
-      load_block<HD>(sq, &P.tq, &q_full[0], head0, r.q0 + tile0 * C::kCols);
-      load_block<HD>(sdo, &P.tdo, &do_full[0], head0, r.q0 + tile0 * C::kCols);
+      load_block<HD, W>(sq, &P.tq, &q_full[0], head0, r.q0 + tile0 * C::kCols);
+      load_block<HD, W>(sdo, &P.tdo, &do_full[0], head0, r.q0 + tile0 * C::kCols);
     }
   }
   if (warp == 1) {
@@ -499,7 +503,11 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  constexpr uint32_t kDp = C::kCols, kDv = 2 * C::kCols, kDk = kDv + HD;  // columns; S at 0
+  constexpr uint32_t kDp = C::kCols, kDv = 2 * C::kCols, kDk = kDv + HD;  // columns; S at 0, and behind them (two S)
+  // the S of block j, and barriers that may complete for the next block before this one's wait
+  auto s_col = [](int j) { return C::kTwoS && (j & 1) ? kDk + HD : 0u; };
+  auto s_par = [](int j) { return C::kTwoS ? j & 1 : 0; };
+  auto s_phase = [](int j) { return C::kTwoS ? j >> 1 : j; };
   bool ok = true;
   if (C::kPerSm == 2 && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");  // see kPerSm
 
@@ -510,11 +518,11 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       for (int j = 1; j < n; ++j) {
         ok = mbar_wait(&q_empty[j % 3], static_cast<uint32_t>((j / 3) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_block<HD>(sq + j % 3 * C::kBlock, &P.tq, &q_full[j % 3], h, r.q0 + t * C::kCols);
+        load_block<HD, W>(sq + j % 3 * C::kBlock, &P.tq, &q_full[j % 3], h, r.q0 + t * C::kCols);
         ++ql;
         ok = mbar_wait(&do_empty[j & 1], static_cast<uint32_t>((j >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        load_block<HD>(sdo + (j & 1) * C::kBlock, &P.tdo, &do_full[j & 1], h, r.q0 + t * C::kCols);
+        load_block<HD, W>(sdo + (j & 1) * C::kBlock, &P.tdo, &do_full[j & 1], h, r.q0 + t * C::kCols);
         ++dl;
         if (++t == tile0 + tiles) t = tile0, ++h;
       }
@@ -524,39 +532,40 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       for (int j = dl > 2 ? dl - 2 : 0; j < dl; ++j) mbar_wait(&do_full[j & 1], static_cast<uint32_t>((j >> 1) & 1), nullptr);
     }
   } else if (warp == 1) {
-    // One issuer keeps the order dV_j, S_{j+1}, dK_j, dP_{j+1}: S_{j+1} is what the softmax waits for
-    // next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1} came 600
+    // One issuer keeps the order dV_j, S_{j+1} (two S: S_{j+2}), dK_j, dP_{j+1}: S_{j+1} is what the
+    // softmax waits for next. Issued by two warps, the two chains share the tensor core evenly and S_{j+1} came 600
     // cycles later.
     if (n > 0) {
       auto score = [&](int j) {  // S^T_j; the P^T before it in these columns went into an earlier product
         if (!wait_all(&q_ready[j % 3], j / 3, abort_flag)) return false;
         if (elect_one()) {
-          product_ss<HD>(tmem, smem_u32(sk), smem_u32(sq) + j % 3 * C::kBlock);
-          umma_commit(s_full);
+          product_ss<HD, W>(tmem + s_col(j), smem_u32(sk), smem_u32(sq) + j % 3 * C::kBlock);
+          umma_commit(&s_full[s_par(j)]);
         }
         return true;
       };
       auto dprob = [&](int j) {  // dP^T_j; dS^T_{j-1} over it went into a product issued before
         if (!wait_all(&do_ready[j & 1], j >> 1, abort_flag)) return false;
         if (elect_one()) {
-          product_ss<HD>(tmem + kDp, smem_u32(sv), smem_u32(sdo) + (j & 1) * C::kBlock);
+          product_ss<HD, W>(tmem + kDp, smem_u32(sv), smem_u32(sdo) + (j & 1) * C::kBlock);
           umma_commit(dp_full);
         }
         return true;
       };
-      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0);
+      ok = wait_all(kv_full, 0, abort_flag) && score(0) && dprob(0) && (!C::kTwoS || n < 2 || score(1));
       for (int j = 0; j < n && ok; ++j) {
-        ok = wait_all(p_full, j, abort_flag);
+        ok = wait_all(&p_full[s_par(j)], s_phase(j), abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDv, tmem, smem_u32(sdo) + (j & 1) * C::kBlock, j > 0);
+          product_ts<HD, W>(tmem + kDv, tmem + s_col(j), smem_u32(sdo) + (j & 1) * C::kBlock, j > 0);
           umma_commit(&do_empty[j & 1]);
         }
-        if (j + 1 < n) ok = score(j + 1);
+        constexpr int ahead = C::kTwoS ? 2 : 1;
+        if (j + ahead < n) ok = score(j + ahead);
         ok = ok && wait_all(ds_full, j, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kBlock, j > 0);
+          product_ts<HD, W>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kBlock, j > 0);
           umma_commit(&q_empty[j % 3]);
           if (j + 1 == n) umma_commit(done);
         }
@@ -580,22 +589,23 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
         l[e] = x == -INFINITY ? INFINITY : x * kLog2e;
         d[e] = i < live ? P.delta[at + i] : 0.f;
       }
-      // block j - 2 is done with its vectors once its last product is complete
+      // With two of these vectors, block j - 2 is done with its own once its last product is
+      // complete; with three, the copy of Q_j came after that of block j - 3.
       ok = wait_all(&q_full[j % 3], j / 3, abort_flag) &&
-           (j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
+           (C::kVecs == 3 || j < 2 || wait_all(&q_empty[(j - 2) % 3], (j - 2) / 3, abort_flag));
       if (!ok) break;
-      float* v = reinterpret_cast<float*>(smem + C::kOffVec + (j & 1) * C::kVecBytes);
+      float* v = reinterpret_cast<float*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes);
 #pragma unroll
       for (int e = 0; e < C::kParts; ++e) {
         v[e * 32 + lane] = l[e];
         v[C::kCols + e * 32 + lane] = d[e];
       }
-      if (live < C::kCols) clear_rows<HD>(sq + j % 3 * C::kBlock, live, lane);
+      if (live < C::kCols) clear_rows<HD, W>(sq + j % 3 * C::kBlock, live, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_ready[j % 3]);
       ok = wait_all(&do_full[j & 1], j >> 1, abort_flag);
       if (!ok) break;
-      if (live < C::kCols) clear_rows<HD>(sdo + (j & 1) * C::kBlock, live, lane);
+      if (live < C::kCols) clear_rows<HD, W>(sdo + (j & 1) * C::kBlock, live, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&do_ready[j & 1]);
       if (++t == tile0 + tiles) t = tile0, ++h;
@@ -608,11 +618,11 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
     const float sl = a.scale * kLog2e;
     int t = tile0;
     for (int j = 0; j < n; ++j) {
-      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(s_full, j, abort_flag);
+      ok = wait_all(&q_ready[j % 3], j / 3, abort_flag) && wait_all(&s_full[s_par(j)], s_phase(j), abort_flag);
       if (!ok) break;
-      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + (j & 1) * C::kVecBytes) + part * 8;
+      const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes) + part * 8;
       const float4* dlt = lse + C::kCols / 4;
-      const uint32_t ts = tmem + lanes + part * 32, tp = tmem + lanes + kDp + part * 32;
+      const uint32_t ts = tmem + lanes + s_col(j) + part * 32, tp = tmem + lanes + kDp + part * 32;
       uint32_t s[32], p[32], pk[16];
       tmem_ld32(ts, s);
       tmem_wait_ld();
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(&p_full[s_par(j)]);
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tp, p);
@@ -660,17 +670,18 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
       if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok && n > 0) ok = wait_all(done, 0, abort_flag);
-    // half of the parts write dV, half dK, 64 columns each
-    const int tensor = part / (C::kParts / 2), col = part % (C::kParts / 2) * 64;
+    // half of the parts write dV, half dK
+    constexpr int kShare = 2 * HD / C::kParts;
+    const int tensor = part / (C::kParts / 2), col = part % (C::kParts / 2) * kShare;
     const uint32_t acc = tmem + lanes + (tensor == 0 ? kDv : kDk);
     if (split > 1) {
-      leave_sums<HD>(smem, acc, tensor, col, w * 32 + lane, n == 0);
+      leave_sums<HD, kShare>(smem, acc, tensor, col, w * 32 + lane, n == 0);
     } else {
       // staged where V and K were: their products are complete
       const muon_heads_t& out = tensor == 0 ? a.dv : a.dk;
-      store_rows<64>(acc + col, tensor == 0 ? sv : sk, w, lane, col, tensor == 0 ? 1.f : a.scale, n == 0,
-                     static_cast<uint16_t*>(out.ptr) + (r.k0 + key0 + w * 32) * out.ld + kvh * out.head + col, out.ld,
-                     ok ? r.n - key0 - w * 32 : 0, a.head_dim);
+      store_rows<kShare>(acc + col, tensor == 0 ? sv : sk, w, lane, col, tensor == 0 ? 1.f : a.scale, n == 0,
+                         static_cast<uint16_t*>(out.ptr) + (r.k0 + key0 + w * 32) * out.ld + kvh * out.head + col, out.ld,
+                         ok ? r.n - key0 - w * 32 : 0, a.head_dim);
     }
     tc_fence_before();
   }
@@ -682,7 +693,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, BwdCfg<HD>::kPerSm) atte
   if (split > 1) {
     cluster_sync_all();
     if (warp >= 4)
-      join_sums<HD>(smem, a, split, rank, static_cast<int>(threadIdx.x) - 128, kvh, r.k0 + key0, r.n - key0);
+      join_sums<HD, W>(smem, a, split, rank, static_cast<int>(threadIdx.x) - 128, kvh, r.k0 + key0, r.n - key0);
     cluster_sync_all();  // nobody leaves while its sums are read
   }
   if (warp == 1) {
@@ -703,47 +714,50 @@ int dkv_split(const muon_attention_t& a, int64_t grid) {
   return split;
 }
 
-template <int HD>
-cudaError_t launch(const BwdParams& P, int dev, int64_t grid_q, int64_t grid_k, cudaStream_t st) {
-  constexpr int smem = BwdCfg<HD>::kSmemBytes, kThreads = BwdCfg<HD>::kThreads;
-  static_assert(smem <= 227 * 1024, "shared memory");
-  // the shared-memory opt-in is a per-device attribute: set it once on each device
-  static std::atomic<uint64_t> attr_devices{0};
+// Head dimension 64: blocks of 64 columns, two of them on an SM, where a grid gives every SM more
+// than two; else blocks of 128, whose chain is shorter per column. dQ / dK and dV of causal
+// sequences, 64 against 128 columns: 4096 tokens and 8 heads (264 blocks) 54 / 73 against 42 / 56 us,
+// 12 heads (396) 60 / 79 against 65 / 90, 24 heads (792) 106 / 138 against 120 / 162.
+bool narrow(int64_t grid) { return grid > 2 * 148; }
+
+template <class C>
+cudaError_t launch(void (*kernel)(BwdParams), std::atomic<uint64_t>& attr_devices, const BwdParams& P, int dev, int64_t grid,
+                   int cluster, cudaStream_t st) {
+  static_assert(C::kSmemBytes <= 227 * 1024, "shared memory");
+  // function attributes are per device: set them once on each device
   const uint64_t bit = dev < 64 ? (uint64_t{1} << dev) : 0;
   if (bit == 0 || !(attr_devices.load(std::memory_order_acquire) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(attention_dq_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attention_dkv_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    // all of the SM's memory, so that two blocks fit
-    if (e == cudaSuccess && BwdCfg<HD>::kPerSm > 1)
-      e = cudaFuncSetAttribute(attention_dq_kernel<HD>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess && BwdCfg<HD>::kPerSm > 1)
-      e = cudaFuncSetAttribute(attention_dkv_kernel<HD>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e == cudaSuccess && C::kPerSm > 1)  // all of the SM's memory, so that two blocks fit
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     attr_devices.fetch_or(bit, std::memory_order_acq_rel);
   }
-  if (P.a.q_tokens > 0) {
-    attention_dq_kernel<HD><<<static_cast<unsigned>(grid_q), kThreads, smem, st>>>(P);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (P.a.k_tokens == 0) return cudaSuccess;
-  const int split = dkv_split(P.a, grid_k);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid_k * split), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, attention_dkv_kernel<HD>, P);
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P);
+}
+
+template <int HD, int W>
+cudaError_t launch_dq(const BwdParams& P, int dev, int64_t grid, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_devices{0};
+  return launch<BwdCfg<HD, W>>(attention_dq_kernel<HD, W>, attr_devices, P, dev, grid, 1, st);
+}
+
+template <int HD, int W>
+cudaError_t launch_dkv(const BwdParams& P, int dev, int64_t grid, int split, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_devices{0};
+  return launch<BwdCfg<HD, W>>(attention_dkv_kernel<HD, W>, attr_devices, P, dev, grid * split, split, st);
 }
 
 }  // namespace
@@ -753,7 +767,7 @@ cudaError_t launch_attention_backward(const muon_attention_t& a, float* delta, i
   std::memset(&P, 0, sizeof(P));
   P.a = a;
   P.delta = delta;
-  const int box = a.head_dim <= 64 ? BwdCfg<64>::kCols : BwdCfg<128>::kCols;
+  const int box = a.head_dim <= 64 ? 64 : 128;
   if (!encode_heads_map(&P.tq, a.q, a.q_tokens, a.heads, a.head_dim, box) ||
       !encode_heads_map(&P.tdo, a.dout, a.q_tokens, a.heads, a.head_dim, box) ||
       !encode_heads_map(&P.tk, a.k, a.k_tokens, a.kv_heads, a.head_dim, box) ||
@@ -762,7 +776,17 @@ cudaError_t launch_attention_backward(const muon_attention_t& a, float* delta, i
   const int64_t grid_q = tile_slots(a.q_offsets, a.n_seq, a.q_tokens, kRows) * a.heads;
   const int64_t grid_k = tile_slots(a.k_offsets, a.n_seq, a.k_tokens, kRows) * a.kv_heads;
   if (grid_q >= (int64_t(1) << 31) || grid_k >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  return a.head_dim <= 64 ? launch<64>(P, dev, grid_q, grid_k, st) : launch<128>(P, dev, grid_q, grid_k, st);
+  if (a.q_tokens > 0) {
+    const cudaError_t e = a.head_dim > 64  ? launch_dq<128, 128>(P, dev, grid_q, st)
+                          : narrow(grid_q) ? launch_dq<64, 64>(P, dev, grid_q, st)
+                                           : launch_dq<64, 128>(P, dev, grid_q, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.k_tokens == 0) return cudaSuccess;
+  const int split = dkv_split(a, grid_k);
+  return a.head_dim > 64          ? launch_dkv<128, 128>(P, dev, grid_k, split, st)
+         : narrow(grid_k * split) ? launch_dkv<64, 64>(P, dev, grid_k, split, st)
+                                  : launch_dkv<64, 128>(P, dev, grid_k, split, st);
 }
 
 }  // namespace muon

@@ -323,6 +323,9 @@ ATTN = [
     ([3, 0, 7, 200], [0, 9, 130, 1], 2, 2, 128), ([1, 1, 1], [700, 128, 129], 4, 1, 64), ([1000], None, 1, 1, 128),
     ([640, 1, 2, 129], None, 8, 2, 128), ([130], [0], 2, 1, 64), ([0], [130], 2, 1, 64), ([1500], None, 2, 2, 72),
     ([513], [769], 3, 3, 128),
+    # many heads: grids that fill the GPU take other blocks
+    ([65, 300, 1, 130], None, 80, 80, 64), ([257], None, 120, 60, 40), ([3, 0, 7, 200], [0, 9, 130, 1], 100, 100, 64),
+    ([64, 63], [190, 1], 128, 32, 8), ([200, 321], [64, 500], 72, 72, 128),
 ]
 
 
