@@ -356,6 +356,8 @@ MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, void* works
  * The backward pass recomputes P = exp(S - lse) and needs the forward pass's o and lse:
  *   delta_i = o_i . dout_i,  dV = P^T dout,  dS = P (dout V^T - delta)
  *   dQ = scale dS K,  dK = scale dS^T Q   (dK and dV summed over the heads of a key head)
+ * o and lse may be those of more keys than the call's: the gradients are then these keys'
+ * terms of the whole. A row whose softmax is one key alone has dQ = 0 exactly.
  * Keys that no row sees get zero gradients. Sums are taken in a fixed order: the results
  * of equal calls are equal bit for bit.
  * Tensors q, o, dout, dq (q_tokens x heads x head_dim) and k, v, dk, dv (k_tokens x

@@ -133,6 +133,14 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t
     umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
 }
 
+// Whether the probability of a row's lone key is 1 up to the rounding of its exponent (lse in units
+// of log 2, rounded a few times). Then o is the key's v and dS = 0: taken so, dQ of such a row is
+// zero to the last bit, not the difference of two sums of o . dout. (Not so where a caller passes
+// the lse of more keys than these.)
+__device__ __forceinline__ bool is_one(float p, float lse) {
+  return fabsf(p - 1.f) <= fmaf(fabsf(lse), 0x1p-21f, 0x1p-21f);
+}
+
 // ------------------------------------------------------------------ dQ and delta
 // Chain A: S_j = Q K_j^T (two buffers), dQ += dS_j K_j.  Chain B: dP_j = dout V_j^T.
 template <int HD, int W>
@@ -323,6 +331,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
       if (!ok) break;
 #pragma unroll
       for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[e]), sl, -lse)));
+      if (j == 0 && part == 0 && vis == 1 && is_one(__uint_as_float(s[0]), lse)) s[0] = 0;
       __syncwarp();
       if (C::kPerSm == 1 && lane == 0) mbar_arrive(&turn[4 * grp + w]);
       ok = wait_all(dp_full, j, abort_flag);
@@ -628,6 +637,9 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
       tmem_wait_ld();
       // the first row of this part of the block that sees the key (rows are columns here)
       const int first = a.causal ? key - shift - t * C::kCols - part * 32 : 0;
+      // and those, [lone, lone_end), that see key 0 alone (is_one)
+      const int lone = (a.causal ? max(0, -shift) : 0) - t * C::kCols - part * 32;
+      const int lone_end = key0 > 0 ? -1 : (r.n == 1 ? r.m : a.causal ? 1 - shift : 0) - t * C::kCols - part * 32;
       if (++t == tile0 + tiles) t = tile0;
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
@@ -649,6 +661,11 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[s_par(j)]);
+      if (lone < 32 && lone_end > max(lone, 0)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e >= lone && e < lone_end && is_one(__uint_as_float(s[e]), reinterpret_cast<const float*>(lse)[e])) s[e] = 0;
+      }
       ok = wait_all(dp_full, j, abort_flag);
       if (!ok) break;
       tmem_ld32(tp, p);

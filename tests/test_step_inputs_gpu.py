@@ -498,6 +498,43 @@ def test_attention_keys_masked_by_infinite_entries(B, d):
     ref.check(s_max, want["s_max"], torch.as_tensor(tol["s_max"]), "s_max")
 
 
+@pytest.mark.parametrize("heads,d", [(4, 128), (4, 64), (160, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_gradients_of_lone_keys_are_exactly_zero(B, heads, d, causal):
+    """A row that sees one key has P = 1 whatever its logit: dQ of the row is zero, and dK gets
+    nothing from it, without a rounding. Sequences of one key, and first rows of causal ones."""
+    q_len, k_len = [1, 5, 130, 200, 3, 140], [1, 1, 1, 200, 6, 70]
+    q, k, v, do = inputs(15, q_len, k_len, heads, heads // 2, d)
+    o, _, _, dq, dk, _ = both(B, q, k, v, do, q_len, k_len, causal)
+    a = b = 0
+    for m, n in zip(q_len, k_len):
+        seen = [min(n, i + n - m + 1) if causal else n for i in range(m)]
+        for i in range(m):
+            if seen[i] == 1:
+                assert bool((dq[a + i] == 0).all()), (m, n, i)
+        if max(seen) == 1:
+            assert bool((dk[b:b + n] == 0).all()), (m, n)
+        a, b = a + m, b + n
+    assert bool((dq != 0).any()) and bool((dk != 0).any())
+
+
+@pytest.mark.parametrize("heads,d", [(2, 128), (2, 64), (160, 64)])
+def test_attention_gradients_by_parts_of_the_keys(B, heads, d):
+    """With o and lse of all keys, the gradients of parts of the keys (one of a single key) are the
+    terms of the whole: dQ adds up, dK and dV lie side by side."""
+    q, k, v, do = inputs(16, [150], [150], heads, heads, d)
+    o, lse = B.attention_forward(q, k, v, causal=False)
+    want, tol = ref.attention(q, k, v, [150], [150], False, d ** -0.5, do, o, lse)
+    parts = [(0, 1), (1, 130), (130, 150)]
+    got = [B.attention_backward(do, q, k[a:b], v[a:b], o, lse, causal=False) for a, b in parts]
+    # three roundings of a part's dQ to bf16, each of a term that ref.attention bounds with the sum
+    mag = sum(g[0].double().abs() for g in got)
+    ref.check(sum(g[0].double() for g in got), want["dq"], tol["dq"] + ref.U_BF16 * mag, "dq")
+    ref.check(torch.cat([g[1] for g in got]), want["dk"], tol["dk"], "dk")
+    ref.check(torch.cat([g[2] for g in got]), want["dv"], tol["dv"], "dv")
+    assert bool((got[0][1] != 0).any())
+
+
 def test_attention_gradients_against_differences(B):
     """A directional difference of sum(o * dout) in float64 against the kernel's gradients."""
     lens = [70, 33]
