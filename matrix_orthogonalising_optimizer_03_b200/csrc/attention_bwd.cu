@@ -8,7 +8,8 @@
 // and dV, over all query heads of the key head. S and dout V^T are computed in both: seven
 // products instead of five, against fp32 atomics on dQ, whose order changes its sums.
 // A thread owns 32 elements of one lane's row. P and dS are rounded to bf16 (at most 2^-8 relative,
-// errors of either sign) and written back over the scores they came from, where the next product
+// errors of either sign; sums of a single block also add the product with the rounding's rest, see
+// kExact) and written back over the scores they came from, where the next product
 // takes them as its tensor-memory operand; the transposes that dV and dK need cost nothing, because
 // the second kernel computes S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
 // Head dimension 128: 128 x 128 scores at a time, 16 warps, one block on an SM. Per 128 x 128
@@ -52,6 +53,9 @@ struct BwdCfg {
   // four warps that move and issue leave some to the others: 128 x 64 + 256 x 88 is the same total.
   static constexpr int kPerSm = W == 64 ? 2 : 1;
   static constexpr uint32_t kTmem = 512 / kPerSm;
+  // Sums of a single block also take the rest of the rounding of P and dS (store_operand). Two
+  // blocks an SM leave no registers for it (it spilled: 107 -> 119 us), and are many tiles.
+  static constexpr bool kExact = kPerSm == 1;
   static constexpr int kTile = kRows * HD * 2;
   static constexpr int kBlock = kCols * HD * 2;
   static constexpr int kRing3 = 3, kRing2 = 2;  // the operand of two chains, and of one
@@ -125,12 +129,33 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t
 // D (+)= A B over the rows or keys of a block: A bf16 in tensor memory (each 32 of them in the
 // first 16 of the 32 columns they came from), B an MN-major block in shared memory.
 template <int HD, int W>
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate) {
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate, bool exact) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
   const uint32_t bd = desc_lo(b_addr, W * 128);
 #pragma unroll
   for (int k = 0; k < W / 16; ++k)
     umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8, bd + 128u * k, kDescHi, idesc, accumulate || k != 0);
+  if (exact)  // and the rest of A, see store_operand
+#pragma unroll
+    for (int k = 0; k < W / 16; ++k)
+      umma_f16_ts_lo(d, a_tmem + (k >> 1) * 32 + (k & 1) * 8 + 16, bd + 128u * k, kDescHi, idesc, true);
+}
+
+// Writes 32 values as bf16 into the first 16 columns of a thread's 32, where product_ts takes them;
+// with `exact`, what their rounding left as bf16 into the other 16.
+__device__ __forceinline__ void store_operand(uint32_t taddr, const uint32_t (&x)[32], bool exact) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) pk[e] = round_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+  tmem_st16(taddr, pk);
+  if (exact) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      pk[e] = round_bf16x2(__uint_as_float(x[2 * e]) - __uint_as_float(pk[e] << 16),
+                           __uint_as_float(x[2 * e + 1]) - __uint_as_float(pk[e] & 0xFFFF0000u));
+    tmem_st16(taddr + 16, pk);
+  }
+  tmem_wait_st();
 }
 
 // Whether the probability of a row's lone key is 1 up to the rounding of its exponent (lse in units
@@ -249,7 +274,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
         ok = wait_all(&ds_full[j & 1], j >> 1, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD, W>(tmem + kDq, tmem + (j & 1) * C::kCols, smem_u32(sk) + j % 3 * C::kBlock, j > 0);
+          product_ts<HD, W>(tmem + kDq, tmem + (j & 1) * C::kCols, smem_u32(sk) + j % 3 * C::kBlock, j > 0, C::kExact && n == 1);
           umma_commit(&k_empty[j % 3]);
           if (j + 1 == n) umma_commit(done);
         }
@@ -348,11 +373,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
         for (int e = 0; e < 32; ++e)
           if (e >= vis) s[e] = 0;
       }
-      uint32_t pk[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = round_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-      tmem_st16(ts, pk);
-      tmem_wait_st();
+      store_operand(ts, s, C::kExact && n == 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ds_full[j & 1]);
@@ -566,7 +587,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
         ok = wait_all(&p_full[s_par(j)], s_phase(j), abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD, W>(tmem + kDv, tmem + s_col(j), smem_u32(sdo) + (j & 1) * C::kBlock, j > 0);
+          product_ts<HD, W>(tmem + kDv, tmem + s_col(j), smem_u32(sdo) + (j & 1) * C::kBlock, j > 0, C::kExact && n == 1);
           umma_commit(&do_empty[j & 1]);
         }
         constexpr int ahead = C::kTwoS ? 2 : 1;
@@ -574,7 +595,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
         ok = ok && wait_all(ds_full, j, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          product_ts<HD, W>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kBlock, j > 0);
+          product_ts<HD, W>(tmem + kDk, tmem + kDp, smem_u32(sq) + j % 3 * C::kBlock, j > 0, C::kExact && n == 1);
           umma_commit(&q_empty[j % 3]);
           if (j + 1 == n) umma_commit(done);
         }
@@ -632,7 +653,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
       const float4* lse = reinterpret_cast<const float4*>(smem + C::kOffVec + j % C::kVecs * C::kVecBytes) + part * 8;
       const float4* dlt = lse + C::kCols / 4;
       const uint32_t ts = tmem + lanes + s_col(j) + part * 32, tp = tmem + lanes + kDp + part * 32;
-      uint32_t s[32], p[32], pk[16];
+      uint32_t s[32], p[32];
       tmem_ld32(ts, s);
       tmem_wait_ld();
       // the first row of this part of the block that sees the key (rows are columns here)
@@ -654,10 +675,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
         for (int e = 0; e < 32; ++e)
           if (e < first) s[e] = 0;
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = round_bf16x2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-      tmem_st16(ts, pk);
-      tmem_wait_st();
+      store_operand(ts, s, C::kExact && n == 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[s_par(j)]);
@@ -673,15 +691,12 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 d = dlt[e / 4];
-        const float x0 = __uint_as_float(s[e]) * (__uint_as_float(p[e]) - d.x);
-        const float x1 = __uint_as_float(s[e + 1]) * (__uint_as_float(p[e + 1]) - d.y);
-        const float x2 = __uint_as_float(s[e + 2]) * (__uint_as_float(p[e + 2]) - d.z);
-        const float x3 = __uint_as_float(s[e + 3]) * (__uint_as_float(p[e + 3]) - d.w);
-        pk[e / 2] = round_bf16x2(x0, x1);
-        pk[e / 2 + 1] = round_bf16x2(x2, x3);
+        s[e] = __float_as_uint(__uint_as_float(s[e]) * (__uint_as_float(p[e]) - d.x));
+        s[e + 1] = __float_as_uint(__uint_as_float(s[e + 1]) * (__uint_as_float(p[e + 1]) - d.y));
+        s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * (__uint_as_float(p[e + 2]) - d.z));
+        s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * (__uint_as_float(p[e + 3]) - d.w));
       }
-      tmem_st16(tp, pk);
-      tmem_wait_st();
+      store_operand(tp, s, C::kExact && n == 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);

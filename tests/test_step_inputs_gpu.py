@@ -518,6 +518,22 @@ def test_attention_gradients_of_lone_keys_are_exactly_zero(B, heads, d, causal):
     assert bool((dq != 0).any()) and bool((dk != 0).any())
 
 
+@pytest.mark.parametrize("q_len,k_len,h,g,d", [([3, 10, 60], None, 2, 2, 96), ([3], [12], 2, 1, 64), ([128], [100], 3, 3, 128)])
+def test_attention_gradients_of_short_sequences_round_once(B, q_len, k_len, h, g, d):
+    """Sums of one block take P and dS with 16 bits, so that dV is off by the rounding of the result
+    and the fp32 sums alone: 2^-8 |dV| and an eighth of the general bound, 2^-11 of the sum of
+    magnitudes (what is left of P's rounding is 2^-16 of it, the error of S about 2^-12)."""
+    k_len = q_len if k_len is None else k_len
+    q, k, v, do = inputs(17, q_len, k_len, h, g, d)
+    qo, ko = ints(offsets_of(q_len)), ints(offsets_of(k_len))
+    o, lse = B.attention_forward(q, k, v, q_offsets=qo, k_offsets=ko, causal=False)
+    dq, dk, dv = B.attention_backward(do, q, k, v, o, lse, q_offsets=qo, k_offsets=ko, causal=False)
+    want, tol = ref.attention(q, k, v, q_len, k_len, False, d ** -0.5, do, o, lse)
+    ref.check(dv, want["dv"], ref.U_BF16 * want["dv"].abs() + tol["dv"] / 8, "dv")
+    for n, t in (("dq", dq), ("dk", dk)):
+        ref.check(t, want[n], tol[n], n)
+
+
 @pytest.mark.parametrize("heads,d", [(2, 128), (2, 64), (160, 64)])
 def test_attention_gradients_by_parts_of_the_keys(B, heads, d):
     """With o and lse of all keys, the gradients of parts of the keys (one of a single key) are the
