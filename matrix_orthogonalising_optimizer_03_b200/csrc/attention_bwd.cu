@@ -9,19 +9,19 @@
 // products instead of five, against fp32 atomics on dQ, whose order changes its sums.
 // A thread owns 32 elements of one lane's row. P and dS are rounded to bf16 (at most 2^-8 relative,
 // errors of either sign; sums of a single block also add the product with the rounding's rest, see
-// kExact) and written back over the scores they came from, where the next product
-// takes them as its tensor-memory operand; the transposes that dV and dK need cost nothing, because
-// the second kernel computes S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
+// kExact) and written back over the scores they came from, where the next product takes them as
+// its tensor-memory operand; the transposes that dV and dK need cost nothing, because the second
+// kernel computes S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
 // Head dimension 128: 128 x 128 scores at a time, 16 warps, one block on an SM. Per 128 x 128
 // scores the products take 1536 cycles (dQ) and 2048 (dK, dV) at the full rate; measured 2100 and
 // 3000, the tensor core active 64 and 68 % of the time. An M = 128 product whose operands both come
 // from shared memory runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles; the
 // rest is the chain product - exponential - product of a block.
 // Head dimension 64, large grids: 128 x 64 scores at a time, 8 warps, two blocks on an SM, whose
-// chains, starts and ends (about 8000 cycles of a block) overlap. With 128 x 128 scores and one block, sequences
-// of 1 to 2311 tokens, 12 heads, took 139 us instead of 109. The exponentials alone, taken in both
-// kernels, are 1024 cycles per 128 x 128 scores of each, the products 1280 and 1536 (S and dP at
-// half of the rate with 64 columns).
+// chains, starts and ends (about 8000 cycles of a block) overlap. With 128 x 128 scores and one
+// block, sequences of 1 to 2311 tokens, 12 heads, took 139 us instead of 110. The exponentials
+// alone, taken in both kernels, are 1024 cycles per 128 x 128 scores of each, the products 1280
+// and 1536 (S and dP at half of the rate with 64 columns).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
