@@ -365,9 +365,10 @@ MUON_API muon_status_t muon_weight_grad(const muon_weight_grad_t* a, void* works
  * token and head strides (in elements) multiples of 8. Views of one buffer (packed q, k,
  * v) may interleave. lse is heads x q_tokens F32, contiguous. head_dim is a multiple of 8
  * up to 128; P and dS are rounded to BF16 for the products, all sums are FP32.
- * Offsets are n_seq + 1 int32 in device memory (NULL: one sequence of all tokens); each is
- * read as clamped to [0, tokens], and a sequence whose end lies before its start is empty.
- * Offsets must not decrease. A NaN or infinity of a sequence stays within it. */
+ * Offsets are n_seq + 1 int32 in device memory; with n_seq == 1 either pointer may be NULL,
+ * which stands for all rows (q_offsets) or all keys (k_offsets), with more neither may
+ * (MUON_ERR_INVALID_ARG). Each offset is read as clamped to [0, tokens], and a sequence whose
+ * end lies before its start is empty. Offsets must not decrease. A NaN or infinity of a sequence stays within it. */
 typedef struct {
   void* ptr;
   int64_t ld;          /* stride between tokens */

@@ -38,9 +38,12 @@ __device__ __forceinline__ int32_t clamp_offset(const int32_t* off, int i, int32
 __device__ __forceinline__ SeqRange seq_range(const muon_attention_t& a, int s) {
   const int32_t qt = static_cast<int32_t>(a.q_tokens), kt = static_cast<int32_t>(a.k_tokens);
   SeqRange r{0, qt, 0, kt};
+  // (a single sequence may have either of the two)
   if (a.q_offsets != nullptr) {
     r.q0 = clamp_offset(a.q_offsets, s, qt);
     r.m = clamp_offset(a.q_offsets, s + 1, qt) - r.q0;
+  }
+  if (a.k_offsets != nullptr) {
     r.k0 = clamp_offset(a.k_offsets, s, kt);
     r.n = clamp_offset(a.k_offsets, s + 1, kt) - r.k0;
   }

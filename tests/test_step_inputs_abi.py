@@ -123,6 +123,18 @@ def test_attention_refusals(lib, kw, status):
     assert lib.muon_attention_forward(None, None) == 1
 
 
+@pytest.mark.parametrize("n_seq", [1, 2, 3])
+def test_attention_offsets_on_one_side(lib, n_seq):
+    """A single sequence may have offsets of its rows or of its keys alone, or none; several need
+    both. The workspace size is 0 for a refused call and launches nothing."""
+    for q_off, k_off in ((None, FAKE + 11 * GB), (FAKE + 10 * GB, None), (None, None)):
+        a = attention(n_seq=n_seq, q_offsets=q_off, k_offsets=k_off)
+        assert (lib.muon_attention_workspace_size(ctypes.byref(a)) > 0) == (n_seq == 1)
+        if n_seq > 1:
+            assert lib.muon_attention_forward(ctypes.byref(a), None) == 1
+            assert lib.muon_attention_backward(ctypes.byref(a), FAKE + 12 * GB, GB, None) == 1
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(dout=B.MuonHeads(None, 256, 64)), 1), (dict(dq=B.MuonHeads(FAKE + 5 * GB, 264, 62)), 2),
     (dict(dq=B.MuonHeads(FAKE, 256, 64)), 4), (dict(dk=B.MuonHeads(FAKE + 7 * GB + 128, 128, 64)), 4),

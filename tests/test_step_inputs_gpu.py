@@ -433,6 +433,37 @@ def test_attention_one_sequence_without_offsets(B):
         ref.check(t, want[n], tol[n], n)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("rows,keys", [((13, 150), None), (None, (20, 161)), ((13, 13), None), (None, (7, 7))])
+def test_attention_one_sequence_with_offsets_on_one_side(B, lib, rows, keys, causal, d):
+    """Through the C call: with offsets of the rows alone the sequence has all keys, with those of
+    the keys alone all rows; what lies outside is not written."""
+    import ctypes
+    q, k, v, do = inputs(18, [170], [190], 4, 2, d)
+    (a, b), (c, e) = rows or (0, 170), keys or (0, 190)
+    o, lse = torch.full_like(q, 4.0), torch.full((4, 170), 4.0, device="cuda")
+    grads = [torch.full_like(t, 4.0) for t in (q, k, v)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan = B.AttentionPlan(q, k, v, o, lse, causal=causal, grads=(do, *grads), status=status)
+    off = ints([a, b] if rows else [c, e])
+    if rows:
+        plan._a.q_offsets = off.data_ptr()
+    else:
+        plan._a.k_offsets = off.data_ptr()
+    ws, stream = plan.workspace, torch.cuda.current_stream().cuda_stream
+    assert lib.muon_attention_forward(ctypes.byref(plan._a), stream) == 0
+    assert lib.muon_attention_backward(ctypes.byref(plan._a), ws.data_ptr(), ws.numel(), stream) == 0
+    want, tol = ref.attention(q[a:b], k[c:e], v[c:e], [b - a], [e - c], causal, d ** -0.5, do[a:b], o[a:b], lse[:, a:b])
+    ref.check(o[a:b], want["o"], tol["o"], "o")
+    ref.check(lse[:, a:b], want["lse"], tol["lse"], "lse")
+    for n, t, (lo, hi) in zip(("dq", "dk", "dv"), grads, ((a, b), (c, e), (c, e))):
+        ref.check(t[lo:hi], want[n], tol[n], n)
+    for t, (lo, hi) in zip([o, lse.t(), *grads], ((a, b), (a, b), (a, b), (c, e), (c, e))):
+        assert bool((t[:lo] == 4).all()) and bool((t[hi:] == 4).all())
+    assert int(status) == 0
+
+
 def test_attention_rows_outside_every_sequence_stay(B):
     """Rows before the first and behind the last sequence are neither read nor written, and a
     sequence of NaN leaves its neighbours alone."""
