@@ -486,9 +486,10 @@ def _act8_array(xs, cks):
         rows, cols = x.shape
         if rows != c.rows or cols != c.cols:
             raise MuonError(2, "activation and checkpoint shapes differ")
-        a, ld = arr[i], x.stride(0)
+        a = arr[i]
         a.X, a.q, a.exps, a.ld_q, a.ld_e = x.data_ptr(), c._q_ptr, c._e_ptr, *c.ld
-        a.rows, a.cols, a.ld_x, a.dtype = rows, cols, ld if ld > cols else cols, _dtype_code(x)
+        # (a single row may carry any stride; rows that overlap are refused by the call)
+        a.rows, a.cols, a.ld_x, a.dtype = rows, cols, x.stride(0) if rows > 1 else cols, _dtype_code(x)
     return arr
 
 

@@ -63,6 +63,49 @@ def test_act8_read_buffers_may_be_shared(lib):
         assert lib.muon_act8_store(inside, n, None) == 4
 
 
+class Strided:
+    """What the binding looks at of a 2-D CUDA tensor (this machine may have none)."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, rows, cols, ld, dtype, ptr=FAKE):
+        self.shape, self.strides, self.dtype, self.ptr = (rows, cols), (ld, 1), dtype, ptr
+
+    def dim(self):
+        return 2
+
+    def size(self, i):
+        return self.shape[i]
+
+    def stride(self, i):
+        return self.strides[i]
+
+    def data_ptr(self):
+        return self.ptr
+
+
+@pytest.mark.parametrize("ld,status", [(0, 2), (16, 2), (63, 2), (64, None), (80, None)])
+def test_act8_rows_that_overlap_are_refused(lib, ld, status):
+    """A broadcast row (stride 0) or overlapping windows reach the C call with the stride that they
+    have, which refuses them; taken as dense they would be read and written past their end."""
+    import torch
+    ck = B.Act8(Strided(8, 64, 64, torch.int8, FAKE + GB), Strided(8, 16, 16, torch.uint8, FAKE + 2 * GB), 64)
+    for dtype in (torch.float32, torch.bfloat16):
+        arr = B._act8_array([Strided(8, 64, ld, dtype)], [ck])
+        assert arr[0].ld_x == ld
+        for f in (lib.muon_act8_store, lib.muon_act8_restore):
+            got = f(arr, 1, None)
+            assert got == status if status else got not in (1, 2, 3, 4)
+
+
+@pytest.mark.parametrize("rows", [0, 1])
+@pytest.mark.parametrize("ld", [0, 1, 64, 90])
+def test_act8_a_single_row_may_have_any_stride(lib, rows, ld):
+    import torch
+    ck = B.Act8(Strided(rows, 64, ld, torch.int8, FAKE + GB), Strided(rows, 16, ld, torch.uint8, FAKE + 2 * GB), 64)
+    arr = B._act8_array([Strided(rows, 64, ld, torch.float32)], [ck])
+    assert lib.muon_act8_store(arr, 1, None) not in (1, 2, 3, 4)
+
+
 def wgrad(**kw):
     a = dict(dY=FAKE, q=FAKE + GB, exps=FAKE + 2 * GB, dW=FAKE + 3 * GB, offsets=FAKE + 4 * GB, status_dev=None,
              tokens=100, out=50, in_=70, ld_dy=56, ld_q=80, ld_e=16, ld_w=70, stride_w=3500, groups=3, w_dtype=1,

@@ -116,6 +116,24 @@ def test_store_takes_lists_in_several_launches(B):
     B.act8_restore([], [])
 
 
+def test_rows_that_overlap_are_refused(B):
+    """A broadcast row and overlapping windows, as source and as target; nothing is launched."""
+    row = torch.ones(64, device="cuda")
+    ck = B.new_act8(8, 64)
+    before = ck.q.clone()
+    for x in (row.expand(8, 64), torch.ones(200, device="cuda").as_strided((8, 64), (16, 1))):
+        for call in (lambda: B.act8_store([x], [ck]), lambda: B.act8_restore([ck], [x])):
+            with pytest.raises(B.MuonError) as e:
+                call()
+            assert e.value.status == 2
+    torch.cuda.synchronize()
+    assert torch.equal(ck.q, before) and bool((row == 1).all())
+    one = torch.ones(8, 200, device="cuda").t()[:1]             # a single row, of stride 1
+    B.act8_store([row[None, :8].expand(1, 8)], [B.new_act8(1, 8)])
+    with pytest.raises(B.MuonError):
+        B.act8_store([one], [B.new_act8(1, 8)])                 # its columns are 200 apart
+
+
 # ---------------------------------------------------------------- weight gradients
 def stored(B, gen, tokens, inn, scale=1.0):
     ck = B.new_act8(tokens, inn)
