@@ -195,6 +195,12 @@ def _check_2d(t, name: str):
         raise MuonError(1, f"{name} must be a CUDA tensor")
 
 
+def _ld(t) -> int:
+    """The leading dimension of a 2-D tensor. A single row may carry any stride; rows that overlap
+    keep the stride that the calls refuse."""
+    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+
+
 def matrix_array(params, grads, momenta):
     """The muon_matrix_t array for lists of W (fp32), G (fp32/bf16), M (fp32) tensors."""
     n = len(params)
@@ -207,8 +213,7 @@ def matrix_array(params, grads, momenta):
         if tuple(g.shape) != tuple(w.shape) or tuple(m.shape) != tuple(w.shape):
             raise MuonError(2, "W, grad and momentum shapes differ")
         arr[i] = MuonMatrix(w.data_ptr(), g.data_ptr(), m.data_ptr(), w.size(0), w.size(1),
-                            max(w.stride(0), w.size(1)), max(g.stride(0), g.size(1)),
-                            max(m.stride(0), m.size(1)), _dtype_code(w), _dtype_code(g))
+                            _ld(w), _ld(g), _ld(m), _dtype_code(w), _dtype_code(g))
     return arr
 
 
@@ -360,19 +365,21 @@ class Plan:
             pass
 
 
+def _ns_matrix(x, o) -> MuonNSMatrix:
+    _check_2d(x, "X")
+    _check_2d(o, "O")
+    if x.dtype != o.dtype or tuple(x.shape) != tuple(o.shape):
+        raise MuonError(3, "X and O must have the same dtype and shape")
+    return MuonNSMatrix(x.data_ptr(), o.data_ptr(), x.size(0), x.size(1), _ld(x), _ld(o), _dtype_code(x), 0)
+
+
 def newton_schulz(xs, outs, hp: MuonHParams, workspace=None, stream=None):
     """O_i = NS(X_i / (||X_i||_F + eps)) for lists of 2-D CUDA tensors (fp32 or bf16)."""
     lib = load()
     n = len(xs)
     arr = (MuonNSMatrix * n)()
     for i, (x, o) in enumerate(zip(xs, outs)):
-        _check_2d(x, "X")
-        _check_2d(o, "O")
-        if x.dtype != o.dtype or tuple(x.shape) != tuple(o.shape):
-            raise MuonError(3, "X and O must have the same dtype and shape")
-        arr[i] = MuonNSMatrix(x.data_ptr(), o.data_ptr(), x.size(0), x.size(1),
-                              max(x.stride(0), x.size(1)), max(o.stride(0), o.size(1)),
-                              _dtype_code(x), 0)
+        arr[i] = _ns_matrix(x, o)
     if workspace is None:
         size = lib.muon_ns_workspace_size(arr, n, ctypes.byref(hp))
         workspace = new_workspace(size, xs[0].device if n else "cuda")
@@ -389,16 +396,11 @@ def newton_schulz_noalloc(x, o, hp: MuonHParams, status=None, stream=None):
     status: optional CUDA int32/uint32 one-element tensor for the device error word."""
     lib = load()
     status_ptr = _status_ptr(status)
-    _check_2d(x, "X")
-    _check_2d(o, "O")
-    if x.dtype != o.dtype or tuple(x.shape) != tuple(o.shape):
-        raise MuonError(3, "X and O must have the same dtype and shape")
+    m = _ns_matrix(x, o)
     if o.device != x.device:
         raise MuonError(1, "X and O must be on the same device")
     if status is not None and status.device != x.device:
         raise MuonError(1, "status must be on the device of X")
-    m = MuonNSMatrix(x.data_ptr(), o.data_ptr(), x.size(0), x.size(1), max(x.stride(0), x.size(1)),
-                     max(o.stride(0), o.size(1)), _dtype_code(x), 0)
     with _on(x.device):
         _check(lib.muon_newton_schulz_noalloc(ctypes.byref(m), ctypes.byref(hp), status_ptr,
                                               _stream_ptr(stream)), "muon_newton_schulz_noalloc")
@@ -420,7 +422,7 @@ class QkClipPlan:
                 raise MuonError(3, "QK-Clip weights must be float32")
             if w.device != s_max.device:
                 raise MuonError(1, "QK-Clip weights and s_max must be on the same GPU")
-            arr[i] = MuonQkSlice(w.data_ptr(), r0, nr, w.size(1), max(w.stride(0), w.size(1)), h, pw)
+            arr[i] = MuonQkSlice(w.data_ptr(), r0, nr, w.size(1), _ld(w), h, pw)
         if s_max.dtype != _torch().float32 or not s_max.is_cuda:
             raise MuonError(1, "s_max must be a CUDA float32 tensor")
         self._arr, self._n, self.s_max, self.tau = arr, len(slices), s_max, float(tau)

@@ -212,3 +212,54 @@ def test_qk_clip_plan_rejects_bad_inputs_before_any_launch(lib):
     for slices in bad:
         with pytest.raises(B.MuonError):
             B.QkClipPlan(slices, s_dev)
+
+
+class Strided:
+    """What the binding looks at of a 2-D CUDA tensor (this machine may have none)."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, rows, cols, ld, ptr, dtype=None):
+        import torch
+        self.shape, self.strides, self.ptr = (rows, cols), (ld, 1), ptr
+        self.dtype = dtype or torch.float32
+
+    def dim(self):
+        return 2
+
+    def size(self, i):
+        return self.shape[i]
+
+    def stride(self, i):
+        return self.strides[i]
+
+    def data_ptr(self):
+        return self.ptr
+
+    def numel(self):
+        return self.shape[0] * self.shape[1]
+
+
+@pytest.mark.parametrize("rows,ld,good", [(8, 0, False), (8, 16, False), (8, 63, False), (8, 64, True), (8, 100, True),
+                                          (1, 0, True), (1, 1, True), (1, 100, True)])
+def test_matrices_whose_rows_overlap_are_refused(lib, rows, ld, good):
+    """A broadcast row or overlapping windows reach the calls with the stride that they have, which
+    refuse them; taken as dense they would be read and written past their end."""
+    hp = B.hparams()
+
+    def mat(i, stride=64):
+        return Strided(rows, 64, stride, FAKE + i * (1 << 30))
+    for bad in range(3):
+        w, g, m = (mat(i, ld if i == bad else 64) for i in range(3))
+        arr = B.matrix_array([w], [g], [m])
+        assert lib.muon_validate(arr, 1, ctypes.byref(hp)) == (0 if good else 2)
+    for x, o in ((mat(0, ld), mat(1)), (mat(0), mat(1, ld))):
+        one = B._ns_matrix(x, o)
+        assert (lib.muon_ns_workspace_size(ctypes.byref(one), 1, ctypes.byref(hp)) > 0) == good
+        if not good:
+            assert lib.muon_newton_schulz_noalloc(ctypes.byref(one), ctypes.byref(hp), None, None) == 2
+    s_max = Strided(1, 4, 4, FAKE + (9 << 30))
+    plan = B.QkClipPlan([(mat(0, ld), 0, rows, 0, 0.5)], s_max)
+    if not good:
+        assert lib.muon_qk_clip(plan._arr, 1, s_max.data_ptr(), 4, 100.0, None) == 2
+    else:
+        assert plan._arr[0].ld >= 64
