@@ -90,8 +90,10 @@ struct FwdParams {
 };
 
 // Raises *p to v: positive floats order as integers, negative ones in reverse as unsigned.
-// The result does not depend on the order of the calls; NaN changes nothing.
+// The result does not depend on the order of the calls; NaN changes nothing. (-0 is taken as +0:
+// as an integer it would be below everything.)
 __device__ __forceinline__ void atomic_max_float(float* p, float v) {
+  v += 0.f;
   if (v >= 0.f) atomicMax(reinterpret_cast<int*>(p), __float_as_int(v));
   else if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
 }

@@ -529,6 +529,19 @@ def test_attention_s_max_is_raised_only(B):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_attention_s_max_of_minus_zero(B, d):
+    """A largest logit that underflows to -0 raises s_max from -inf and from below zero to zero, and
+    no further: q.k = -2^-100 exactly, times a scale of 2^-100."""
+    q, k, v, _ = inputs(19, [40], [40], 3, 1, d)
+    q.zero_()
+    k.zero_()
+    q[..., 0], k[..., 0] = 2.0 ** -50, -(2.0 ** -50)
+    s_max = torch.tensor([-math.inf, -1.0, 1e-30], device="cuda")
+    B.attention_forward(q, k, v, scale=2.0 ** -100, s_max=s_max)
+    assert torch.equal(s_max, torch.tensor([0.0, 0.0, 1e-30], device="cuda"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_attention_keys_masked_by_infinite_entries(B, d):
     """Keys whose entries make every logit -inf (with queries of one sign) count for nothing, also
     where they fill the first blocks and what follows has low logits; a row that sees no other key
