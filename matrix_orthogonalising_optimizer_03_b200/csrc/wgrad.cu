@@ -574,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
 #pragma unroll 1
       for (int c = 0; c < N / 64; ++c) {
         uint32_t v[32];
+        __syncwarp();  // lanes past the last column skip the stores: the load takes the warp whole
         if (j.nkb > 0) {
           tmem_ld32(tmem + (static_cast<uint32_t>(w * 32) << 16) + static_cast<uint32_t>(acc * N + half + c * 32), v);
           tmem_wait_ld();

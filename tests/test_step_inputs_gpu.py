@@ -300,6 +300,39 @@ def test_weight_grad_dense_of_each_tile_height_is_exact(B):
         assert torch.equal(dw, dy.float().t() @ (ck.q[:, :inn].float() * 0.5))     # exact in fp32 too
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("out,inn,counts", [
+    (384, 1, [130]), (384, 2563, [130, 0, 65]), (256, 12289, [70]), (768, 2309, [200]), (100, 9001, [64, 3]),
+    (320, 37, [90] * 70)])
+def test_weight_grad_of_columns_that_end_inside_a_warp_is_exact(B, out, inn, counts, dtype):
+    """Lanes past the last column leave the stores early in every chunk of rows. Whole numbers up to
+    2 * 3 * 200 * 2 in fp32, with values that bf16 holds (at most 2^8) else; every tile height."""
+    g = gen_of(inn)
+    t = sum(counts)
+    ck = B.new_act8(t, inn)
+    ck.exps.fill_(127)
+    dy = dy_of(g, t, out)
+    if dtype == F32:
+        ck.q[:, :inn].copy_(torch.randint(-3, 4, (t, inn), generator=g, device="cuda"))
+        dy.copy_(torch.randint(-2, 3, (t, out), generator=g, device="cuda"))
+    else:                                       # one token in eight counts: sums of at most 26 ones
+        ck.q[:, :inn].copy_(torch.randint(-1, 2, (t, inn), generator=g, device="cuda"))
+        dy[::8] = torch.randint(-1, 2, (len(range(0, t, 8)), out), generator=g, device="cuda").to(BF16)
+        dy[torch.arange(t, device="cuda") % 8 != 0] = 0
+    off = offsets_of(counts)
+    want, _ = ref.weight_grad(dy, ck.q[:, :inn], off)
+    buf = torch.full((len(counts), out, inn + 3), 7.0, device="cuda", dtype=dtype)
+    dw = buf[..., :inn]
+    plan = B.WeightGradPlan(dy, ck, dw, offsets=ints(off))
+    more = B.WeightGradPlan(dy, ck, dw, offsets=ints(off), accumulate=True)
+    for _ in range(5):
+        plan.apply()
+        assert torch.equal(dw.double(), want)
+        more.apply()
+        assert torch.equal(dw.double(), 2 * want)
+    assert bool((buf[..., inn:] == 7).all())
+
+
 # ---------------------------------------------------------------- attention
 def inputs(seed, q_len, k_len, h, g, d, pad=0, sharp=1.0):
     """q, k, v, dout as views of wider buffers."""
