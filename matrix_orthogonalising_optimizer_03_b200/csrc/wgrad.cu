@@ -558,7 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad_kernel(const __grid_constan
       if (j.nkb == 0 && (j.part >= 0 || a.accumulate)) continue;
       const int acc = it % C::kAcc;
       if (j.nkb > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], static_cast<uint32_t>((it / C::kAcc) & 1), abort_flag))) {
+        // Every other wait is for one k-block or one epilogue, this one for a tile: its limit grows
+        // with the k-blocks (470 to 950 cycles each; a tile of 4.3 million outlasts the fixed part).
+        const long long limit = kWaitLimitCycles + 4096LL * j.nkb;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&tfull[acc], static_cast<uint32_t>((it / C::kAcc) & 1), abort_flag, limit))) {
           ok = false;
           if (lane == 0) {
             set_error(a.status_dev, MUON_ERR_TIMEOUT);

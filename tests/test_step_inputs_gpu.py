@@ -333,6 +333,26 @@ def test_weight_grad_of_columns_that_end_inside_a_warp_is_exact(B, out, inn, cou
     assert bool((buf[..., inn:] == 7).all())
 
 
+def test_weight_grad_of_a_group_that_takes_longer_than_a_wait(B):
+    """One of 74 small groups has all of 400 million tokens: its tile takes one CTA pair more than a
+    second, longer than the limit of a single wait. All dY but a few tokens' are zero."""
+    tokens, groups = 400_000_000, 74
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 20 GB")
+    ck = B.Act8(torch.ones(tokens, 16, dtype=torch.int8, device="cuda"),
+                torch.full((tokens, 16), 127, dtype=torch.uint8, device="cuda"), 16)
+    dy = torch.zeros(tokens, 8, dtype=BF16, device="cuda")
+    dy[[0, 100_000_000, tokens - 2]] = 3.0
+    dw = torch.full((groups, 8, 16), 5.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    off = ints([0] + [tokens - 1] * (groups - 1) + [tokens])
+    dy[tokens - 1] = 1.0                                        # the last group's
+    B.weight_grad(dy, ck, dw, offsets=off, status=status)
+    assert int(status) == 0
+    assert bool((dw[0] == 9).all()) and bool((dw[1:-1] == 0).all()) and bool((dw[-1] == 1).all())
+
+
 # ---------------------------------------------------------------- attention
 def inputs(seed, q_len, k_len, h, g, d, pad=0, sharp=1.0):
     """q, k, v, dout as views of wider buffers."""
