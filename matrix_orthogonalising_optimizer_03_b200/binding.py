@@ -297,6 +297,17 @@ def new_workspace(nbytes: int, device="cuda"):
     return ws
 
 
+def _check_workspace(workspace, device):
+    """A workspace that the caller brings: contiguous memory of the GPU that the call runs on. (Its
+    size and alignment are checked by the call.)"""
+    if workspace is None:
+        return
+    if not workspace.is_cuda or (device is not None and workspace.device != device):
+        raise MuonError(5, "the workspace must be a CUDA tensor on the device of the tensors")
+    if not workspace.is_contiguous():
+        raise MuonError(5, "the workspace must be contiguous")
+
+
 def workspace_size(params, grads, momenta, hp: MuonHParams) -> int:
     arr = matrix_array(params, grads, momenta)
     return int(load().muon_workspace_size(arr, len(arr), ctypes.byref(hp)))
@@ -306,6 +317,7 @@ def step_batched(params, grads, momenta, hp: MuonHParams, workspace=None, stats=
                  stream=None):
     """One Muon step over the lists (muon_step_batched). Returns the workspace used."""
     lib = load()
+    _check_workspace(workspace, _device_of(params))
     arr = matrix_array(params, grads, momenta)
     n = len(arr)
     if workspace is None:
@@ -325,6 +337,7 @@ class Plan:
 
     def __init__(self, params, grads, momenta, hp: MuonHParams, workspace=None):
         self._lib = load()
+        _check_workspace(workspace, _device_of(params))
         self._arr = matrix_array(params, grads, momenta)
         self._keep = (list(params), list(grads), list(momenta))
         self.n = len(self._arr)
@@ -376,6 +389,7 @@ def _ns_matrix(x, o) -> MuonNSMatrix:
 def newton_schulz(xs, outs, hp: MuonHParams, workspace=None, stream=None):
     """O_i = NS(X_i / (||X_i||_F + eps)) for lists of 2-D CUDA tensors (fp32 or bf16)."""
     lib = load()
+    _check_workspace(workspace, _device_of(xs))
     n = len(xs)
     arr = (MuonNSMatrix * n)()
     for i, (x, o) in enumerate(zip(xs, outs)):
@@ -552,6 +566,7 @@ class WeightGradPlan:
             raise MuonError(2, "dW must be out x in, or groups x out x in with offsets")
         if not dw.is_cuda or dy.device != dw.device or ck.device != dw.device:
             raise MuonError(1, "dY, the checkpoint and dW must be CUDA tensors on the same device")
+        _check_workspace(workspace, dw.device)
         groups, out, inn = dw3.shape
         if groups < 1 or (offsets is not None and offsets.numel() != groups + 1):
             raise MuonError(2, "offsets must have groups + 1 elements")
@@ -640,6 +655,7 @@ class AttentionPlan:
         if s_max is not None and (s_max.dtype != torch.float32 or tuple(s_max.shape) != (h,) or
                                   not s_max.is_contiguous() or s_max.device != dev):
             raise MuonError(2, f"s_max must be a contiguous fp32 tensor of {h} on the device of q")
+        _check_workspace(workspace, dev)
         if (q_offsets is None) != (k_offsets is None):
             raise MuonError(1, "q_offsets and k_offsets are given together")
         if q_offsets is not None and q_offsets.numel() != k_offsets.numel():

@@ -220,6 +220,60 @@ def test_interleaved_views_are_not_aliases(lib):
     assert size(a) == 0
 
 
+class Fake:
+    """A contiguous CUDA tensor as the binding looks at it."""
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, shape, dtype, i=0, device="cuda:0", dense=True):
+        self.shape, self.dtype, self.i, self.device, self.dense = tuple(shape), dtype, i, device, dense
+        self.is_cuda = device != "cpu"
+
+    def dim(self):
+        return len(self.shape)
+
+    def size(self, i):
+        return self.shape[i]
+
+    def stride(self, i):
+        n = 1
+        for x in self.shape[i + 1:]:
+            n *= x
+        return n
+
+    def numel(self):
+        return self.stride(0) * self.shape[0]
+
+    def unsqueeze(self, _):
+        return Fake((1, *self.shape), self.dtype, self.i)
+
+    def is_contiguous(self):
+        return self.dense
+
+    def data_ptr(self):
+        return FAKE + self.i * GB
+
+
+def test_workspaces_of_another_device_are_refused(lib):
+    """A workspace on the CPU, on another GPU or with gaps raises before the call marshals it."""
+    import torch
+    hp, u8, bf = B.hparams(), torch.uint8, torch.bfloat16
+    w, g, m = (Fake((64, 64), torch.float32, i) for i in range(3))
+    ck = B.Act8(Fake((100, 64), torch.int8, 3), Fake((100, 16), u8, 4), 64)
+    dy, dw = Fake((100, 64), bf, 5), Fake((64, 64), torch.float32, 6)
+    x = [Fake((100, 2, 64), bf, 7 + i) for i in range(8)]
+    lse = Fake((2, 100), torch.float32, 20)
+    for ws in (Fake((1 << 28,), u8, 30, "cpu"), Fake((1 << 28,), u8, 30, "cuda:1"), Fake((1 << 28,), u8, 30, dense=False)):
+        for call in (lambda: B.step_batched([w], [g], [m], hp, workspace=ws), lambda: B.Plan([w], [g], [m], hp, workspace=ws),
+                     lambda: B.newton_schulz([w], [g], hp, workspace=ws),
+                     lambda: B.WeightGradPlan(dy, ck, dw, workspace=ws),
+                     lambda: B.AttentionPlan(*x[:4], lse, grads=x[4:], workspace=ws)):
+            with pytest.raises(B.MuonError) as e:
+                call()
+            assert e.value.status == 5
+    good = Fake((1 << 28,), u8, 30)
+    assert B.AttentionPlan(*x[:4], lse, grads=x[4:], workspace=good).workspace is good
+
+
 def test_sizes_match_c_compiler(tmp_path):
     import os
     import subprocess
