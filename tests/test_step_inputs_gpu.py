@@ -725,6 +725,58 @@ def test_offsets_past_32_bits(B):
     assert torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("tokens,heads,kv_heads,d,ld,head", [
+    (200, 2, 2, 64, 64, (1 << 32) + 64),        # heads outermost
+    (20000, 2, 2, 64, 64, (1 << 32) + 64),      # blocks of 64 columns
+    (200, 4, 2, 128, 128, (1 << 32) + 64),      # clusters share the query heads
+    (260, 2, 1, 64, (1 << 24) + 8, 64), (260, 2, 2, 128, (1 << 24) + 8, 128)])
+def test_written_tensors_past_32_bits(B, tokens, heads, kv_heads, d, ld, head):
+    """All tensors of both passes as interleaved views of one buffer, with strides whose offsets pass
+    2^32 elements: the bits of contiguous ones, and nothing written beside them."""
+    plane = tokens * d if ld < head else 2 * d                  # one tensor's share of the outer stride
+    outer = max((tokens - 1) * ld, (heads - 1) * head)
+    buf = torch.empty(outer + 8 * plane + tokens * d + 8, device="cuda", dtype=BF16)
+    names = ("q", "k", "v", "dout", "o", "dq", "dk", "dv")
+    big = {n: buf.as_strided((tokens, kv_heads if n in ("k", "v", "dk", "dv") else heads, d), (ld, head, 1), i * plane)
+           for i, n in enumerate(names)}
+    g = gen_of(tokens + d)
+    for n in names:
+        big[n].copy_(randn(g, *big[n].shape))
+    small = {n: t.clone(memory_format=torch.contiguous_format) for n, t in big.items()}
+    edge = buf.as_strided((heads, 8), (head, 1), 8 * plane) if ld < head else buf.as_strided((tokens, 8), (ld, 1), 8 * plane)
+    edge.fill_(7.0)
+    lses = []
+    for t in (big, small):
+        lse = torch.zeros(heads, tokens, device="cuda")
+        plan = B.AttentionPlan(t["q"], t["k"], t["v"], t["o"], lse, grads=(t["dout"], t["dq"], t["dk"], t["dv"]))
+        plan.forward()
+        plan.backward()
+        lses.append(lse)
+    assert torch.equal(*lses) and bool((edge == 7).all())
+    for n in names:
+        assert torch.equal(big[n], small[n]), n
+
+
+@pytest.mark.parametrize("tokens", [100, 16384])
+def test_weight_gradient_rows_and_groups_past_32_bits(B, tokens):
+    """dW with rows 2^31 elements apart (whole tiles, and parts that are joined), and with groups
+    2^32 apart."""
+    g = gen_of(22)
+    buf = torch.empty(3 * ((1 << 31) - 8) + 64, device="cuda", dtype=BF16)      # 12.9 GB
+    ck, _ = stored(B, g, tokens, 40)
+    dy = dy_of(g, tokens, 4)
+    rows = buf.as_strided((4, 40), ((1 << 31) - 8, 1))
+    groups = buf.as_strided((2, 4, 40), ((1 << 32) + 3, 40, 1), 64)
+    off = ints([0, tokens // 3, tokens])
+    for big, kw in ((rows, {}), (groups, dict(offsets=off))):
+        small = torch.zeros(big.shape, device="cuda", dtype=BF16)
+        big.zero_()
+        for accumulate in (False, True):
+            B.weight_grad(dy, ck, big, accumulate=accumulate, **kw)
+            B.weight_grad(dy, ck, small, accumulate=accumulate, **kw)
+        assert torch.equal(big, small) and bool((small != 0).any())
+
+
 # ---------------------------------------------------------------- together
 def test_a_training_step_from_checkpoints_to_clipped_weights(B):
     """Attention over projections of a small model: the forward pass stores its activations in
@@ -810,3 +862,49 @@ def test_captured_step_on_another_stream_follows_its_buffers(B):
     assert all(torch.equal(a, b) for a, b in zip(got, (o, lse, *grads, dw, ck.q)))
     want, tol = ref.attention(q, k, v, [131, 69], [131, 69], True, 0.125, do, o, lse)
     ref.check(o, want["o"], tol["o"], "o")
+
+
+def test_captured_calls_that_split_their_sums(B):
+    """A weight gradient split along the tokens (its second kernel is launched early), written and
+    accumulated, and a backward pass whose clusters share the query heads, captured on a side stream:
+    replays follow the buffers and equal eager calls bit for bit."""
+    g = gen_of(23)
+    tokens = 6000
+    ck, _ = stored(B, g, tokens, 96)
+    dy = dy_of(g, tokens, 64)
+    off = ints([0, 5000, tokens])
+    dws = [torch.zeros(64, 96, device="cuda"), torch.zeros(2, 64, 96, device="cuda", dtype=BF16)]
+    plans = [B.WeightGradPlan(dy, ck, dws[0], accumulate=True), B.WeightGradPlan(dy, ck, dws[1], offsets=off)]
+    assert all(p.workspace is not None for p in plans)          # split
+    q, k, v, do = inputs(24, [500], [500], 8, 2, 128)
+    o, lse = torch.zeros_like(q), torch.zeros(8, 500, device="cuda")
+    grads = [torch.zeros_like(t) for t in (q, k, v)]
+    att = B.AttentionPlan(q, k, v, o, lse, grads=(do, *grads))
+
+    def step():
+        dws[0].zero_()
+        for p in (plans[0], plans[1], plans[0]):
+            p.apply()
+        att.forward()
+        att.backward()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in range(3):
+        for t in (dy, q, k, v, do):
+            t.copy_(randn(g, *t.shape))
+        off.copy_(ints([0, 1700 * seed, tokens]))
+        for t in (o, lse, *grads, *dws):
+            t.fill_(9.0)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (o, lse, *grads, *dws)]
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(got, (o, lse, *grads, *dws)))
