@@ -8,18 +8,19 @@
 // and dV, over all query heads of the key head. S and dout V^T are computed in both: seven
 // products instead of five, against fp32 atomics on dQ, whose order changes its sums.
 // A thread owns 32 elements of one lane's row. P and dS are rounded to bf16 (at most 2^-8 relative,
-// errors of either sign; sums of a single block also add the product with the rounding's rest, see
-// kExact) and written back over the scores they came from, where the next product takes them as
+// errors of either sign; where a block's whole sum is one product of blocks of 128 it also adds the
+// product with the rounding's rest, see kExact) and written back over the scores they came from, where the next product takes them as
 // its tensor-memory operand; the transposes that dV and dK need cost nothing, because the second
 // kernel computes S^T = K Q^T and (dout V^T)^T = V dout^T to begin with.
 // Head dimension 128: 128 x 128 scores at a time, 16 warps, one block on an SM. Per 128 x 128
-// scores the products take 1536 cycles (dQ) and 2048 (dK, dV) at the full rate; measured 2100 and
-// 3000, the tensor core active 64 and 68 % of the time. An M = 128 product whose operands both come
+// scores the products take 1536 cycles (dQ) and 2048 (dK, dV) at the full rate; measured 2420 and
+// 3440 over the whole kernels (8192 tokens, causal, 16 heads on 4: 311 and 434 us), the tensor core
+// active 66 and 63 % of the time. An M = 128 product whose operands both come
 // from shared memory runs at 0.84 of the rate for N = 128, as it reads 8 KB per 64 cycles; the
 // rest is the chain product - exponential - product of a block.
 // Head dimension 64, large grids: 128 x 64 scores at a time, 8 warps, two blocks on an SM, whose
 // chains, starts and ends (about 8000 cycles of a block) overlap. With 128 x 128 scores and one
-// block, sequences of 1 to 2311 tokens, 12 heads, took 139 us instead of 110. The exponentials
+// block, sequences of 1 to 2311 tokens, 12 heads, took 146 us instead of 112. The exponentials
 // alone, taken in both kernels, are 1024 cycles per 128 x 128 scores of each, the products 1280
 // and 1536 (S and dP at half of the rate with 64 columns).
 #include <cuda.h>
@@ -53,8 +54,10 @@ struct BwdCfg {
   // four warps that move and issue leave some to the others: 128 x 64 + 256 x 88 is the same total.
   static constexpr int kPerSm = W == 64 ? 2 : 1;
   static constexpr uint32_t kTmem = 512 / kPerSm;
-  // Sums of a single block also take the rest of the rounding of P and dS (store_operand). Two
-  // blocks an SM leave no registers for it (it spilled: 107 -> 119 us), and are many tiles.
+  // A thread block whose whole sum is one product (dQ: its rows see at most 128 keys; dK and dV: 128
+  // rows of one query head see its keys) also takes the rest of the rounding of P and dS
+  // (store_operand): errors of 0.0017 instead of 0.0024. Two blocks an SM leave no registers for it
+  // (it spilled: 107 -> 119 us): there a short sequence is off by as much as a long one.
   static constexpr bool kExact = kPerSm == 1;
   static constexpr int kTile = kRows * HD * 2;
   static constexpr int kBlock = kCols * HD * 2;
@@ -106,7 +109,7 @@ __device__ __forceinline__ void load_block(uint8_t* dst, const CUtensorMap* map,
 // that a product would sum over, with factors of zero but perhaps NaN themselves.
 template <int HD, int W>
 __device__ __forceinline__ void clear_rows(uint8_t* block, int live, int lane) {
-    for (int e = live * 8 + lane; e < W * 8; e += 32)
+  for (int e = live * 8 + lane; e < W * 8; e += 32)
 #pragma unroll
     for (int c = 0; c < HD / 64; ++c)
       *reinterpret_cast<uint4*>(block + c * (W * 128) + e * 16) = make_uint4(0, 0, 0, 0);
@@ -117,7 +120,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* block, int live, int lane) {
 // D = A B^T over the head dimension: a tile and a block in shared memory, both K-major.
 template <int HD, int W>
 __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, W, false);
+  constexpr uint32_t idesc = idesc_bf16_f32(128, W, false);
   const uint32_t ad = desc_lo(a_addr, 16), bd = desc_lo(b_addr, 16);
 #pragma unroll
   for (int k = 0; k < HD / 16; ++k) {
@@ -130,7 +133,7 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_addr, uint32_t
 // first 16 of the 32 columns they came from), B an MN-major block in shared memory.
 template <int HD, int W>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_addr, bool accumulate, bool exact) {
-    constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
+  constexpr uint32_t idesc = idesc_bf16_f32(128, HD, true);
   const uint32_t bd = desc_lo(b_addr, W * 128);
 #pragma unroll
   for (int k = 0; k < W / 16; ++k)
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, W>::kThreads, BwdCfg<HD, W>::kPerSm
 // every SM three blocks. Few key heads would otherwise leave SMs idle, and the long tiles of a
 // causal sequence make them wait; more blocks only repeat the loads of K and V and the joins.
 // The whole backward pass at 8192 tokens, causal, split against not: 4 query heads on 1 key head
-// 210 against 500 us, 16 on 4 753 against 769 us.
+// 218 against 504 us, 16 on 4 757 against 759 us (head dimension 96: 798 against 738).
 int dkv_split(const muon_attention_t& a, int64_t grid) {
   int split = 1;
   while (split < 4 && (a.heads / a.kv_heads) % (2 * split) == 0 && grid * split < 3 * 148) split *= 2;
@@ -747,9 +750,9 @@ int dkv_split(const muon_attention_t& a, int64_t grid) {
 }
 
 // Head dimension 64: blocks of 64 columns, two of them on an SM, where a grid gives every SM more
-// than two; else blocks of 128, whose chain is shorter per column. dQ / dK and dV of causal
-// sequences, 64 against 128 columns: 4096 tokens and 8 heads (264 blocks) 54 / 73 against 42 / 56 us,
-// 12 heads (396) 60 / 79 against 65 / 90, 24 heads (792) 106 / 138 against 120 / 162.
+// than two; else blocks of 128, whose chain is shorter per column. Both kernels of causal
+// sequences, 64 against 128 columns: 4096 tokens and 8 heads (264 blocks) 125 against 93 us, 12 heads
+// (396) 134 against 142, 24 heads (792) 229 against 257.
 bool narrow(int64_t grid) { return grid > 2 * 148; }
 
 template <class C>
