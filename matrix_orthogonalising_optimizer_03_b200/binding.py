@@ -625,8 +625,8 @@ class AttentionPlan:
 
     q, o: q_tokens x heads x head_dim; k, v: k_tokens x kv_heads x head_dim (bf16); lse:
     heads x q_tokens fp32. q_offsets / k_offsets: int32 CUDA tensors of n_seq + 1 token
-    offsets, read on the device by every call (None: one sequence; for self-attention pass
-    the same tensor twice). s_max: fp32 tensor of `heads` entries, the S_max of QK-Clip, to be
+    offsets, read on the device by every call, given together (None: one sequence; for
+    self-attention pass the same tensor twice). s_max: fp32 tensor of `heads` entries, the S_max of QK-Clip, to be
     filled with -inf before the first micro-batch. scale: 1 / sqrt(head_dim) by default.
     grads: (dout, dq, dk, dv), needed by backward(). The tensors must stay alive while the
     plan is used."""
@@ -695,8 +695,8 @@ class AttentionPlan:
 
 def attention_forward(q, k, v, o=None, lse=None, q_offsets=None, k_offsets=None, causal: bool = True,
                       scale: Optional[float] = None, s_max=None, status=None, stream=None):
-    """One forward pass (see `AttentionPlan`). Returns (o, lse); tensors that are not given
-    are allocated, with rows outside every sequence zero and -inf."""
+    """One forward pass (see `AttentionPlan`). Returns (o, lse), without an autograd graph;
+    tensors that are not given are allocated, with rows outside every sequence zero and -inf."""
     torch = _torch()
     with _on(q.device if q.is_cuda else None), _on_stream(stream):
         if o is None:

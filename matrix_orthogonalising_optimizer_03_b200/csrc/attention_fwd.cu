@@ -17,9 +17,9 @@
 // to bf16 for the product (at most 2^-8 relative, errors of either sign); the row's sum adds the
 // unrounded values.
 // Bounds, per 128 keys of both blocks: head dimension 128 by the products, 2048 cycles at the full
-// rate (S, with both operands in shared memory and 64 columns, runs at half of it; 3400 measured,
-// 1089 TFLOP/s at 8191 tokens, 12 heads); head dimension 64 by the exponentials, 16 per cycle and
-// SM, 2048 cycles (3100 measured: the sums, maxima and transfers of two softmax warps to a
+// rate (S, with both operands in shared memory and 64 columns, runs at half of it; 3300 measured
+// in a full round of blocks, 1040 to 1110 TFLOP/s at 8191 tokens, 12 heads); head dimension 64 by the exponentials, 16 per cycle and
+// SM, 2048 cycles (3160 measured: the sums, maxima and transfers of two softmax warps to a
 // scheduler do not all hide behind them; moving exponentials to the FMA pipe made it slower).
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -27,8 +27,8 @@
 // tiles go to the 74 CTA pairs in whole rounds, and those left over for the last round are split
 // along the tokens into as many parts as keep all pairs busy, whose fp32 partial sums a second
 // kernel adds in order (no atomics).
-// Bound by the products and their operands for long groups (128 us for 5632 x 2048 from 8192
-// tokens, 1475 TFLOP/s, at the full clock; 158 us under the power cap), by restoring X at 128
+// Bound by the products and their operands for long groups (130 us for 5632 x 2048 from 8192
+// tokens, 1450 TFLOP/s, at the full clock; 161 us under the power cap), by restoring X at 128
 // rows, and by start and epilogue for short groups.
 #include <cuda.h>
 #include <cuda_runtime.h>
